@@ -89,6 +89,18 @@ _SIGNATURES = {
     "ep_combine_backward": (ctypes.c_int, [ctypes.POINTER(ep_handle), ctypes.c_int32, _P, _P, _P, _P, _P, _P]),
     "ep_combine_weight_grad": (ctypes.c_int, [ctypes.POINTER(ep_handle), _P, _P, _P, _P]),
     "ep_grouped_gemm_fp8": (ctypes.c_int, [ctypes.POINTER(ep_handle), _P, _P, _P, _P, ctypes.c_int32, _P, _P]),
+    "ep_grouped_gemm_bf16": (ctypes.c_int, [ctypes.POINTER(ep_handle), _P, _P, ctypes.c_int32, ctypes.c_int32, _P, _P]),
+    "ep_grouped_gemm_bf16_grad_input": (ctypes.c_int, [ctypes.POINTER(ep_handle), _P, _P, ctypes.c_int32,
+                                                       ctypes.c_int32, _P, _P]),
+    "ep_grouped_gemm_bf16_grad_weight": (ctypes.c_int, [ctypes.POINTER(ep_handle), _P, _P, ctypes.c_int32,
+                                                        ctypes.c_int32, ctypes.c_int32, _P, _P]),
+    "ep_grouped_gemm_mxfp4": (ctypes.c_int, [ctypes.POINTER(ep_handle), _P, _P, _P, ctypes.c_int32, ctypes.c_int32,
+                                             _P, _P]),
+    "ep_rms_norm": (ctypes.c_int, [ctypes.c_int32, ctypes.c_int32, ctypes.c_int32, _P, _P, _P, ctypes.c_float, _P, _P,
+                                   _P, _P, _P]),
+    "ep_rms_norm_workspace_bytes": (ctypes.c_size_t, [ctypes.c_int32, ctypes.c_int32]),
+    "ep_rms_norm_backward": (ctypes.c_int, [ctypes.c_int32, ctypes.c_int32, _P, _P, _P, _P, _P, _P, _P, _P,
+                                            ctypes.c_size_t, _P]),
     "ep_handle_read_counts": (ctypes.c_int, [ctypes.POINTER(ep_handle), _P, _P, _P, _P]),
     "ep_handle_check": (ctypes.c_int, [ctypes.POINTER(ep_handle), _P, _P]),
     "ep_status_string": (ctypes.c_char_p, [ctypes.c_int32]),
@@ -185,6 +197,53 @@ def ep_grouped_gemm_fp8(h: ep_handle, a: int, a_scales: int, b: int, b_scales: i
                         stream: int) -> None:
     _check(lib().ep_grouped_gemm_fp8(ctypes.byref(h), a, a_scales, b, b_scales, int(n), out, stream),
            "ep_grouped_gemm_fp8")
+
+
+def ep_grouped_gemm_bf16(h: ep_handle, a: int, b: int, n: int, k: int, out: int, stream: int) -> None:
+    st = (_lib or lib()).ep_grouped_gemm_bf16(ctypes.byref(h), a, b, n, k, out, stream)
+    if st != EP_OK:
+        _check(st, "ep_grouped_gemm_bf16")
+
+
+def ep_grouped_gemm_bf16_grad_input(h: ep_handle, grad_out: int, b: int, n: int, k: int, grad_a: int,
+                                    stream: int) -> None:
+    st = (_lib or lib()).ep_grouped_gemm_bf16_grad_input(ctypes.byref(h), grad_out, b, n, k, grad_a, stream)
+    if st != EP_OK:
+        _check(st, "ep_grouped_gemm_bf16_grad_input")
+
+
+def ep_grouped_gemm_bf16_grad_weight(h: ep_handle, grad_out: int, a: int, n: int, k: int, grad_b_f32: int,
+                                     grad_b: int, stream: int) -> None:
+    st = (_lib or lib()).ep_grouped_gemm_bf16_grad_weight(ctypes.byref(h), grad_out, a, n, k, grad_b_f32, grad_b,
+                                                          stream)
+    if st != EP_OK:
+        _check(st, "ep_grouped_gemm_bf16_grad_weight")
+
+
+def ep_grouped_gemm_mxfp4(h: ep_handle, a: int, b: int, b_scales: int, n: int, k: int, out: int, stream: int) -> None:
+    st = (_lib or lib()).ep_grouped_gemm_mxfp4(ctypes.byref(h), a, b, b_scales, n, k, out, stream)
+    if st != EP_OK:
+        _check(st, "ep_grouped_gemm_mxfp4")
+
+
+def ep_rms_norm(num_tokens: int, hidden: int, dtype: int, x: int, residual, weight: int, eps: float, total, y: int,
+                y_scales, rstd: int, stream: int) -> None:
+    st = (_lib or lib()).ep_rms_norm(num_tokens, hidden, dtype, x, residual, weight, eps, total, y, y_scales, rstd,
+                                     stream)
+    if st != EP_OK:
+        _check(st, "ep_rms_norm")
+
+
+def ep_rms_norm_workspace_bytes(num_tokens: int, hidden: int) -> int:
+    return int(lib().ep_rms_norm_workspace_bytes(int(num_tokens), int(hidden)))
+
+
+def ep_rms_norm_backward(num_tokens: int, hidden: int, total: int, weight: int, rstd: int, grad_y: int, grad_total,
+                         grad_x: int, grad_weight: int, workspace: int, workspace_bytes: int, stream: int) -> None:
+    st = (_lib or lib()).ep_rms_norm_backward(num_tokens, hidden, total, weight, rstd, grad_y, grad_total, grad_x,
+                                              grad_weight, workspace, workspace_bytes, stream)
+    if st != EP_OK:
+        _check(st, "ep_rms_norm_backward")
 
 
 def ep_handle_read_counts(h: ep_handle, cnt, pad, rows, stream: int) -> None:

@@ -204,6 +204,73 @@ ep_status do_combine(const ep_handle* h, const void* y, const float* w, void* ou
     return EP_OK;
 }
 
+// Row fields of the products that accept any alignment.
+ep::RowsArgs rows_args(const ep_handle* h) {
+    const ep_config& c = h->cfg;
+    ep::RowsArgs r;
+    r.cnt = h->cnt;
+    r.pad = h->pad;
+    r.expert_off = h->expert_off;
+    r.E = c.num_experts;
+    r.mode = c.mode;
+    r.C = c.capacity;
+    r.zero_pad = (c.mode == EP_MODE_COMPACT && !(c.flags & EP_FLAG_NO_ZERO_PAD)) ? 1 : 0;
+    return r;
+}
+
+// Widths of a grouped product's rows: kernels take the byte offsets within a
+// tile of rows as 32-bit values.
+constexpr int kMaxProductWidth = 1 << 20;
+
+ep_status check_product(const ep_handle* h, int32_t n, int32_t k, int k_multiple) {
+    ep_status s = check_handle(h);
+    if (s != EP_OK) return s;
+    if (n < 8 || n % 8 != 0) return fail(EP_ERR_INVALID_ARG, "n %d must be a positive multiple of 8", n);
+    if (k < k_multiple || k % k_multiple != 0)
+        return fail(EP_ERR_INVALID_ARG, "k %d must be a positive multiple of %d", k, k_multiple);
+    if (n > kMaxProductWidth || k > kMaxProductWidth)
+        return fail(EP_ERR_UNSUPPORTED, "n %d and k %d may be at most %d", n, k, kMaxProductWidth);
+    return EP_OK;
+}
+
+// Checks a BF16 product and launches it. x, y: the operands; xn, yn, cn: what the
+// caller calls them and the output.
+ep_status do_grouped_gemm_bf16(int dir, const ep_handle* h, const void* x, const char* xn, const void* y,
+                               const char* yn, int32_t n, int32_t k, int out_f32, void* out, const char* cn,
+                               hipStream_t stream) {
+    ep_status s = check_product(h, n, k, 8);
+    if (s != EP_OK) return s;
+    const int64_t pairs = (int64_t)h->num_tokens * h->cfg.num_topk;
+    const bool rows = pairs > 0;  // without a pair no operand is read, and only grad_weight writes
+    if ((rows && x == nullptr) || !aligned(x, 16))
+        return fail(EP_ERR_INVALID_ARG, "%s must be non-NULL and 16-byte aligned", xn);
+    if ((rows && y == nullptr) || !aligned(y, 16))
+        return fail(EP_ERR_INVALID_ARG, "%s must be non-NULL and 16-byte aligned", yn);
+    if (((rows || dir == ep::kGradWeight) && out == nullptr) || !aligned(out, 16))
+        return fail(EP_ERR_INVALID_ARG, "%s must be non-NULL and 16-byte aligned", cn);
+    ep::GroupedArgs a;
+    a.rows = rows_args(h);
+    a.a = (const uint16_t*)x;
+    a.b = (const uint16_t*)y;
+    a.c = out;
+    a.M = dir == ep::kGradWeight ? n : 0;
+    a.N = dir == ep::kForward ? n : k;
+    a.K = dir == ep::kForward ? k : n;
+    a.out_f32 = out_f32;
+    hipError_t e = ep::launch_grouped_gemm_bf16(dir, a, pairs, stream);
+    if (e != hipSuccess) return hip_fail(e, "BF16 grouped GEMM launch");
+    return EP_OK;
+}
+
+ep_status check_norm(int32_t num_tokens, int32_t hidden) {
+    if (num_tokens < 0) return fail(EP_ERR_INVALID_ARG, "num_tokens %d must not be negative", num_tokens);
+    if (hidden < 8 || hidden % 8 != 0)
+        return fail(EP_ERR_INVALID_ARG, "hidden %d must be a positive multiple of 8", hidden);
+    if (hidden > ep::kMaxNormHidden)
+        return fail(EP_ERR_UNSUPPORTED, "hidden %d exceeds %d", hidden, ep::kMaxNormHidden);
+    return EP_OK;
+}
+
 // Bytes of the multi-block layout's per-block partials for one call
 // (counts [nblk][E], distinct tokens [nblk][D], error bits [nblk]; regions
 // 256-byte aligned), and their offsets from the start of that scratch.
@@ -562,6 +629,125 @@ ep_status ep_grouped_gemm_fp8(const ep_handle* h, const void* a, const float* a_
     g.C = c.capacity;
     hipError_t e = ep::launch_grouped_gemm_fp8(g, rows_bound(c), (hipStream_t)stream);
     if (e != hipSuccess) return hip_fail(e, "grouped GEMM launch");
+    return EP_OK;
+}
+
+ep_status ep_grouped_gemm_bf16(const ep_handle* h, const void* a, const void* b, int32_t n, int32_t k, void* out,
+                               void* stream) {
+    return do_grouped_gemm_bf16(ep::kForward, h, a, "a", b, "b", n, k, 0, out, "out", (hipStream_t)stream);
+}
+
+ep_status ep_grouped_gemm_bf16_grad_input(const ep_handle* h, const void* grad_out, const void* b, int32_t n,
+                                          int32_t k, void* grad_a, void* stream) {
+    return do_grouped_gemm_bf16(ep::kGradInput, h, grad_out, "grad_out", b, "b", n, k, 0, grad_a, "grad_a",
+                                (hipStream_t)stream);
+}
+
+ep_status ep_grouped_gemm_bf16_grad_weight(const ep_handle* h, const void* grad_out, const void* a, int32_t n,
+                                           int32_t k, int32_t grad_b_f32, void* grad_b, void* stream) {
+    if (grad_b_f32 != 0 && grad_b_f32 != 1)
+        return fail(EP_ERR_INVALID_ARG, "grad_b_f32 %d must be 0 or 1", grad_b_f32);
+    return do_grouped_gemm_bf16(ep::kGradWeight, h, grad_out, "grad_out", a, "a", n, k, grad_b_f32, grad_b, "grad_b",
+                                (hipStream_t)stream);
+}
+
+ep_status ep_grouped_gemm_mxfp4(const ep_handle* h, const void* a, const void* b, const void* b_scales, int32_t n,
+                                int32_t k, void* out, void* stream) {
+    ep_status s = check_product(h, n, k, 32);
+    if (s != EP_OK) return s;
+    const int64_t pairs = (int64_t)h->num_tokens * h->cfg.num_topk;
+    if (pairs > 0 && (a == nullptr || b == nullptr || b_scales == nullptr || out == nullptr))
+        return fail(EP_ERR_INVALID_ARG, "a, b, b_scales and out must be non-NULL");
+    if (!aligned(a, 16) || !aligned(b, 16) || !aligned(out, 16))
+        return fail(EP_ERR_INVALID_ARG, "a, b and out must be 16-byte aligned");
+    ep::Mxfp4Args g;
+    g.rows = rows_args(h);
+    g.x = (const uint16_t*)a;
+    g.b = (const uint8_t*)b;
+    g.b_scales = (const uint8_t*)b_scales;
+    g.out = (uint16_t*)out;
+    g.N = n;
+    g.K = k;
+    hipError_t e = ep::launch_grouped_gemm_mxfp4(g, pairs, (hipStream_t)stream);
+    if (e != hipSuccess) return hip_fail(e, "MXFP4 grouped GEMM launch");
+    return EP_OK;
+}
+
+ep_status ep_rms_norm(int32_t num_tokens, int32_t hidden, int32_t dtype, const void* x, const void* residual,
+                      const void* weight, float eps, void* total, void* y, float* y_scales, float* rstd,
+                      void* stream) {
+    ep_status s = check_norm(num_tokens, hidden);
+    if (s != EP_OK) return s;
+    if (dtype != EP_BF16 && dtype != EP_FP8_QUANTIZE)
+        return fail(EP_ERR_INVALID_ARG, "dtype %d must be EP_BF16 or EP_FP8_QUANTIZE", (int)dtype);
+    const bool fp8 = dtype == EP_FP8_QUANTIZE;
+    if (fp8 && hidden % 128 != 0)
+        return fail(EP_ERR_INVALID_ARG, "an FP8 output needs hidden %% 128 == 0 (hidden %d)", hidden);
+    if (!(eps > 0.0f) || eps > 3.0e38f) return fail(EP_ERR_INVALID_ARG, "eps must be positive and finite");
+    // an empty batch's arrays may be NULL
+    if (num_tokens > 0 && (residual == nullptr) != (total == nullptr))
+        return fail(EP_ERR_INVALID_ARG, "residual and total must be given together");
+    if (num_tokens > 0 && fp8 != (y_scales != nullptr))
+        return fail(EP_ERR_INVALID_ARG, "y_scales must be given for an FP8 output, and only for it");
+    if (num_tokens > 0 && (x == nullptr || weight == nullptr || y == nullptr || rstd == nullptr))
+        return fail(EP_ERR_INVALID_ARG, "x, weight, y and rstd must be non-NULL");
+    if (!aligned(x, 16) || !aligned(residual, 16) || !aligned(weight, 16) || !aligned(total, 16) || !aligned(y, 16))
+        return fail(EP_ERR_INVALID_ARG, "x, residual, weight, total and y must be 16-byte aligned");
+    if (!aligned(y_scales, 4) || !aligned(rstd, 4))
+        return fail(EP_ERR_INVALID_ARG, "y_scales and rstd must be 4-byte aligned");
+    ep::NormArgs a;
+    a.x = (const uint16_t*)x;
+    a.residual = (const uint16_t*)residual;
+    a.weight = (const uint16_t*)weight;
+    a.total = (uint16_t*)total;
+    a.y = y;
+    a.scales = y_scales;
+    a.rstd = rstd;
+    a.eps = eps;
+    a.T = num_tokens;
+    a.H = hidden;
+    hipError_t e = ep::launch_rms_norm(a, (hipStream_t)stream);
+    if (e != hipSuccess) return hip_fail(e, "RMS norm launch");
+    return EP_OK;
+}
+
+size_t ep_rms_norm_workspace_bytes(int32_t num_tokens, int32_t hidden) {
+    if (check_norm(num_tokens, hidden) != EP_OK) return 0;
+    // never 0 for valid sizes, so that 0 means an error
+    return round_up(4 * (size_t)hidden * (size_t)(num_tokens > 0 ? ep::norm_backward_parts(num_tokens) : 1), 256);
+}
+
+ep_status ep_rms_norm_backward(int32_t num_tokens, int32_t hidden, const void* total, const void* weight,
+                               const float* rstd, const void* grad_y, const void* grad_total, void* grad_x,
+                               float* grad_weight, void* workspace, size_t workspace_bytes, void* stream) {
+    ep_status s = check_norm(num_tokens, hidden);
+    if (s != EP_OK) return s;
+    if (num_tokens > 0 &&
+        (total == nullptr || weight == nullptr || rstd == nullptr || grad_y == nullptr || grad_x == nullptr))
+        return fail(EP_ERR_INVALID_ARG, "total, weight, rstd, grad_y and grad_x must be non-NULL");
+    if (!aligned(total, 16) || !aligned(weight, 16) || !aligned(grad_y, 16) || !aligned(grad_total, 16) ||
+        !aligned(grad_x, 16))
+        return fail(EP_ERR_INVALID_ARG, "total, weight, grad_y, grad_total and grad_x must be 16-byte aligned");
+    if (!aligned(rstd, 4) || grad_weight == nullptr || !aligned(grad_weight, 4))
+        return fail(EP_ERR_INVALID_ARG, "rstd and grad_weight must be 4-byte aligned, grad_weight non-NULL");
+    if (workspace == nullptr || !aligned(workspace, 256))
+        return fail(EP_ERR_INVALID_ARG, "workspace must be non-NULL and 256-byte aligned");
+    const size_t need = ep_rms_norm_workspace_bytes(num_tokens, hidden);
+    if (workspace_bytes < need)
+        return fail(EP_ERR_WORKSPACE, "workspace has %zu bytes, the norm's backward needs %zu", workspace_bytes, need);
+    ep::NormBackwardArgs a;
+    a.total = (const uint16_t*)total;
+    a.weight = (const uint16_t*)weight;
+    a.rstd = rstd;
+    a.grad_y = (const uint16_t*)grad_y;
+    a.grad_total = (const uint16_t*)grad_total;
+    a.grad_x = (uint16_t*)grad_x;
+    a.grad_weight = grad_weight;
+    a.partial = (float*)workspace;
+    a.T = num_tokens;
+    a.H = hidden;
+    hipError_t e = ep::launch_rms_norm_backward(a, (hipStream_t)stream);
+    if (e != hipSuccess) return hip_fail(e, "RMS norm backward launch");
     return EP_OK;
 }
 

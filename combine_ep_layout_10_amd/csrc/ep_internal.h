@@ -128,6 +128,72 @@ struct GemmArgs {
     int E, K, N, mode, C;
 };
 
+// BF16 products grouped by expert (ep_gemm_bf16.hip): C [M, N] of expert e is
+// the sum over K of A and B. The rows are the expert's receive rows: M in the
+// first two directions, the reduction in the third.
+enum GroupedDirection { kForward = 0, kGradInput = 1, kGradWeight = 2 };
+
+// The rows of a layout, for the products that accept any alignment.
+struct RowsArgs {
+    const int32_t* cnt;
+    const int32_t* pad;
+    const int32_t* expert_off;
+    int E, mode, C;
+    int zero_pad;  // clear the padding rows of the output
+};
+
+struct GroupedArgs {
+    RowsArgs rows;
+    const uint16_t* a;  // [rows, K]; kGradWeight: grad_out [rows, M]
+    const uint16_t* b;  // weights: kForward [E, N, K], kGradInput [E, K, N]; kGradWeight: a [rows, N]
+    void* c;            // bf16 [rows, N]; kGradWeight: binary32 or bf16 [E, M, N]
+    int M, N, K;
+    int out_f32;  // kGradWeight: binary32 output
+};
+
+// Products with MXFP4 weights (ep_gemm_mxfp4.hip).
+struct Mxfp4Args {
+    RowsArgs rows;
+    const uint16_t* x;        // bf16 [rows, K]
+    const uint8_t* b;         // [E, N, K / 2]
+    const uint8_t* b_scales;  // [E, N, K / 32]
+    uint16_t* out;            // bf16 [rows, N]
+    int N, K;
+};
+
+// RMS norm (ep_norm.hip) and its backward.
+struct NormArgs {
+    const uint16_t* x;
+    const uint16_t* residual;  // or NULL
+    const uint16_t* weight;
+    uint16_t* total;  // bf16(x + residual); NULL without a residual
+    void* y;          // bf16 or E4M3FN
+    float* scales;    // [T, H / 128] for an FP8 output, else NULL
+    float* rstd;
+    float eps;
+    int T, H;
+};
+
+struct NormBackwardArgs {
+    const uint16_t* total;
+    const uint16_t* weight;
+    const float* rstd;
+    const uint16_t* grad_y;
+    const uint16_t* grad_total;  // or NULL
+    uint16_t* grad_x;
+    float* grad_weight;
+    float* partial;  // [norm_backward_parts(T), H]
+    int T, H;
+};
+
+// Channels of a norm's row: at most 4 vectors of 8 for each of 1,024 lanes.
+constexpr int kMaxNormHidden = 1 << 15;
+// Row groups of the norm's backward, each with its own partial sum of the
+// weight gradient: a function of T alone, so that results never depend on the
+// launch geometry.
+constexpr int kNormParts = 512;
+inline int norm_backward_parts(int T) { return T < kNormParts ? T : kNormParts; }
+
 // Padding rows per zero-fill piece (a piece of one expert's padding): in the
 // dispatch kernel, and in the single-launch layout + dispatch, where every
 // block also redoes the small layout and so should be few. In the dispatch
@@ -157,6 +223,11 @@ hipError_t launch_dispatch(int kind, const DispatchArgs& a, hipStream_t stream);
 hipError_t launch_combine(const CombineArgs& a, hipStream_t stream);
 hipError_t launch_weight_grad(const WeightGradArgs& a, hipStream_t stream);
 hipError_t launch_grouped_gemm_fp8(const GemmArgs& a, int64_t rows_bound, hipStream_t stream);
+// pairs: num_tokens * num_topk, the most rows that hold a pair.
+hipError_t launch_grouped_gemm_bf16(int dir, const GroupedArgs& a, int64_t pairs, hipStream_t stream);
+hipError_t launch_grouped_gemm_mxfp4(const Mxfp4Args& a, int64_t pairs, hipStream_t stream);
+hipError_t launch_rms_norm(const NormArgs& a, hipStream_t stream);
+hipError_t launch_rms_norm_backward(const NormBackwardArgs& a, hipStream_t stream);
 // Kernel arguments of the single-launch layout + dispatch, packed into the
 // fields that kernel reads: the handle's arrays as 32-bit offsets from the
 // workspace base, small sizes as 16-bit fields. A launch costs the host

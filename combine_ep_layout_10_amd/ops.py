@@ -12,6 +12,12 @@ Mapping to the DeepEP README ("Interfaces and examples"):
   combine_weight_grad          -> the weight gradient of the weighted combine
   grouped_gemm_fp8             -> the expert GEMM the layout is built for
   dispatch with an old Handle  -> decode_dispatch with cached_handle
+
+Around them, what an expert layer needs next: the experts' BF16 products in the
+three directions of training (grouped_gemm_bf16, ..._grad_input,
+..._grad_weight), their products with 4-bit weights (grouped_gemm_mxfp4), and
+the RMS norm before the dispatch with its backward (rms_norm,
+rms_norm_backward).
 """
 from __future__ import annotations
 
@@ -361,6 +367,155 @@ def grouped_gemm_fp8(h: Handle, a: torch.Tensor, a_scales: torch.Tensor, b: torc
                           _dev(b, "b", torch.uint8), _dev(b_scales, "b_scales", torch.float32), n,
                           _dev(out, "out", torch.bfloat16), _stream())
     return out
+
+
+def _product_out(out: Optional[torch.Tensor], shape, dtype, device, name: str) -> torch.Tensor:
+    if out is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    _need(out, shape, name)
+    return out
+
+
+def grouped_gemm_bf16(h: Handle, a: torch.Tensor, b: torch.Tensor, out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """BF16 products grouped by expert over the receive layout, any alignment:
+    out [rows bound, n], rows of expert e times b[e] [n, k]. Padding rows of
+    out are zero-filled (unless FLAG_NO_ZERO_PAD); rows past the layout are
+    not written."""
+    R, E = h.cfg.recv_rows_bound(), h.cfg.num_experts
+    if b.dim() != 3 or b.shape[0] != E:
+        raise ValueError("b must be [E, n, k]")
+    n, k = b.shape[1], b.shape[2]
+    _need(a, (R, k), "a")
+    out = _product_out(out, (R, n), torch.bfloat16, a.device, "out")
+    cur = _current_device()
+    F.ep_grouped_gemm_bf16(h.c, _dev(a, "a", torch.bfloat16, cur), _dev(b, "b", torch.bfloat16, cur), n, k,
+                           _dev(out, "out", torch.bfloat16, cur), _raw_stream(cur))
+    return out
+
+
+def grouped_gemm_bf16_grad_input(h: Handle, grad_out: torch.Tensor, b: torch.Tensor,
+                                 grad_a: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Gradient of grouped_gemm_bf16 with respect to a: grad_a [rows bound, k],
+    rows of grad_out [rows bound, n] times b[e] [n, k]."""
+    R, E = h.cfg.recv_rows_bound(), h.cfg.num_experts
+    if b.dim() != 3 or b.shape[0] != E:
+        raise ValueError("b must be [E, n, k]")
+    n, k = b.shape[1], b.shape[2]
+    _need(grad_out, (R, n), "grad_out")
+    grad_a = _product_out(grad_a, (R, k), torch.bfloat16, grad_out.device, "grad_a")
+    cur = _current_device()
+    F.ep_grouped_gemm_bf16_grad_input(h.c, _dev(grad_out, "grad_out", torch.bfloat16, cur),
+                                      _dev(b, "b", torch.bfloat16, cur), n, k,
+                                      _dev(grad_a, "grad_a", torch.bfloat16, cur), _raw_stream(cur))
+    return grad_a
+
+
+def grouped_gemm_bf16_grad_weight(h: Handle, grad_out: torch.Tensor, a: torch.Tensor,
+                                  grad_b: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Gradient of grouped_gemm_bf16 with respect to b: grad_b [E, n, k], the
+    sum over each expert's rows of grad_out[r, :] x a[r, :]; float32 unless a
+    bfloat16 grad_b is given. Experts without a row get zeros."""
+    R, E = h.cfg.recv_rows_bound(), h.cfg.num_experts
+    if grad_out.dim() != 2 or a.dim() != 2:
+        raise ValueError("grad_out must be [rows bound, n] and a [rows bound, k]")
+    n, k = grad_out.shape[1], a.shape[1]
+    _need(grad_out, (R, n), "grad_out")
+    _need(a, (R, k), "a")
+    grad_b = _product_out(grad_b, (E, n, k), torch.float32, grad_out.device, "grad_b")
+    cur = _current_device()
+    p = _dev(grad_b, "grad_b", (torch.float32, torch.bfloat16), cur)
+    F.ep_grouped_gemm_bf16_grad_weight(h.c, _dev(grad_out, "grad_out", torch.bfloat16, cur),
+                                       _dev(a, "a", torch.bfloat16, cur), n, k, int(grad_b.dtype is torch.float32), p,
+                                       _raw_stream(cur))
+    return grad_b
+
+
+def grouped_gemm_mxfp4(h: Handle, a: torch.Tensor, b: torch.Tensor, b_scales: torch.Tensor,
+                       out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """grouped_gemm_bf16 with MXFP4 weights: b uint8 [E, n, k / 2] holds two
+    E2M1 codes a byte (low nibble first), b_scales uint8 [E, n, k / 32] their
+    E8M0 scales."""
+    R, E = h.cfg.recv_rows_bound(), h.cfg.num_experts
+    if b.dim() != 3 or b.shape[0] != E:
+        raise ValueError("b must be [E, n, k / 2]")
+    n, k = b.shape[1], 2 * b.shape[2]
+    _need(a, (R, k), "a")
+    _need(b_scales, (E, n, k // 32), "b_scales")
+    out = _product_out(out, (R, n), torch.bfloat16, a.device, "out")
+    cur = _current_device()
+    F.ep_grouped_gemm_mxfp4(h.c, _dev(a, "a", torch.bfloat16, cur), _dev(b, "b", torch.uint8, cur),
+                            _dev(b_scales, "b_scales", torch.uint8, cur), n, k,
+                            _dev(out, "out", torch.bfloat16, cur), _raw_stream(cur))
+    return out
+
+
+# ---------------------------------------------------------------- RMS norm
+
+def rms_norm(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6, residual: Optional[torch.Tensor] = None,
+             dtype: int = BF16, total: Optional[torch.Tensor] = None, y: Optional[torch.Tensor] = None,
+             y_scales: Optional[torch.Tensor] = None, rstd: Optional[torch.Tensor] = None):
+    """RMS norm of x (+ residual). Returns (y, y_scales, total, rstd): y [T, H]
+    bf16 (y_scales None), or with dtype FP8_QUANTIZE the codes (uint8) and
+    their 1x128 scales, which dispatch takes with FP8_PREQUANT; total, the
+    bf16 sum that was normalised (x itself without a residual), into x's or
+    residual's own buffer when given as `total`; rstd [T], for the backward."""
+    if x.dim() != 2:
+        raise ValueError("x must be [T, H]")
+    T, H = x.shape
+    fp8 = dtype == FP8_QUANTIZE
+    _need(weight, (H,), "weight")
+    _need(residual, (T, H), "residual")
+    if residual is None:
+        if total is not None:
+            raise ValueError("total is written only with a residual")
+    else:
+        total = _product_out(total, (T, H), torch.bfloat16, x.device, "total")
+    y = _product_out(y, (T, H), torch.uint8 if fp8 else torch.bfloat16, x.device, "y")
+    if fp8:
+        y_scales = _product_out(y_scales, (T, H // 128), torch.float32, x.device, "y_scales")
+    rstd = _product_out(rstd, (T,), torch.float32, x.device, "rstd")
+    cur = _current_device()
+    F.ep_rms_norm(T, H, dtype, _dev(x, "x", torch.bfloat16, cur), _opt(residual, "residual", torch.bfloat16, cur),
+                  _dev(weight, "weight", torch.bfloat16, cur), eps, _opt(total, "total", torch.bfloat16, cur),
+                  _dev(y, "y", torch.uint8 if fp8 else torch.bfloat16, cur),
+                  _opt(y_scales, "y_scales", torch.float32, cur), _dev(rstd, "rstd", torch.float32, cur),
+                  _raw_stream(cur))
+    return y, y_scales, (x if total is None else total), rstd
+
+
+def rms_norm_workspace(num_tokens: int, hidden: int, device="cuda") -> torch.Tensor:
+    """Workspace of rms_norm_backward, for callers that keep one."""
+    n = F.ep_rms_norm_workspace_bytes(num_tokens, hidden)
+    if n == 0:
+        raise F.EPError(F.EP_ERR_INVALID_ARG, "ep_rms_norm_workspace_bytes", F.last_error_message())
+    return torch.empty(n, dtype=torch.uint8, device=device)
+
+
+def rms_norm_backward(total: torch.Tensor, weight: torch.Tensor, rstd: torch.Tensor, grad_y: torch.Tensor,
+                      grad_total: Optional[torch.Tensor] = None, grad_x: Optional[torch.Tensor] = None,
+                      grad_weight: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None):
+    """Backward of rms_norm: (grad_x [T, H] bf16, grad_weight [H] float32).
+    grad_x is the gradient of x and of residual; grad_total is the gradient
+    that reaches total by other ways than y (grad_x may be its own buffer)."""
+    if total.dim() != 2:
+        raise ValueError("total must be [T, H]")
+    T, H = total.shape
+    _need(weight, (H,), "weight")
+    _need(rstd, (T,), "rstd")
+    _need(grad_y, (T, H), "grad_y")
+    _need(grad_total, (T, H), "grad_total")
+    grad_x = _product_out(grad_x, (T, H), torch.bfloat16, total.device, "grad_x")
+    grad_weight = _product_out(grad_weight, (H,), torch.float32, total.device, "grad_weight")
+    if workspace is None:
+        workspace = rms_norm_workspace(T, H, total.device)
+    cur = _current_device()
+    F.ep_rms_norm_backward(T, H, _dev(total, "total", torch.bfloat16, cur), _dev(weight, "weight", torch.bfloat16, cur),
+                           _dev(rstd, "rstd", torch.float32, cur), _dev(grad_y, "grad_y", torch.bfloat16, cur),
+                           _opt(grad_total, "grad_total", torch.bfloat16, cur),
+                           _dev(grad_x, "grad_x", torch.bfloat16, cur),
+                           _dev(grad_weight, "grad_weight", torch.float32, cur),
+                           _dev(workspace, "workspace", torch.uint8, cur), workspace.numel(), _raw_stream(cur))
+    return grad_x, grad_weight
 
 # ---------------------------------------------------------------- bound calls
 

@@ -331,6 +331,113 @@ ep_status ep_combine_weight_grad(const ep_handle* h, const void* grad_out, const
 ep_status ep_grouped_gemm_fp8(const ep_handle* h, const void* a, const float* a_scales, const void* b,
                               const float* b_scales, int32_t n, void* out, void* stream);
 
+/* BF16 products grouped by expert over the receive layout, for any
+ * expert_alignment or capacity: the experts' products of a training step, in
+ * its three directions. Live rows are those that hold a pair: expert e's first
+ * cnt[e] rows (FIXED: pad[e]). Only live rows are read as operands, so the
+ * contents of padding rows, and of experts without a pair, never matter. n
+ * (output channels) and k (input channels; not tied to cfg.hidden, so that an
+ * expert's second layer is the same call) are multiples of 8, at most 2^20
+ * (EP_ERR_UNSUPPORTED above). Products of bf16 values are summed in binary32
+ * by the MFMA, in an order that depends on n, k and the live rows alone, and
+ * rounded once, to nearest even.
+ *
+ * Forward: for every live row r of expert e and c < n,
+ *   out[r, c] = bf16( sum_j a[r, j] * b[e, c, j] ),  j < k.
+ *   a    device bf16 [rows bound, k].
+ *   b    device bf16 [E, n, k]: one row of k weights per output channel, as
+ *        ep_grouped_gemm_fp8's.
+ *   out  device bf16 [rows bound, n]. COMPACT padding rows are zero-filled
+ *        unless EP_FLAG_NO_ZERO_PAD; no other row is touched. Must not overlap
+ *        an operand (also below). */
+ep_status ep_grouped_gemm_bf16(const ep_handle* h, const void* a, const void* b, int32_t n, int32_t k, void* out,
+                               void* stream);
+
+/* Gradient of ep_grouped_gemm_bf16 with respect to a: for every live row r of
+ * expert e and j < k,
+ *   grad_a[r, j] = bf16( sum_c grad_out[r, c] * b[e, c, j] ),  c < n.
+ *   grad_out  device bf16 [rows bound, n].
+ *   b         device bf16 [E, n, k], the forward's.
+ *   grad_a    device bf16 [rows bound, k]; padding rows as the forward's. */
+ep_status ep_grouped_gemm_bf16_grad_input(const ep_handle* h, const void* grad_out, const void* b, int32_t n,
+                                          int32_t k, void* grad_a, void* stream);
+
+/* Gradient of ep_grouped_gemm_bf16 with respect to b, whole: for every expert
+ * e, c < n and j < k,
+ *   grad_b[e, c, j] = sum_r grad_out[r, c] * a[r, j] over e's live rows,
+ * zero for an expert without a live row.
+ *   grad_out  device bf16 [rows bound, n].
+ *   a         device bf16 [rows bound, k], the forward's.
+ *   grad_b    device [E, n, k]: binary32 when grad_b_f32 is 1, bf16 when 0. */
+ep_status ep_grouped_gemm_bf16_grad_weight(const ep_handle* h, const void* grad_out, const void* a, int32_t n,
+                                           int32_t k, int32_t grad_b_f32, void* grad_b, void* stream);
+
+/* Products with 4-bit weights grouped by expert, for serving: as
+ * ep_grouped_gemm_bf16, with the weights held as MXFP4 (OCP Microscaling
+ * Formats: E2M1 codes with one E8M0 scale for each 32 of them along k),
+ *   out[r, c] = bf16( sum_j a[r, j] * e2m1(code[e, c, j]) * 2^(scale[e, c, j / 32] - 127) ).
+ *   a         device bf16 [rows bound, k]; k is a multiple of 32.
+ *   b         device bytes [E, n, k / 2]: code j in byte j / 2, even j in the
+ *             low nibble; a code is sign, two exponent bits, one mantissa bit
+ *             (0, 0.5, 1, 1.5, 2, 3, 4, 6 and their negatives).
+ *   b_scales  device bytes [E, n, k / 32], any alignment. 255 is NaN: its 32
+ *             weights, and so the sums they enter, are NaN.
+ *   out       as ep_grouped_gemm_bf16's, and likewise n.
+ * A weight is a bf16 value (weights past bf16's largest finite value are
+ * infinite, as in binary32), products are summed in binary32 by the MFMA and
+ * rounded once. */
+ep_status ep_grouped_gemm_mxfp4(const ep_handle* h, const void* a, const void* b, const void* b_scales, int32_t n,
+                                int32_t k, void* out, void* stream);
+
+/* RMS norm with the residual's addition: the norm before the router and the
+ * dispatch, whose FP8 output is an EP_FP8_PREQUANT dispatch's input. For every
+ * token t < num_tokens and channel c < hidden:
+ *   s[c] = bf16(x[t, c] + residual[t, c]), written to total (without a
+ *          residual s = x, and total must be NULL);
+ *   rstd[t] = 1 / sqrt(mean_c s[c]^2 + eps), in binary32;
+ *   u[c] = s[c] * weight[c], exact in binary32;
+ * EP_BF16: y[t, c] = bf16(u[c] * rstd[t]);
+ * EP_FP8_QUANTIZE, for each 128 channels: q = max|u| / 448,
+ *   y[t, c] = E4M3FN(u[c] / q) rounded to nearest even and saturated to +-448,
+ *   y_scales = q * rstd[t] (q = 0: zero codes, scale 0). rstd multiplies a
+ *   whole row and so enters the scale alone.
+ *   x, residual, total  device bf16 [num_tokens, hidden]; total may be x's or
+ *                       residual's own buffer.
+ *   weight    device bf16 [hidden].
+ *   eps       positive.
+ *   y         device bf16 or E4M3FN [num_tokens, hidden].
+ *   y_scales  device binary32 [num_tokens, hidden / 128] for FP8, else NULL.
+ *   rstd      device binary32 [num_tokens].
+ * hidden is a multiple of 8 (FP8: of 128), at most 32768 (EP_ERR_UNSUPPORTED
+ * above). */
+ep_status ep_rms_norm(int32_t num_tokens, int32_t hidden, int32_t dtype, const void* x, const void* residual,
+                      const void* weight, float eps, void* total, void* y, float* y_scales, float* rstd,
+                      void* stream);
+
+/* Bytes of workspace ep_rms_norm_backward needs; 0 when the sizes are invalid
+ * (see ep_last_error_message). */
+size_t ep_rms_norm_workspace_bytes(int32_t num_tokens, int32_t hidden);
+
+/* Backward of ep_rms_norm (of y before an FP8 output's rounding): with s and
+ * rstd the forward's, g = grad_y[t] and m = mean_c(g[c] * weight[c] * s[c] * rstd[t]),
+ *   grad_x[t, c] = bf16( rstd[t] * (g[c] * weight[c] - s[c] * rstd[t] * m) + grad_total[t, c] ),
+ *   grad_weight[c] = sum_t g[c] * s[c] * rstd[t].
+ * grad_x is the gradient of x and of residual alike.
+ *   total       device bf16 [num_tokens, hidden]: the forward's total (x when
+ *               it had no residual).
+ *   rstd        device binary32 [num_tokens]: the forward's.
+ *   grad_y      device bf16 [num_tokens, hidden].
+ *   grad_total  device bf16 [num_tokens, hidden], the gradient that reaches
+ *               total by other ways than y, or NULL.
+ *   grad_x      device bf16 [num_tokens, hidden]; may be grad_total's own buffer.
+ *   grad_weight device binary32 [hidden]; zeros for an empty batch.
+ *   workspace   device, >= ep_rms_norm_workspace_bytes, 256-byte aligned; not
+ *               to be shared by calls that may overlap.
+ * Sums are taken in binary32 in an order that depends on the sizes alone. */
+ep_status ep_rms_norm_backward(int32_t num_tokens, int32_t hidden, const void* total, const void* weight,
+                               const float* rstd, const void* grad_y, const void* grad_total, void* grad_x,
+                               float* grad_weight, void* workspace, size_t workspace_bytes, void* stream);
+
 /* Copies cnt and pad (host arrays of E, either may be NULL) and the row
  * total R (host, may be NULL) to the host. Synchronises the stream: this is
  * the README's CPU synchronisation of a non-cached dispatch. */

@@ -1,0 +1,126 @@
+"""Argument checks of the experts' products and of the RMS norm on the CPU: every
+call below fails a check before anything reaches the GPU, so no pointer is
+dereferenced."""
+import ctypes
+
+import pytest
+
+from combine_ep_layout_10_amd import _ffi as F
+from test_abi_cpu import fake_handle
+
+FAKE = ctypes.c_void_p(1 << 20)
+ODD = ctypes.c_void_p((1 << 20) + 8)     # 8-byte, not 16-byte, aligned
+BYTE = ctypes.c_void_p((1 << 20) + 2)
+BAD, UNSUP, WS = F.EP_ERR_INVALID_ARG, F.EP_ERR_UNSUPPORTED, F.EP_ERR_WORKSPACE
+
+
+def bf16_calls():
+    l = F.lib()
+    return {
+        "forward": lambda h, x, y, n, k, c: l.ep_grouped_gemm_bf16(h, x, y, n, k, c, None),
+        "grad_input": lambda h, x, y, n, k, c: l.ep_grouped_gemm_bf16_grad_input(h, x, y, n, k, c, None),
+        "grad_weight": lambda h, x, y, n, k, c: l.ep_grouped_gemm_bf16_grad_weight(h, x, y, n, k, 1, c, None),
+    }
+
+
+@pytest.mark.parametrize("name", ["forward", "grad_input", "grad_weight"])
+def test_bf16_products(name):
+    f = bf16_calls()[name]
+    h = ctypes.byref(fake_handle())
+    assert f(None, FAKE, FAKE, 64, 64, FAKE) == BAD
+    for n in (0, -8, 4, 12, 63):
+        assert f(h, FAKE, FAKE, n, 64, FAKE) == BAD, n
+        assert f(h, FAKE, FAKE, 64, n, FAKE) == BAD, n
+    assert f(h, FAKE, FAKE, (1 << 20) + 8, 64, FAKE) == UNSUP
+    assert f(h, FAKE, FAKE, 64, (1 << 20) + 8, FAKE) == UNSUP
+    for bad in (None, ODD):
+        assert f(h, bad, FAKE, 64, 64, FAKE) == BAD
+        assert f(h, FAKE, bad, 64, 64, FAKE) == BAD
+        assert f(h, FAKE, FAKE, 64, 64, bad) == BAD
+        assert "16-byte" in F.last_error_message()
+    broken = fake_handle()
+    broken.cnt = None
+    assert f(ctypes.byref(broken), FAKE, FAKE, 64, 64, FAKE) == BAD
+    broken = fake_handle()
+    broken.num_tokens = 65
+    assert f(ctypes.byref(broken), FAKE, FAKE, 64, 64, FAKE) == BAD
+
+
+def test_errors_name_the_callers_arguments():
+    l, h = F.lib(), ctypes.byref(fake_handle())
+    assert l.ep_grouped_gemm_bf16_grad_input(h, None, FAKE, 64, 64, FAKE, None) == BAD
+    assert F.last_error_message().startswith("grad_out ")
+    assert l.ep_grouped_gemm_bf16_grad_weight(h, FAKE, FAKE, 64, 64, 0, None, None) == BAD
+    assert F.last_error_message().startswith("grad_b ")
+    for f32 in (-1, 2):
+        assert l.ep_grouped_gemm_bf16_grad_weight(h, FAKE, FAKE, 64, 64, f32, FAKE, None) == BAD
+
+
+def test_empty_batch_needs_no_pointers():
+    """Without a pair nothing is read or written: NULL operands are fine, and nothing is launched."""
+    l, e = F.lib(), fake_handle()
+    e.num_tokens = 0
+    h = ctypes.byref(e)
+    assert l.ep_grouped_gemm_bf16(h, None, None, 64, 64, None, None) == F.EP_OK
+    assert l.ep_grouped_gemm_bf16_grad_input(h, None, None, 64, 64, None, None) == F.EP_OK
+    assert l.ep_grouped_gemm_mxfp4(h, None, None, None, 64, 64, None, None) == F.EP_OK
+    assert l.ep_grouped_gemm_bf16_grad_weight(h, None, None, 64, 64, 1, None, None) == BAD   # it writes zeros
+    assert l.ep_rms_norm(0, 64, F.EP_BF16, None, None, None, 1e-6, None, None, None, None, None) == F.EP_OK
+
+
+def test_mxfp4_products():
+    f, h = F.lib().ep_grouped_gemm_mxfp4, ctypes.byref(fake_handle())
+    assert f(None, FAKE, FAKE, FAKE, 64, 64, FAKE, None) == BAD
+    for n in (0, 12):
+        assert f(h, FAKE, FAKE, FAKE, n, 64, FAKE, None) == BAD
+    for k in (0, 16, 48, -32):
+        assert f(h, FAKE, FAKE, FAKE, 64, k, FAKE, None) == BAD, k
+    assert f(h, FAKE, FAKE, FAKE, 64, (1 << 20) + 32, FAKE, None) == UNSUP
+    for args in ((None, FAKE, FAKE, FAKE), (FAKE, None, FAKE, FAKE), (FAKE, FAKE, None, FAKE), (FAKE, FAKE, FAKE, None),
+                 (ODD, FAKE, FAKE, FAKE), (FAKE, ODD, FAKE, FAKE), (FAKE, FAKE, FAKE, ODD)):
+        assert f(h, args[0], args[1], args[2], 64, 64, args[3], None) == BAD, args
+
+
+def test_norm():
+    f = F.lib().ep_rms_norm
+
+    def call(T=4, H=256, dtype=F.EP_BF16, x=FAKE, res=None, w=FAKE, eps=1e-6, total=None, y=FAKE, sc=None, rstd=FAKE):
+        return f(T, H, dtype, x, res, w, eps, total, y, sc, rstd, None)
+
+    assert call(T=-1) == BAD
+    for H in (0, -8, 100):
+        assert call(H=H) == BAD
+    assert call(H=32776) == UNSUP
+    assert call(dtype=F.EP_FP8_PREQUANT, sc=FAKE) == BAD
+    assert call(dtype=9) == BAD
+    assert call(H=200, dtype=F.EP_FP8_QUANTIZE, sc=FAKE) == BAD
+    assert call(dtype=F.EP_FP8_QUANTIZE) == BAD                  # scales missing
+    assert call(sc=FAKE) == BAD                                  # scales of a BF16 output
+    for eps in (0.0, -1e-6, float("nan"), float("inf")):
+        assert call(eps=eps) == BAD, eps
+    assert call(res=FAKE) == BAD and call(total=FAKE) == BAD     # only together
+    for name in ("x", "w", "y", "rstd"):
+        assert call(**{name: None}) == BAD, name
+    for name in ("x", "w", "y"):
+        assert call(**{name: ODD}) == BAD, name
+    assert call(res=ODD, total=FAKE) == BAD and call(res=FAKE, total=ODD) == BAD
+    assert call(rstd=BYTE) == BAD and call(dtype=F.EP_FP8_QUANTIZE, sc=BYTE) == BAD
+
+
+def test_norm_backward():
+    l = F.lib()
+    need = l.ep_rms_norm_workspace_bytes(4, 256)
+    assert need == 4 * 256 * 4 and l.ep_rms_norm_workspace_bytes(100000, 256) == 512 * 256 * 4
+    assert l.ep_rms_norm_workspace_bytes(0, 8) > 0
+    assert l.ep_rms_norm_workspace_bytes(-1, 256) == 0 and l.ep_rms_norm_workspace_bytes(4, 100) == 0
+
+    def call(T=4, H=256, s=FAKE, w=FAKE, rstd=FAKE, g=FAKE, gt=None, gx=FAKE, gw=FAKE, ws=FAKE, n=need):
+        return l.ep_rms_norm_backward(T, H, s, w, rstd, g, gt, gx, gw, ws, n, None)
+
+    assert call(T=-1) == BAD and call(H=100) == BAD and call(H=32776) == UNSUP
+    for name in ("s", "w", "rstd", "g", "gx", "gw", "ws"):
+        assert call(**{name: None}) == BAD, name
+    for name in ("s", "w", "g", "gt", "gx", "ws"):
+        assert call(**{name: ODD}) == BAD, name
+    assert call(rstd=BYTE) == BAD and call(gw=BYTE) == BAD
+    assert call(n=need - 1) == WS and "needs" in F.last_error_message()
