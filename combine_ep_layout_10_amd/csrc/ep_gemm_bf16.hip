@@ -12,113 +12,310 @@
 //   grad_weight  A [K rows, M]        B [K rows, N]
 // bf16 products are exact in binary32 and the MFMA accumulates in binary32, so
 // the only rounding is the output's.
+//
+// One kernel for the three: a block of 8 waves computes a tile of 256 x 256,
+// wave (wm, wn) the 16-row pieces 2 i + wm of it by the columns 64 wn .. + 63,
+// with v_mfma_f32_16x16x32_bf16. The reduction runs in steps of 32: both
+// operands' slices (16 KiB each) move from memory to LDS by DMA, into a ring of
+// kStages. All tails (rows, columns, reduction) are the buffer resource's range
+// check, which fills zeros.
+//
+// Rows: an expert's rows are cut into ceil(rows / 256) tiles of equal size
+// (rounded up to 32), and the loop is compiled for every number MI of 32-row
+// steps, so an expert with 260 rows costs two tiles of 5/8 and 4/8, and one
+// with 6 rows a single piece instead of a whole tile.
+//
+// Schedule: the waves form two groups (wm), half a step apart: while one
+// group's MFMAs run, the other reads its operands from LDS and issues DMA,
+// then a barrier exchanges the roles. Each SIMD holds one wave of either group,
+// so its matrix unit always has work.
+//
+// LDS: a slice of an operand that is contiguous along the reduction is
+// [256 rows][32 k] (64-byte rows); its 16-byte chunk c of row r is stored at
+// c ^ (r / 4 mod 4), so that 16 rows read at one chunk hit all 64 banks once. The
+// other operands are [32 k][256 columns] (512-byte rows) and are read through
+// the transposing LDS read, 4 k by 16 columns; their 32-byte pair of chunks p of
+// row k is stored at p ^ f(k), f(k) = k mod 4 + 4 (k / 8 mod 2), which spreads the
+// 8 rows that 32 lanes read over the banks.
+#include "ep_mma_dev.h"
 #include "ep_rows_dev.h"
 
 namespace ep {
 
-typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
-typedef float f32x4_t __attribute__((ext_vector_type(4)));
-
 namespace {
 
-constexpr int kBM = 64, kBN = 64, kBK = 32;
-constexpr int kPitch = kBK + 8;  // LDS row pitch (elements): 16-byte reads of 16 rows spread over the banks
+constexpr int kTile = 256;
+constexpr int kStep = 32;                    // reduction of one stage
+constexpr int kStages = 4;
+constexpr int kSlice = kTile * kStep * 2;    // bytes of one operand's slice
+constexpr int kLoads = 4;                    // DMA loads of a wave for a stage: two of A, two of B
+constexpr int kGroupRows = 8;                // row tiles that share column tiles in the block order
 
-// 64 x 32 operand tile into LDS as [64][kPitch], zeros outside `rows` x
-// `red`. KMAJOR: element (r, k) at src[k * ld + r], otherwise at src[r * ld + k].
-template <bool KMAJOR>
-__device__ __forceinline__ void stage(uint16_t* lds, const uint16_t* src, int64_t ld, int r0, int rows, int k0, int red) {
-    const int tid = threadIdx.x;  // 256 threads, 8 elements each
-    uint4 v = make_uint4(0u, 0u, 0u, 0u);
-    if (KMAJOR) {
-        const int k = tid >> 3, r = (tid & 7) * 8;
-        if (k0 + k < red && r0 + r < rows) v = *(const uint4*)(src + (int64_t)(k0 + k) * ld + r0 + r);
-        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-        for (int i = 0; i < 8; ++i) lds[(r + i) * kPitch + k] = (uint16_t)(w[i >> 1] >> (16 * (i & 1)));
-    } else {
-        const int r = tid >> 2, k = (tid & 3) * 8;
-        if (r0 + r < rows && k0 + k < red) v = *(const uint4*)(src + (int64_t)(r0 + r) * ld + k0 + k);
-        *(uint4*)(lds + r * kPitch + k) = v;
-    }
+struct Tile {
+    int e;           // expert
+    int m0, n0;      // first row (of the expert's) and column
+    int rows;        // rows of the tile that exist
+    bool last_rows;  // the expert's last row tile
+    ExpertRows er;
+};
+
+// Tile of logical block `local` among an expert's nt_m x nt_n: groups of
+// kGroupRows row tiles, within a group column by column, so that blocks that
+// run together on an XCD share few operand tiles.
+__device__ __forceinline__ void order_tiles(int local, int nt_m, int nt_n, int* m, int* n) {
+    const int g = local / (kGroupRows * nt_n);
+    const int in_group = min(kGroupRows, nt_m - g * kGroupRows);
+    const int rem = local - g * kGroupRows * nt_n;
+    *n = rem / in_group;
+    *m = g * kGroupRows + rem % in_group;
 }
 
 template <int DIR>
-__global__ __launch_bounds__(256) void k_grouped_gemm_bf16(GroupedArgs a) {
-    __shared__ __attribute__((aligned(16))) uint16_t s_a[kBM * kPitch];
-    __shared__ __attribute__((aligned(16))) uint16_t s_b[kBN * kPitch];
-    const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
-    const int nt_n = (a.N + kBN - 1) / kBN;
-    const int n0 = ((int)blockIdx.x % nt_n) * kBN;
-    int e, tile;
+__device__ __forceinline__ bool find_tile(const GroupedArgs& a, Tile* t) {
+    const int nt_n = (a.N + kTile - 1) / kTile;
+    int m, n;
     if (DIR == kGradWeight) {
-        const int nt_m = (a.M + kBM - 1) / kBM;
-        tile = (int)(blockIdx.x / nt_n) % nt_m;
-        e = (int)(blockIdx.x / nt_n) / nt_m;
-    } else if (!find_row_tile(a.rows, kBM, (int)(blockIdx.x / nt_n), &e, &tile)) {
-        return;
+        const int nt_m = (a.M + kTile - 1) / kTile;
+        const int L = logical_block((int)gridDim.x);
+        t->e = __builtin_amdgcn_readfirstlane(L / (nt_m * nt_n));
+        order_tiles(L % (nt_m * nt_n), nt_m, nt_n, &m, &n);
+        t->er = expert_rows(a.rows, t->e);
+        t->m0 = m * kTile;
+        t->rows = min(kTile, a.M - t->m0);
+        t->last_rows = false;
+    } else {
+        int local;
+        if (!find_expert(a.rows, kTile, nt_n, &t->e, &local)) return false;
+        t->er = expert_rows(a.rows, t->e);
+        const int live = t->er.live, nt_m = (live + kTile - 1) / kTile;
+        order_tiles(local, nt_m, nt_n, &m, &n);
+        const int each = ((live + nt_m - 1) / nt_m + 31) & ~31;  // rows of a tile; never leaves the last one empty
+        t->m0 = m * each;
+        t->rows = min(each, live - t->m0);
+        t->last_rows = m == nt_m - 1;
     }
-    const ExpertRows er = expert_rows(a.rows, e);
-    const int m0 = tile * kBM;
-    const int rows = DIR == kGradWeight ? a.M : er.live;  // valid rows of A
-    const int red = DIR == kGradWeight ? er.live : a.K;   // length of the reduction
-    const uint16_t* pa = a.a + (int64_t)er.first * (DIR == kGradWeight ? a.M : a.K);
-    const uint16_t* pb = DIR == kGradWeight ? a.b + (int64_t)er.first * a.N : a.b + (int64_t)e * a.N * a.K;
+    t->n0 = n * kTile;
+    t->m0 = __builtin_amdgcn_readfirstlane(t->m0);
+    t->n0 = __builtin_amdgcn_readfirstlane(t->n0);
+    t->rows = __builtin_amdgcn_readfirstlane(t->rows);
+    return true;
+}
 
-    f32x4_t acc[4];
+// One operand's way from memory to LDS and to the MFMAs. KMAJOR: the reduction
+// runs over the rows in memory (element (r, k) at base[k * ld + r]), otherwise
+// along them (base[r * ld + k]). `count`: rows of the tile that exist; `red`:
+// length of the reduction.
+template <bool KMAJOR>
+struct Operand {
+    const char* base;  // of the tile, reduction step 0
+    int ld;            // bytes between rows
+    int count, red;
+    uint32_t lds;      // this operand's ring
+    uint32_t off[2];   // byte offsets of this lane's two loads
+    int chunk;         // KMAJOR false: chunk (8 values of k) this lane loads
+
+    __device__ __forceinline__ void init(const uint16_t* src, int64_t ld_values, int r0, int rows, int reduction,
+                                         uint32_t ring, int w, int lane) {
+        ld = (int)(2 * ld_values);
+        count = rows;
+        red = reduction;
+        lds = ring;
+        base = (const char*)src + (KMAJOR ? 2 * (int64_t)r0 : (int64_t)r0 * ld);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) acc[i] = (f32x4_t){0.0f, 0.0f, 0.0f, 0.0f};
-    for (int k0 = 0; k0 < red; k0 += kBK) {
-        __syncthreads();
-        stage<DIR == kGradWeight>(s_a, pa, DIR == kGradWeight ? a.M : a.K, m0, rows, k0, red);
-        stage<DIR != kForward>(s_b, pb, DIR == kForward ? a.K : a.N, n0, a.N, k0, red);
-        __syncthreads();
-        // wave w: rows 16 w .. 16 w + 15, all 64 columns; operands swapped, so
-        // a lane ends up with row lane % 16 and four adjacent columns
-        const bf16x8_t fa = *(const bf16x8_t*)(s_a + (16 * w + (lane & 15)) * kPitch + (lane >> 4) * 8);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const bf16x8_t fb = *(const bf16x8_t*)(s_b + (16 * i + (lane & 15)) * kPitch + (lane >> 4) * 8);
-            acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fb, fa, acc[i], 0, 0, 0);
+        for (int j = 0; j < 2; ++j) {
+            if (KMAJOR) {
+                const int k = (2 * w + j) * 2 + (lane >> 5), pos = lane & 31;
+                const int c = (((pos >> 1) ^ swizzle(k)) << 1) | (pos & 1);
+                off[j] = 8 * c < rows ? (uint32_t)(k * ld + 16 * c) : kOutOfRange;
+            } else {
+                const int r = (2 * w + j) * 16 + (lane >> 2);
+                chunk = (lane & 3) ^ ((r >> 2) & 3);
+                off[j] = (uint32_t)(r * ld + 16 * chunk);
+            }
         }
     }
-    const int row = m0 + 16 * w + (lane & 15);
-    const int64_t crow = DIR == kGradWeight ? (int64_t)e * a.M + row : (int64_t)er.first + row;
+    __device__ __forceinline__ static int swizzle(int k) { return (k & 3) | (((k >> 3) & 1) << 2); }
+
+    // Step kb into stage st; steps at or past `steps` load nothing (zeros).
+    __device__ __forceinline__ void issue(int kb, int steps, int st, int w) const {
+        const uint32_t to = lds + st * kSlice + w * 2048;
+        if (KMAJOR) {
+            // a lane past the tile's columns is out of range by its offset, a row past the reduction by the size
+            const int left = min(red - kb * kStep, kStep);
+            const int size = kb < steps ? left * ld : 0;
+            const char* b = base + (int64_t)kb * kStep * ld;
+            dma16(b, size, off[0], to);
+            dma16(b, size, off[1], to + 1024);
+        } else {
+            const int size = kb < steps ? count * ld - kb * (2 * kStep) : 0;
+            const char* b = base + (int64_t)kb * (2 * kStep);
+            uint32_t o0 = off[0], o1 = off[1];
+            const int left = red - kb * kStep;
+            if (left < kStep && 8 * chunk >= left) o0 = o1 = kOutOfRange;  // the reduction's tail
+            dma16(b, size, o0, to);
+            dma16(b, size, o1, to + 1024);
+        }
+    }
+};
+
+// The tile's product with MI pieces of 16 rows for each wave, and its stores.
+template <int DIR, int MI>
+__device__ __forceinline__ void run_tile(const GroupedArgs& a, const Tile& t, uint32_t lds_a, uint32_t lds_b) {
+    constexpr bool KA = DIR == kGradWeight, KB = DIR != kForward;  // operands whose reduction runs over rows
+    const int tid = threadIdx.x, lane = tid & 63, r16 = lane & 15, g = lane >> 4;
+    const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int wm = w >> 2, wn = w & 3;
+    const int cols = min(kTile, a.N - t.n0);
+    const int red = DIR == kGradWeight ? t.er.live : a.K;
+    const int steps = (red + kStep - 1) / kStep;
+
+    Operand<KA> A;
+    Operand<KB> B;
+    if (DIR == kGradWeight) {
+        A.init(a.a + (int64_t)t.er.first * a.M, a.M, t.m0, t.rows, red, lds_a, w, lane);
+        B.init(a.b + (int64_t)t.er.first * a.N, a.N, t.n0, cols, red, lds_b, w, lane);
+    } else {
+        A.init(a.a + (int64_t)t.er.first * a.K, a.K, t.m0, t.rows, red, lds_a, w, lane);
+        B.init(a.b + (int64_t)t.e * a.N * a.K, DIR == kForward ? a.K : a.N, t.n0, cols, red, lds_b, w, lane);
+    }
+    // LDS addresses of this lane's operands in stage 0. Contiguous along k: row
+    // 16 p + r16, chunk g; piece p is 1024 p bytes on. Otherwise: k = 8 g + r16 / 4
+    // (and 4 further), values 4 (r16 % 4) of column piece p; pieces that agree
+    // in p mod 8 are 256 bytes apart.
+    uint32_t ra[4], rb[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const int col = n0 + 16 * i + 4 * (lane >> 4);
-        if (row >= rows || col >= a.N) continue;
-        if (DIR == kGradWeight && a.out_f32)
-            *(float4*)((float*)a.c + crow * a.N + col) = make_float4(acc[i][0], acc[i][1], acc[i][2], acc[i][3]);
-        else
-            *(uint2*)((uint16_t*)a.c + crow * a.N + col) =
-                make_uint2(pack_bf16x2(acc[i][0], acc[i][1]), pack_bf16x2(acc[i][2], acc[i][3]));
+        const int k = 8 * g + (r16 >> 2);
+        if (KA) ra[i] = lds_a + k * 512 + (((2 * i + wm) ^ Operand<true>::swizzle(k)) << 5) + (r16 & 3) * 8;
+        else ra[i] = lds_a + (16 * wm + r16) * 64 + ((g ^ ((r16 >> 2) & 3)) << 4);
+        if (KB) rb[i] = lds_b + k * 512 + (((4 * wn + i) ^ Operand<true>::swizzle(k)) << 5) + (r16 & 3) * 8;
+        else rb[i] = lds_b + (64 * wn + r16) * 64 + ((g ^ ((r16 >> 2) & 3)) << 4);
     }
-    // the expert's last row tile clears its padding rows
-    if (DIR != kGradWeight && a.rows.zero_pad && m0 + kBM >= er.live)
-        clear_padding((uint16_t*)a.c, a.N, er, n0, kBN);
+
+    f32x4_t acc[MI][4];
+#pragma unroll
+    for (int i = 0; i < MI; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) acc[i][j] = (f32x4_t){0.0f, 0.0f, 0.0f, 0.0f};
+
+    // Ring: step kb lives in stage kb mod kStages. In its reading half of step
+    // kb a group reads stage kb, then sends step kb + kStages - 1 into the stage of
+    // step kb - 1 (both groups have read it: the other one's reading half lies
+    // a barrier back), then waits until its own loads of step kb + 1 have
+    // landed; the other group's are waited for before a barrier that comes
+    // earlier than the first read of them.
+#pragma unroll
+    for (int kb = 0; kb < kStages - 1; ++kb) {
+        A.issue(kb, steps, kb, w);
+        B.issue(kb, steps, kb, w);
+    }
+    wait_vmcnt<(kStages - 2) * kLoads>();
+    block_barrier();
+    if (wm == 1) block_barrier();  // the second group starts half a step later
+    int st = 0;
+    for (int kb = 0; kb < steps; ++kb) {
+        bf16x8_t fa[MI], fb[4];
+        const uint32_t at = (uint32_t)(st * kSlice);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) fb[j] = KB ? read_transposed(rb[j] + at, 2048) : read_lds(rb[0] + at + 1024 * j);
+#pragma unroll
+        for (int i = 0; i < MI; ++i)
+            fa[i] = KA ? read_transposed(ra[i & 3] + at + 256 * (i >> 2), 2048) : read_lds(ra[0] + at + 2048 * i);
+        const int into = st == 0 ? kStages - 1 : st - 1;
+        A.issue(kb + kStages - 1, steps, into, w);
+        B.issue(kb + kStages - 1, steps, into, w);
+        wait_vmcnt<(kStages - 2) * kLoads>();
+        wait_lgkmcnt0();
+        block_barrier();
+        __builtin_amdgcn_s_setprio(1);
+        // operands swapped: each 16 x 16 piece comes out transposed, lane (g, r16)
+        // holding row r16 and columns 4 g .. 4 g + 3
+#pragma unroll
+        for (int i = 0; i < MI; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fb[j], fa[i], acc[i][j], 0, 0, 0);
+        __builtin_amdgcn_s_setprio(0);
+        block_barrier();
+        st = st == kStages - 1 ? 0 : st + 1;
+    }
+    if (wm == 0) block_barrier();
+    wait_vmcnt<0>();
+
+    // Epilogue: the four column pieces of a row are exchanged between the four
+    // lane groups, so that a lane holds 16 adjacent columns.
+    const int col = t.n0 + 64 * wn + 16 * g;
+#pragma unroll
+    for (int i = 0; i < MI; ++i) {
+        const int row = 16 * (2 * i + wm) + r16;
+        const bool live = row < t.rows;
+        const int64_t at = ((DIR == kGradWeight ? (int64_t)t.e * a.M : (int64_t)t.er.first) + t.m0 + row) * a.N + col;
+        if (DIR == kGradWeight && a.out_f32) {
+            uint32_t v[4][4];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                uint32_t r[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) r[j] = __float_as_uint(acc[i][j][q]);
+                transpose4(r);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) v[j][q] = r[j];
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (live && col + 4 * j < a.N)
+                    *(uint4*)((float*)a.c + at + 4 * j) = make_uint4(v[j][0], v[j][1], v[j][2], v[j][3]);
+        } else {
+            uint32_t lo[4], hi[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                lo[j] = pack_bf16x2(acc[i][j][0], acc[i][j][1]);
+                hi[j] = pack_bf16x2(acc[i][j][2], acc[i][j][3]);
+            }
+            transpose4(lo);
+            transpose4(hi);
+            if (live && col < a.N) *(uint4*)((uint16_t*)a.c + at) = make_uint4(lo[0], hi[0], lo[1], hi[1]);
+            if (live && col + 8 < a.N) *(uint4*)((uint16_t*)a.c + at + 8) = make_uint4(lo[2], hi[2], lo[3], hi[3]);
+        }
+    }
+    if (DIR != kGradWeight && a.rows.zero_pad && t.last_rows) clear_padding((uint16_t*)a.c, a.N, t.er, t.n0, kTile);
+}
+
+template <int DIR>
+__global__ __launch_bounds__(512) void k_grouped_gemm_bf16(GroupedArgs a) {
+    __shared__ __attribute__((aligned(1024))) uint8_t s_ring[2 * kStages * kSlice];
+    Tile t;
+    if (!find_tile<DIR>(a, &t)) return;
+    const uint32_t lds_a = lds_offset(s_ring), lds_b = lds_a + kStages * kSlice;
+    asm volatile("" ::"v"(s_ring) : "memory");  // the ring is written by the DMA alone
+    switch ((t.rows + 31) / 32) {
+        case 1: return run_tile<DIR, 1>(a, t, lds_a, lds_b);
+        case 2: return run_tile<DIR, 2>(a, t, lds_a, lds_b);
+        case 3: return run_tile<DIR, 3>(a, t, lds_a, lds_b);
+        case 4: return run_tile<DIR, 4>(a, t, lds_a, lds_b);
+        case 5: return run_tile<DIR, 5>(a, t, lds_a, lds_b);
+        case 6: return run_tile<DIR, 6>(a, t, lds_a, lds_b);
+        case 7: return run_tile<DIR, 7>(a, t, lds_a, lds_b);
+        default: return run_tile<DIR, 8>(a, t, lds_a, lds_b);
+    }
 }
 
 }  // namespace
 
 hipError_t launch_grouped_gemm_bf16(int dir, const GroupedArgs& a, int64_t pairs, hipStream_t stream) {
-    const int64_t nt_n = (a.N + kBN - 1) / kBN;
-    int64_t mtiles;
-    if (dir == kGradWeight)
-        mtiles = (int64_t)a.rows.E * ((a.M + kBM - 1) / kBM);
-    else
-        mtiles = max_row_tiles(a.rows, kBM, pairs);
+    const int64_t nt_n = (a.N + kTile - 1) / kTile;
+    const int64_t mtiles = dir == kGradWeight ? (int64_t)a.rows.E * ((a.M + kTile - 1) / kTile)
+                                              : max_row_tiles(a.rows, kTile, pairs);
     const int64_t blocks = mtiles * nt_n;
     if (blocks == 0) return hipSuccess;
-    if (blocks > 0xFFFFFF) return hipErrorInvalidValue;  // 2^32 threads a launch
-    if (launch_debug())
-        launch_debug_print("k_grouped_gemm_bf16", dim3((unsigned)blocks), dim3(256), "direction %d n %d", dir, a.N);
+    if (blocks > 0x7FFFFF) return hipErrorInvalidValue;  // 2^32 threads a launch
+    const dim3 grid((unsigned)blocks), block(512);
+    if (launch_debug()) launch_debug_print("k_grouped_gemm_bf16", grid, block, "direction %d n %d", dir, a.N);
     if (dir == kForward)
-        hipLaunchKernelGGL(k_grouped_gemm_bf16<kForward>, dim3((unsigned)blocks), dim3(256), 0, stream, a);
+        hipLaunchKernelGGL(k_grouped_gemm_bf16<kForward>, grid, block, 0, stream, a);
     else if (dir == kGradInput)
-        hipLaunchKernelGGL(k_grouped_gemm_bf16<kGradInput>, dim3((unsigned)blocks), dim3(256), 0, stream, a);
+        hipLaunchKernelGGL(k_grouped_gemm_bf16<kGradInput>, grid, block, 0, stream, a);
     else
-        hipLaunchKernelGGL(k_grouped_gemm_bf16<kGradWeight>, dim3((unsigned)blocks), dim3(256), 0, stream, a);
+        hipLaunchKernelGGL(k_grouped_gemm_bf16<kGradWeight>, grid, block, 0, stream, a);
     return hipGetLastError();
 }
 

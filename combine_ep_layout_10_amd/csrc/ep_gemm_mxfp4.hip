@@ -30,11 +30,11 @@ constexpr int kCols = 64;    // output columns of a block: 16 for each of 4 wave
 __global__ __launch_bounds__(256) void k_grouped_gemm_mxfp4(Mxfp4Args a) {
     const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
     const int nt_n = (a.N + kCols - 1) / kCols;
-    int e, tile;
-    if (!find_row_tile(a.rows, kTokens, (int)(blockIdx.x / nt_n), &e, &tile)) return;
+    int e, local;
+    if (!find_expert(a.rows, kTokens, nt_n, &e, &local)) return;
     const ExpertRows er = expert_rows(a.rows, e);
-    const int n0 = ((int)blockIdx.x % nt_n) * kCols + 16 * w;
-    const int m0 = tile * kTokens;
+    const int block_n0 = (local % nt_n) * kCols, n0 = block_n0 + 16 * w;
+    const int m0 = local / nt_n * kTokens;
     // lane: weight row (output column) and token lane % 16, k piece lane / 16
     const int r16 = lane & 15, g = lane >> 4;
     const int col = min(n0 + r16, a.N - 1);  // columns past N repeat the last and are not stored
@@ -55,7 +55,7 @@ __global__ __launch_bounds__(256) void k_grouped_gemm_mxfp4(Mxfp4Args a) {
         *(uint2*)(a.out + ((int64_t)er.first + m0 + r16) * a.N + c0) =
             make_uint2(pack_bf16x2(acc[0], acc[1]), pack_bf16x2(acc[2], acc[3]));
     if (a.rows.zero_pad && m0 + kTokens >= er.live)
-        clear_padding(a.out, a.N, er, ((int)blockIdx.x % nt_n) * kCols, kCols);
+        clear_padding(a.out, a.N, er, block_n0, kCols);
 }
 
 }  // namespace

@@ -1,0 +1,84 @@
+// Building blocks of the matrix kernels that feed LDS by DMA.
+#pragma once
+
+#include "ep_internal.h"
+
+namespace ep {
+
+typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
+typedef float f32x4_t __attribute__((ext_vector_type(4)));
+typedef int i32x4_t __attribute__((ext_vector_type(4)));
+
+// s_waitcnt with one counter limited (gfx9 encoding: vmcnt bits 3:0 and
+// 15:14, expcnt 6:4, lgkmcnt 11:8; the others left at their maxima).
+template <int N>
+__device__ __forceinline__ void wait_vmcnt() {
+    __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | (7 << 4) | (15 << 8));
+}
+__device__ __forceinline__ void wait_lgkmcnt0() { __builtin_amdgcn_s_waitcnt(0xC07F); }
+
+// Barrier of the block without the compiler's wait for every outstanding
+// access: the waits that a stage needs are stated where it is used. Nothing
+// is moved across it.
+__device__ __forceinline__ void block_barrier() {
+    __builtin_amdgcn_sched_barrier(0);
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_sched_barrier(0);
+}
+
+// A byte offset that is out of range of every buffer resource made here
+// (their sizes stay below 2^30): the DMA then writes zeros (checked on MI355X).
+constexpr uint32_t kOutOfRange = 0x7FFFFFF0u;
+
+// 16 bytes a lane from a buffer resource (wave-uniform base and size) at the
+// lane's byte offset, to LDS at lds + 16 * lane. Offsets at or past the size
+// read as zeros without touching memory, which is how tails and rows past an
+// expert's last are cut off. Inline assembly, because for the intrinsic the
+// compiler waits for all outstanding DMA before any LDS read; the waits are
+// explicit here. m0 goes in as an operand (the asm never writes it); the s_nop
+// is the wait state an m0 write needs before a DMA reads it.
+__device__ __forceinline__ void dma16(const void* base, int size, uint32_t off, uint32_t lds) {
+    const uint64_t b = (uint64_t)(uintptr_t)base;
+    const i32x4_t r = {__builtin_amdgcn_readfirstlane((int)(uint32_t)b),
+                       __builtin_amdgcn_readfirstlane((int)(uint32_t)(b >> 32)), __builtin_amdgcn_readfirstlane(size),
+                       kBufferFlags};
+    asm volatile("s_nop 0\n\tbuffer_load_dwordx4 %0, %1, 0 offen lds" ::"v"(off), "s"(r), "{m0}"(lds) : "memory");
+}
+
+__device__ __forceinline__ uint32_t lds_offset(const void* p) { return (uint32_t)(uintptr_t)p; }
+
+// Transposing LDS read (16 lanes share a 4 x 16 block of 16-bit values): lane
+// i of a group of 16 passes the address of 4 consecutive values of row i / 4
+// and gets column i of the block, rows 0 to 3 (checked on MI355X).
+typedef short i16x4_t __attribute__((ext_vector_type(4)));
+typedef __attribute__((address_space(3))) i16x4_t lds_i16x4_t;
+
+__device__ __forceinline__ bf16x8_t read_transposed(uint32_t lds, int second) {
+    struct {
+        i16x4_t lo, hi;
+    } v;
+    v.lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4_t*)lds);
+    v.hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4_t*)(lds + second));
+    return __builtin_bit_cast(bf16x8_t, v);
+}
+
+typedef __attribute__((address_space(3))) bf16x8_t lds_bf16x8_t;
+__device__ __forceinline__ bf16x8_t read_lds(uint32_t lds) { return *(const lds_bf16x8_t*)lds; }
+
+// Transposes 4 x 4 words between four registers and the four groups of 16
+// lanes: afterwards register a of group g holds what register g of group a did.
+__device__ __forceinline__ void transpose4(uint32_t r[4]) {
+    typedef unsigned int u32x2_t __attribute__((ext_vector_type(2)));
+    const u32x2_t x02 = __builtin_amdgcn_permlane32_swap(r[0], r[2], false, false);
+    const u32x2_t x13 = __builtin_amdgcn_permlane32_swap(r[1], r[3], false, false);
+    const u32x2_t y01 = __builtin_amdgcn_permlane16_swap(x02[0], x13[0], false, false);
+    const u32x2_t y23 = __builtin_amdgcn_permlane16_swap(x02[1], x13[1], false, false);
+    r[0] = y01[0];
+    r[1] = y01[1];
+    r[2] = y23[0];
+    r[3] = y23[1];
+}
+
+}  // namespace ep

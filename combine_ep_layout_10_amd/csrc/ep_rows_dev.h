@@ -26,26 +26,54 @@ __device__ __forceinline__ ExpertRows expert_rows(const RowsArgs& a, int e) {
     return r;
 }
 
-// Row tile m of the whole layout: its expert and its index within the expert,
-// experts in order, each with ceil(live / bm) tiles. Every wave finds it by
-// itself (64 experts at a time, one a lane, prefix sums over the wave), so no
-// barrier and no table in memory is needed. Returns false past the last tile.
-__device__ __forceinline__ bool find_row_tile(const RowsArgs& a, int bm, int m, int* expert, int* tile) {
+// Logical block of this block among `total` that have work: each XCD gets a
+// contiguous range (block b runs on XCD b mod 8 as its (b / 8)-th), so that
+// neighbours share operands in one XCD's L2.
+__device__ __forceinline__ int logical_block(int total) {
+    constexpr int kXcds = 8;
+    const int q = total / kXcds, r = total % kXcds;
+    const int xcd = (int)blockIdx.x % kXcds, idx = (int)blockIdx.x / kXcds;
+    return (xcd < r ? xcd * (q + 1) : r * (q + 1) + (xcd - r) * q) + idx;
+}
+
+// Blocks are numbered expert by expert: an expert with c live rows has
+// ceil(c / bm) * per of them. Finds this block's expert and its number within
+// the expert (both wave-uniform); false when it has no work. The counts are
+// known only on the device, so every wave finds its place by itself (64
+// experts at a time, one a lane, prefix sums over the wave): no barrier and
+// no table in memory.
+__device__ __forceinline__ bool find_expert(const RowsArgs& a, int bm, int per, int* expert, int* local) {
+    constexpr int kChunks = kMaxExperts / kWave;
     const int lane = lane_id();
-    int before = 0;
-    for (int e0 = 0; e0 < a.E; e0 += kWave) {
-        const int e = e0 + lane;
-        int n = 0;
-        if (e < a.E) n = ((a.mode == EP_MODE_COMPACT ? a.cnt[e] : a.pad[e]) + bm - 1) / bm;
-        const int upto = before + wave_inclusive_scan(n);
-        const uint64_t past = ballot64(upto > m);
+    const int32_t* count = a.mode == EP_MODE_COMPACT ? a.cnt : a.pad;  // FIXED: min(cnt, C)
+    int upto[kChunks], own[kChunks];  // row tiles up to and with this lane's expert, and its own
+#pragma unroll
+    for (int c = 0; c < kChunks; ++c) {
+        own[c] = 0;
+        if (c * kWave >= a.E) break;
+        const int e = c * kWave + lane;
+        if (e < a.E) own[c] = (count[e] + bm - 1) / bm;
+    }
+    int sum = 0;
+#pragma unroll
+    for (int c = 0; c < kChunks; ++c) {
+        if (c * kWave >= a.E) break;
+        upto[c] = sum + wave_inclusive_scan(own[c]);
+        sum = __builtin_amdgcn_readlane(upto[c], kWave - 1);
+    }
+    const int total = sum * per;
+    if ((int)blockIdx.x >= total) return false;
+    const int L = logical_block(total), m = L / per;
+#pragma unroll
+    for (int c = 0; c < kChunks; ++c) {
+        if (c * kWave >= a.E) break;
+        const uint64_t past = ballot64(upto[c] > m);
         if (past != 0) {
             const int l = __builtin_ctzll(past);
-            *expert = e0 + l;
-            *tile = m - __builtin_amdgcn_readlane(upto - n, l);
+            *expert = c * kWave + l;
+            *local = L - __builtin_amdgcn_readlane(upto[c] - own[c], l) * per;
             return true;
         }
-        before = __builtin_amdgcn_readlane(upto, kWave - 1);
     }
     return false;
 }
