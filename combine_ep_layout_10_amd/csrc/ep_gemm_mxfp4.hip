@@ -18,8 +18,8 @@
 // slices of KC values of k, two slices deep; 16-byte chunk c of row r is stored at
 // c ^ (r mod 16), so that 16 rows read at one chunk hit all 64 banks once.
 // S splits the reduction over the waves of a block, so that a small problem
-// still reaches every CU: wave group ks takes chunks ks, ks + S, ... and the S
-// sums are added in order at the end.
+// still reaches every CU: wave group ks takes the ks-th part of every slice, and
+// the S sums are added in order at the end.
 #include "ep_mma_dev.h"
 #include "ep_rows_dev.h"
 
@@ -41,11 +41,10 @@ __device__ __forceinline__ bf16x8_t decode_mxfp4(uint32_t word, float scale) {
     return (bf16x8_t){p0[0], p0[1], p1[0], p1[1], p2[0], p2[1], p3[0], p3[1]};
 }
 
-template <int TB>
-constexpr int slice_k() { return TB <= 32 ? 1024 : 512; }
-
-template <int TB>
-constexpr int lds_bytes() { return 2 * TB * slice_k<TB>() * 2; }
+// k values of a slice of rows: 8 chunks for a wave of 16 columns, 4 (so as many
+// loads) for one of 32.
+template <int MC>
+constexpr int slice_k() { return MC == 1 ? 1024 : 512; }
 
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t resource(const void* p, int size) {
     return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), 0, size, kBufferFlags);
@@ -55,9 +54,10 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t resource(const void* p, int si
 template <int TB, int MC, int S, int NT>
 __device__ __forceinline__ void run_tile(const Mxfp4Args& a, const ExpertRows& er, int e, int m0, int rows, int n0,
                                          uint8_t* s_x) {
-    constexpr int KC = slice_k<TB>(), NC = KC / 128;   // chunks of a slice
+    constexpr int KC = slice_k<MC>(), NC = KC / 128;   // chunks of a slice
     constexpr int B = NC / S;                          // chunks of a slice that one wave takes
     constexpr int P = kInFlight > B * MC ? kInFlight / (B * MC) : 1;  // slices whose weights are in registers
+    constexpr int R = P > 1 ? P : 2;  // slices whose scales are in registers
     constexpr int XL = NT * 16 * KC * 2 / 16 / (64 * kWaves);          // 16-byte loads a thread for a slice of rows
     const int tid = threadIdx.x, lane = tid & 63, r16 = lane & 15, g = lane >> 4;
     const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -70,20 +70,37 @@ __device__ __forceinline__ void run_tile(const Mxfp4Args& a, const ExpertRows& e
     const int cols = max(0, min(16 * MC, a.N - c0));
     const int64_t wrow = (int64_t)e * a.N + min(c0, a.N - 1);
     const __amdgpu_buffer_rsrc_t rb = resource(a.b + wrow * (a.K / 2), cols * (a.K / 2));
-    const __amdgpu_buffer_rsrc_t rs = resource(a.b_scales + wrow * groups, cols * groups);
+    const uint8_t* ws = a.b_scales + wrow * groups;
     const __amdgpu_buffer_rsrc_t rx = resource(a.x + ((int64_t)er.first + m0) * a.K, rows * a.K * 2);
 
+    // Codes: chunk b of this wave's B in slice kc. Scales: the 4 B bytes a column
+    // that go with them, as words (word b: chunk b, byte g: group g). A byte
+    // load for each chunk would cost as many requests as the codes do (313
+    // against 220 us at 128 tokens x top-8, 64 experts, 4096 x 7168).
     u32x4_t code[P][B][MC];
-    uint32_t scale[P][B][MC];
+    uint32_t scale[R][B][MC];
     auto load = [&](int kc, int p, int b) {
-        const int group = (kc * NC + b * S + ks) * 4 + g;
+        const int group = (kc * NC + ks * B + b) * 4 + g;
+#pragma unroll
+        for (int c = 0; c < MC; ++c)
+            code[p][b][c] = __builtin_amdgcn_raw_buffer_load_b128(
+                rb, group < groups ? (16 * c + r16) * (a.K / 2) + 16 * group : kOutOfRange, 0, 0);
+    };
+    auto load_scales = [&](int kc, int p) {
+        if (kc >= slices) return;
+        const int first = (kc * NC + ks * B) * 4;
 #pragma unroll
         for (int c = 0; c < MC; ++c) {
-            const bool in = group < groups;
-            code[p][b][c] =
-                __builtin_amdgcn_raw_buffer_load_b128(rb, in ? (16 * c + r16) * (a.K / 2) + 16 * group : kOutOfRange, 0, 0);
-            scale[p][b][c] =
-                __builtin_amdgcn_raw_buffer_load_b8(rs, in ? (16 * c + r16) * groups + group : kOutOfRange, 0, 0);
+            const uint8_t* s = ws + (int64_t)min(16 * c + r16, max(cols - 1, 0)) * groups + first;
+            if ((kc + 1) * KC <= a.K) {
+                __builtin_memcpy(&scale[p][0][c], s, 4);  // any alignment
+#pragma unroll
+                for (int b = 1; b < B; ++b) __builtin_memcpy(&scale[p][b][c], s + 4 * b, 4);
+            } else {  // the last slice may end inside a word
+#pragma unroll
+                for (int b = 0; b < B; ++b)
+                    scale[p][b][c] = first + 4 * b + g < groups ? (uint32_t)s[4 * b + g] << (8 * g) : 0u;
+            }
         }
     };
     u32x4_t xr[XL];
@@ -104,9 +121,11 @@ __device__ __forceinline__ void run_tile(const Mxfp4Args& a, const ExpertRows& e
 
     load_rows(0);
 #pragma unroll
-    for (int p = 0; p < P; ++p)
+    for (int p = 0; p < P; ++p) {
+        load_scales(p, p);
 #pragma unroll
         for (int b = 0; b < B; ++b) load(p, p, b);
+    }
     f32x4_t acc[NT][MC];
 #pragma unroll
     for (int n = 0; n < NT; ++n)
@@ -116,24 +135,28 @@ __device__ __forceinline__ void run_tile(const Mxfp4Args& a, const ExpertRows& e
     wait_lgkmcnt0();
     block_barrier();
 
-    for (int kc0 = 0; kc0 < slices; kc0 += P) {
+    for (int kc0 = 0; kc0 < slices; kc0 += R) {
 #pragma unroll
-        for (int p = 0; p < P; ++p) {
-            const int kc = kc0 + p;
+        for (int r = 0; r < R; ++r) {
+            const int kc = kc0 + r, p = r % P;
             if (kc >= slices) break;
             // the next slice of rows travels while this one is used; its stage
             // was last read a barrier ago
             if (kc + 1 < slices) load_rows(kc + 1);
+            if (P == 1) load_scales(kc + 1, (r + 1) % R);
             const uint8_t* x = s_x + (kc & 1) * (TB * KC * 2) + r16 * (KC * 2);
 #pragma unroll
             for (int b = 0; b < B; ++b) {
-                const int sub = b * S + ks;
+                const int sub = ks * B + b;
+                uint32_t power[MC];
+#pragma unroll
+                for (int c = 0; c < MC; ++c) power[c] = __builtin_amdgcn_ubfe(scale[r][b][c], 8 * g, 8) << 23;
 #pragma unroll
                 for (int t = 0; t < 4; ++t) {
                     bf16x8_t f[MC];
 #pragma unroll
                     for (int c = 0; c < MC; ++c)
-                        f[c] = decode_mxfp4(code[p][b][c][t], __uint_as_float(scale[p][b][c] << 23));
+                        f[c] = decode_mxfp4(code[p][b][c][t], __uint_as_float(power[c]));
 #pragma unroll
                     for (int n = 0; n < NT; ++n) {
                         const bf16x8_t v =
@@ -145,6 +168,7 @@ __device__ __forceinline__ void run_tile(const Mxfp4Args& a, const ExpertRows& e
                 }
                 load(kc + P, p, b);
             }
+            if (P > 1) load_scales(kc + P, r);
             if (kc + 1 < slices) store_rows((kc + 1) & 1);
             wait_lgkmcnt0();
             block_barrier();
@@ -185,7 +209,7 @@ __device__ __forceinline__ void run_tile(const Mxfp4Args& a, const ExpertRows& e
 template <int TB, int MC, int S>
 __global__ __launch_bounds__(64 * kWaves) void k_grouped_gemm_mxfp4(Mxfp4Args a) {
     constexpr int kCols = 16 * MC * kWaves / S;
-    __shared__ __attribute__((aligned(16))) uint8_t s_x[lds_bytes<TB>()];
+    __shared__ __attribute__((aligned(16))) uint8_t s_x[2 * TB * slice_k<MC>() * 2];
     const int nt_n = (a.N + kCols - 1) / kCols;
     int e, local;
     if (!find_expert(a.rows, TB, nt_n, &e, &local)) return;
@@ -227,15 +251,18 @@ hipError_t launch_grouped_gemm_mxfp4(const Mxfp4Args& a, int64_t pairs, hipStrea
     // read once (an expert's rows scatter around their mean).
     const int64_t experts = pairs < a.rows.E ? pairs : a.rows.E;
     const int64_t mean = (pairs + a.rows.E - 1) / a.rows.E;
-    // Column pieces of 16 for each of the 256 CUs: the reduction is split until
-    // each has about 16 waves. Never by the device's real CU count: the order of
-    // the sums must not depend on it.
+    // The reduction is split while that leaves about one block a CU (256 of 8
+    // waves), and only where every part keeps 512 of k. One token x 4096 x 7168 on
+    // 8, 4, 2, 1 experts: split 1, 2, 4, 8 take 27.5, 16.1, 12.3, 10.5 us, the next
+    // smaller split -, 19.2, 14.5, 11.4 us, the next larger 32.3, 18.1, 16.1 us.
+    // Never by the device's real CU count: the order of the sums must not depend on it.
     const int64_t waves = experts * ((a.N + 15) / 16);
-    const int split = waves >= 4096 ? 1 : waves >= 2048 ? 2 : waves >= 1024 ? 4 : 8;
+    int split = waves >= 1536 ? 1 : waves >= 768 ? 2 : waves >= 384 ? 4 : 8;
+    while (split > 1 && a.K < 512 * split) split /= 2;
     if (mean > 20) return launch<64, 2, 1>(a, pairs, stream);
     if (mean > 6) {
         switch (split) {
-            case 1: return launch<32, 1, 1>(a, pairs, stream);
+            case 1: return launch<32, 2, 1>(a, pairs, stream);
             case 2: return launch<32, 1, 2>(a, pairs, stream);
             case 4: return launch<32, 1, 4>(a, pairs, stream);
             default: return launch<32, 1, 8>(a, pairs, stream);

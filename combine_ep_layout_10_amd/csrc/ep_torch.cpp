@@ -12,15 +12,19 @@
 #include <initializer_list>
 #include <stdexcept>
 #include <string>
+#include <tuple>
 
 #include "../../include/ep.h"
 
 namespace {
 
+// A failed call raises the package's EPError (a RuntimeError with the status).
 void ok(ep_status s, const char* where) {
-    if (s != EP_OK)
-        throw std::runtime_error(std::string(where) + " failed: " + ep_status_string(s) + ": " +
-                                 ep_last_error_message());
+    if (s == EP_OK) return;
+    const std::string message = ep_last_error_message();
+    py::object error = py::module_::import("combine_ep_layout_10_amd._ffi").attr("EPError");
+    PyErr_SetObject(error.ptr(), error((int)s, where, message).ptr());
+    throw py::error_already_set();
 }
 
 // Device pointer of a contiguous tensor of dtype dt on device dev.
@@ -66,6 +70,12 @@ int64_t rows_bound(const ep_config* c) {
 }
 
 at::ScalarType idx_type(const ep_config* c) { return c->idx_bits == 64 ? at::kLong : at::kInt; }
+
+// A tensor's size as the C ABI's int32_t.
+int32_t width(int64_t n) {
+    if (n > INT32_MAX) throw std::invalid_argument("a size of " + std::to_string(n) + " exceeds 2^31 - 1");
+    return (int32_t)n;
+}
 
 void* stream_of(int64_t s) { return reinterpret_cast<void*>(s); }
 
@@ -186,6 +196,144 @@ void dispatch_backward(int64_t handle, const at::Tensor& grad_recv, const c10::o
     combine_like(handle, grad_recv, c10::nullopt, grad_x, grad_row_w, grad_topk_w, true, stream, dev);
 }
 
+// ---------------------------------------------------------------- experts' products and norm
+
+// `out` when given (checked), otherwise a new tensor on `like`'s device.
+at::Tensor output(const c10::optional<at::Tensor>& out, std::initializer_list<int64_t> want, at::ScalarType dt,
+                  const at::Tensor& like, const char* name) {
+    if (!out.has_value()) return at::empty(at::IntArrayRef(want.begin(), want.size()), like.options().dtype(dt));
+    shape(*out, want, name);
+    return *out;
+}
+
+void experts_first(const at::Tensor& b, int64_t E, const char* what) {
+    if (b.dim() != 3 || b.size(0) != E) throw std::invalid_argument(std::string("b must be ") + what);
+}
+
+at::Tensor grouped_gemm_bf16(int64_t handle, const at::Tensor& a, const at::Tensor& b,
+                             const c10::optional<at::Tensor>& out, int64_t stream, int64_t dev) {
+    const ep_handle* h = handle_of(handle);
+    const int64_t R = rows_bound(&h->cfg);
+    experts_first(b, h->cfg.num_experts, "[E, n, k]");
+    const int64_t n = b.size(1), k = b.size(2);
+    shape(a, {R, k}, "a");
+    const void *pa = ptr(a, "a", at::kBFloat16, dev), *pb = ptr(b, "b", at::kBFloat16, dev);
+    at::Tensor o = output(out, {R, n}, at::kBFloat16, a, "out");
+    ok(ep_grouped_gemm_bf16(h, pa, pb, width(n), width(k), ptr(o, "out", at::kBFloat16, dev), stream_of(stream)),
+       "ep_grouped_gemm_bf16");
+    return o;
+}
+
+at::Tensor grouped_gemm_bf16_grad_input(int64_t handle, const at::Tensor& grad_out, const at::Tensor& b,
+                                        const c10::optional<at::Tensor>& grad_a, int64_t stream, int64_t dev) {
+    const ep_handle* h = handle_of(handle);
+    const int64_t R = rows_bound(&h->cfg);
+    experts_first(b, h->cfg.num_experts, "[E, n, k]");
+    const int64_t n = b.size(1), k = b.size(2);
+    shape(grad_out, {R, n}, "grad_out");
+    const void *pg = ptr(grad_out, "grad_out", at::kBFloat16, dev), *pb = ptr(b, "b", at::kBFloat16, dev);
+    at::Tensor o = output(grad_a, {R, k}, at::kBFloat16, grad_out, "grad_a");
+    ok(ep_grouped_gemm_bf16_grad_input(h, pg, pb, width(n), width(k), ptr(o, "grad_a", at::kBFloat16, dev),
+                                       stream_of(stream)),
+       "ep_grouped_gemm_bf16_grad_input");
+    return o;
+}
+
+at::Tensor grouped_gemm_bf16_grad_weight(int64_t handle, const at::Tensor& grad_out, const at::Tensor& a,
+                                         const c10::optional<at::Tensor>& grad_b, int64_t stream, int64_t dev) {
+    const ep_handle* h = handle_of(handle);
+    const int64_t R = rows_bound(&h->cfg), E = h->cfg.num_experts;
+    if (grad_out.dim() != 2 || a.dim() != 2)
+        throw std::invalid_argument("grad_out must be [rows bound, n] and a [rows bound, k]");
+    const int64_t n = grad_out.size(1), k = a.size(1);
+    shape(grad_out, {R, n}, "grad_out");
+    shape(a, {R, k}, "a");
+    const void *pg = ptr(grad_out, "grad_out", at::kBFloat16, dev), *pa = ptr(a, "a", at::kBFloat16, dev);
+    const bool f32 = !grad_b.has_value() || grad_b->scalar_type() != at::kBFloat16;
+    const at::ScalarType dt = f32 ? at::kFloat : at::kBFloat16;
+    at::Tensor o = output(grad_b, {E, n, k}, dt, grad_out, "grad_b");
+    ok(ep_grouped_gemm_bf16_grad_weight(h, pg, pa, width(n), width(k), f32 ? 1 : 0, ptr(o, "grad_b", dt, dev),
+                                        stream_of(stream)),
+       "ep_grouped_gemm_bf16_grad_weight");
+    return o;
+}
+
+at::Tensor grouped_gemm_mxfp4(int64_t handle, const at::Tensor& a, const at::Tensor& b, const at::Tensor& b_scales,
+                              const c10::optional<at::Tensor>& out, int64_t stream, int64_t dev) {
+    const ep_handle* h = handle_of(handle);
+    const int64_t R = rows_bound(&h->cfg), E = h->cfg.num_experts;
+    experts_first(b, E, "[E, n, k / 2]");
+    const int64_t n = b.size(1), k = 2 * b.size(2);
+    shape(a, {R, k}, "a");
+    shape(b_scales, {E, n, k / 32}, "b_scales");
+    const void *pa = ptr(a, "a", at::kBFloat16, dev), *pb = ptr(b, "b", at::kByte, dev);
+    const void* ps = ptr(b_scales, "b_scales", at::kByte, dev);
+    at::Tensor o = output(out, {R, n}, at::kBFloat16, a, "out");
+    ok(ep_grouped_gemm_mxfp4(h, pa, pb, ps, width(n), width(k), ptr(o, "out", at::kBFloat16, dev), stream_of(stream)),
+       "ep_grouped_gemm_mxfp4");
+    return o;
+}
+
+std::tuple<at::Tensor, c10::optional<at::Tensor>, at::Tensor, at::Tensor> rms_norm(
+    const at::Tensor& x, const at::Tensor& weight, double eps, const c10::optional<at::Tensor>& residual, int64_t dtype,
+    const c10::optional<at::Tensor>& total, const c10::optional<at::Tensor>& y,
+    const c10::optional<at::Tensor>& y_scales, const c10::optional<at::Tensor>& rstd, int64_t stream, int64_t dev) {
+    if (x.dim() != 2) throw std::invalid_argument("x must be [T, H]");
+    const int64_t T = x.size(0), H = x.size(1);
+    const bool fp8 = dtype == EP_FP8_QUANTIZE;
+    shape(weight, {H}, "weight");
+    opt_shape(residual, {T, H}, "residual");
+    if (!residual.has_value() && total.has_value())
+        throw std::invalid_argument("total is written only with a residual");
+    if (!fp8 && y_scales.has_value()) throw std::invalid_argument("y_scales is written only for an FP8 output");
+    const void *px = ptr(x, "x", at::kBFloat16, dev), *pw = ptr(weight, "weight", at::kBFloat16, dev);
+    const void* pr = opt_ptr(residual, "residual", at::kBFloat16, dev);
+    const at::ScalarType yt = fp8 ? at::kByte : at::kBFloat16;
+    at::Tensor t = residual.has_value() ? output(total, {T, H}, at::kBFloat16, x, "total") : x;
+    at::Tensor o = output(y, {T, H}, yt, x, "y");
+    at::Tensor r = output(rstd, {T}, at::kFloat, x, "rstd");
+    c10::optional<at::Tensor> s;
+    if (fp8) s = output(y_scales, {T, H / 128}, at::kFloat, x, "y_scales");
+    ok(ep_rms_norm(width(T), width(H), (int32_t)dtype, px, pr, pw, (float)eps,
+                   residual.has_value() ? ptr(t, "total", at::kBFloat16, dev) : nullptr, ptr(o, "y", yt, dev),
+                   (float*)opt_ptr(s, "y_scales", at::kFloat, dev), (float*)ptr(r, "rstd", at::kFloat, dev),
+                   stream_of(stream)),
+       "ep_rms_norm");
+    return {o, s, t, r};
+}
+
+std::tuple<at::Tensor, at::Tensor> rms_norm_backward(
+    const at::Tensor& total, const at::Tensor& weight, const at::Tensor& rstd, const at::Tensor& grad_y,
+    const c10::optional<at::Tensor>& grad_total, const c10::optional<at::Tensor>& grad_x,
+    const c10::optional<at::Tensor>& grad_weight, const c10::optional<at::Tensor>& workspace, int64_t stream,
+    int64_t dev) {
+    if (total.dim() != 2) throw std::invalid_argument("total must be [T, H]");
+    const int64_t T = total.size(0), H = total.size(1);
+    shape(weight, {H}, "weight");
+    shape(rstd, {T}, "rstd");
+    shape(grad_y, {T, H}, "grad_y");
+    opt_shape(grad_total, {T, H}, "grad_total");
+    const void *ps = ptr(total, "total", at::kBFloat16, dev), *pw = ptr(weight, "weight", at::kBFloat16, dev);
+    const void *pg = ptr(grad_y, "grad_y", at::kBFloat16, dev);
+    const float* pr = (const float*)ptr(rstd, "rstd", at::kFloat, dev);
+    const void* pt = opt_ptr(grad_total, "grad_total", at::kBFloat16, dev);
+    at::Tensor gx = output(grad_x, {T, H}, at::kBFloat16, total, "grad_x");
+    at::Tensor gw = output(grad_weight, {H}, at::kFloat, total, "grad_weight");
+    at::Tensor ws;
+    if (workspace.has_value()) {
+        ws = *workspace;
+    } else {
+        const size_t need = ep_rms_norm_workspace_bytes(width(T), width(H));
+        if (need == 0) ok(EP_ERR_INVALID_ARG, "ep_rms_norm_workspace_bytes");
+        ws = at::empty({(int64_t)need}, total.options().dtype(at::kByte));
+    }
+    ok(ep_rms_norm_backward(width(T), width(H), ps, pw, pr, pg, pt, ptr(gx, "grad_x", at::kBFloat16, dev),
+                            (float*)ptr(gw, "grad_weight", at::kFloat, dev), ptr(ws, "workspace", at::kByte, dev),
+                            (size_t)ws.numel(), stream_of(stream)),
+       "ep_rms_norm_backward");
+    return {gx, gw};
+}
+
 }  // namespace
 
 PYBIND11_MODULE(TORCH_EXTENSION_NAME, m) {
@@ -196,4 +344,10 @@ PYBIND11_MODULE(TORCH_EXTENSION_NAME, m) {
     m.def("combine_backward", &combine_backward);
     m.def("combine", &combine);
     m.def("dispatch_backward", &dispatch_backward);
+    m.def("grouped_gemm_bf16", &grouped_gemm_bf16);
+    m.def("grouped_gemm_bf16_grad_input", &grouped_gemm_bf16_grad_input);
+    m.def("grouped_gemm_bf16_grad_weight", &grouped_gemm_bf16_grad_weight);
+    m.def("grouped_gemm_mxfp4", &grouped_gemm_mxfp4);
+    m.def("rms_norm", &rms_norm);
+    m.def("rms_norm_backward", &rms_norm_backward);
 }

@@ -369,45 +369,21 @@ def grouped_gemm_fp8(h: Handle, a: torch.Tensor, a_scales: torch.Tensor, b: torc
     return out
 
 
-def _product_out(out: Optional[torch.Tensor], shape, dtype, device, name: str) -> torch.Tensor:
-    if out is None:
-        return torch.empty(shape, dtype=dtype, device=device)
-    _need(out, shape, name)
-    return out
-
-
 def grouped_gemm_bf16(h: Handle, a: torch.Tensor, b: torch.Tensor, out: Optional[torch.Tensor] = None) -> torch.Tensor:
     """BF16 products grouped by expert over the receive layout, any alignment:
     out [rows bound, n], rows of expert e times b[e] [n, k]. Padding rows of
     out are zero-filled (unless FLAG_NO_ZERO_PAD); rows past the layout are
     not written."""
-    R, E = h.cfg.recv_rows_bound(), h.cfg.num_experts
-    if b.dim() != 3 or b.shape[0] != E:
-        raise ValueError("b must be [E, n, k]")
-    n, k = b.shape[1], b.shape[2]
-    _need(a, (R, k), "a")
-    out = _product_out(out, (R, n), torch.bfloat16, a.device, "out")
     cur = _current_device()
-    F.ep_grouped_gemm_bf16(h.c, _dev(a, "a", torch.bfloat16, cur), _dev(b, "b", torch.bfloat16, cur), n, k,
-                           _dev(out, "out", torch.bfloat16, cur), _raw_stream(cur))
-    return out
+    return _B.grouped_gemm_bf16(ctypes.addressof(h.c), a, b, out, _raw_stream(cur), cur)
 
 
 def grouped_gemm_bf16_grad_input(h: Handle, grad_out: torch.Tensor, b: torch.Tensor,
                                  grad_a: Optional[torch.Tensor] = None) -> torch.Tensor:
     """Gradient of grouped_gemm_bf16 with respect to a: grad_a [rows bound, k],
     rows of grad_out [rows bound, n] times b[e] [n, k]."""
-    R, E = h.cfg.recv_rows_bound(), h.cfg.num_experts
-    if b.dim() != 3 or b.shape[0] != E:
-        raise ValueError("b must be [E, n, k]")
-    n, k = b.shape[1], b.shape[2]
-    _need(grad_out, (R, n), "grad_out")
-    grad_a = _product_out(grad_a, (R, k), torch.bfloat16, grad_out.device, "grad_a")
     cur = _current_device()
-    F.ep_grouped_gemm_bf16_grad_input(h.c, _dev(grad_out, "grad_out", torch.bfloat16, cur),
-                                      _dev(b, "b", torch.bfloat16, cur), n, k,
-                                      _dev(grad_a, "grad_a", torch.bfloat16, cur), _raw_stream(cur))
-    return grad_a
+    return _B.grouped_gemm_bf16_grad_input(ctypes.addressof(h.c), grad_out, b, grad_a, _raw_stream(cur), cur)
 
 
 def grouped_gemm_bf16_grad_weight(h: Handle, grad_out: torch.Tensor, a: torch.Tensor,
@@ -415,19 +391,8 @@ def grouped_gemm_bf16_grad_weight(h: Handle, grad_out: torch.Tensor, a: torch.Te
     """Gradient of grouped_gemm_bf16 with respect to b: grad_b [E, n, k], the
     sum over each expert's rows of grad_out[r, :] x a[r, :]; float32 unless a
     bfloat16 grad_b is given. Experts without a row get zeros."""
-    R, E = h.cfg.recv_rows_bound(), h.cfg.num_experts
-    if grad_out.dim() != 2 or a.dim() != 2:
-        raise ValueError("grad_out must be [rows bound, n] and a [rows bound, k]")
-    n, k = grad_out.shape[1], a.shape[1]
-    _need(grad_out, (R, n), "grad_out")
-    _need(a, (R, k), "a")
-    grad_b = _product_out(grad_b, (E, n, k), torch.float32, grad_out.device, "grad_b")
     cur = _current_device()
-    p = _dev(grad_b, "grad_b", (torch.float32, torch.bfloat16), cur)
-    F.ep_grouped_gemm_bf16_grad_weight(h.c, _dev(grad_out, "grad_out", torch.bfloat16, cur),
-                                       _dev(a, "a", torch.bfloat16, cur), n, k, int(grad_b.dtype is torch.float32), p,
-                                       _raw_stream(cur))
-    return grad_b
+    return _B.grouped_gemm_bf16_grad_weight(ctypes.addressof(h.c), grad_out, a, grad_b, _raw_stream(cur), cur)
 
 
 def grouped_gemm_mxfp4(h: Handle, a: torch.Tensor, b: torch.Tensor, b_scales: torch.Tensor,
@@ -435,18 +400,8 @@ def grouped_gemm_mxfp4(h: Handle, a: torch.Tensor, b: torch.Tensor, b_scales: to
     """grouped_gemm_bf16 with MXFP4 weights: b uint8 [E, n, k / 2] holds two
     E2M1 codes a byte (low nibble first), b_scales uint8 [E, n, k / 32] their
     E8M0 scales."""
-    R, E = h.cfg.recv_rows_bound(), h.cfg.num_experts
-    if b.dim() != 3 or b.shape[0] != E:
-        raise ValueError("b must be [E, n, k / 2]")
-    n, k = b.shape[1], 2 * b.shape[2]
-    _need(a, (R, k), "a")
-    _need(b_scales, (E, n, k // 32), "b_scales")
-    out = _product_out(out, (R, n), torch.bfloat16, a.device, "out")
     cur = _current_device()
-    F.ep_grouped_gemm_mxfp4(h.c, _dev(a, "a", torch.bfloat16, cur), _dev(b, "b", torch.uint8, cur),
-                            _dev(b_scales, "b_scales", torch.uint8, cur), n, k,
-                            _dev(out, "out", torch.bfloat16, cur), _raw_stream(cur))
-    return out
+    return _B.grouped_gemm_mxfp4(ctypes.addressof(h.c), a, b, b_scales, out, _raw_stream(cur), cur)
 
 
 # ---------------------------------------------------------------- RMS norm
@@ -457,30 +412,12 @@ def rms_norm(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6, residual:
     """RMS norm of x (+ residual). Returns (y, y_scales, total, rstd): y [T, H]
     bf16 (y_scales None), or with dtype FP8_QUANTIZE the codes (uint8) and
     their 1x128 scales, which dispatch takes with FP8_PREQUANT; total, the
-    bf16 sum that was normalised (x itself without a residual), into x's or
-    residual's own buffer when given as `total`; rstd [T], for the backward."""
-    if x.dim() != 2:
-        raise ValueError("x must be [T, H]")
-    T, H = x.shape
-    fp8 = dtype == FP8_QUANTIZE
-    _need(weight, (H,), "weight")
-    _need(residual, (T, H), "residual")
-    if residual is None:
-        if total is not None:
-            raise ValueError("total is written only with a residual")
-    else:
-        total = _product_out(total, (T, H), torch.bfloat16, x.device, "total")
-    y = _product_out(y, (T, H), torch.uint8 if fp8 else torch.bfloat16, x.device, "y")
-    if fp8:
-        y_scales = _product_out(y_scales, (T, H // 128), torch.float32, x.device, "y_scales")
-    rstd = _product_out(rstd, (T,), torch.float32, x.device, "rstd")
+    bf16 sum that was normalised (x itself without a residual), written into
+    `total` when given, which may be x or residual; rstd [T], for the backward."""
     cur = _current_device()
-    F.ep_rms_norm(T, H, dtype, _dev(x, "x", torch.bfloat16, cur), _opt(residual, "residual", torch.bfloat16, cur),
-                  _dev(weight, "weight", torch.bfloat16, cur), eps, _opt(total, "total", torch.bfloat16, cur),
-                  _dev(y, "y", torch.uint8 if fp8 else torch.bfloat16, cur),
-                  _opt(y_scales, "y_scales", torch.float32, cur), _dev(rstd, "rstd", torch.float32, cur),
-                  _raw_stream(cur))
-    return y, y_scales, (x if total is None else total), rstd
+    y, y_scales, total, rstd = _B.rms_norm(x, weight, eps, residual, dtype, total, y, y_scales, rstd, _raw_stream(cur),
+                                           cur)
+    return y, y_scales, (x if residual is None else total), rstd
 
 
 def rms_norm_workspace(num_tokens: int, hidden: int, device="cuda") -> torch.Tensor:
@@ -497,25 +434,9 @@ def rms_norm_backward(total: torch.Tensor, weight: torch.Tensor, rstd: torch.Ten
     """Backward of rms_norm: (grad_x [T, H] bf16, grad_weight [H] float32).
     grad_x is the gradient of x and of residual; grad_total is the gradient
     that reaches total by other ways than y (grad_x may be its own buffer)."""
-    if total.dim() != 2:
-        raise ValueError("total must be [T, H]")
-    T, H = total.shape
-    _need(weight, (H,), "weight")
-    _need(rstd, (T,), "rstd")
-    _need(grad_y, (T, H), "grad_y")
-    _need(grad_total, (T, H), "grad_total")
-    grad_x = _product_out(grad_x, (T, H), torch.bfloat16, total.device, "grad_x")
-    grad_weight = _product_out(grad_weight, (H,), torch.float32, total.device, "grad_weight")
-    if workspace is None:
-        workspace = rms_norm_workspace(T, H, total.device)
     cur = _current_device()
-    F.ep_rms_norm_backward(T, H, _dev(total, "total", torch.bfloat16, cur), _dev(weight, "weight", torch.bfloat16, cur),
-                           _dev(rstd, "rstd", torch.float32, cur), _dev(grad_y, "grad_y", torch.bfloat16, cur),
-                           _opt(grad_total, "grad_total", torch.bfloat16, cur),
-                           _dev(grad_x, "grad_x", torch.bfloat16, cur),
-                           _dev(grad_weight, "grad_weight", torch.float32, cur),
-                           _dev(workspace, "workspace", torch.uint8, cur), workspace.numel(), _raw_stream(cur))
-    return grad_x, grad_weight
+    return _B.rms_norm_backward(total, weight, rstd, grad_y, grad_total, grad_x, grad_weight, workspace,
+                                _raw_stream(cur), cur)
 
 # ---------------------------------------------------------------- bound calls
 

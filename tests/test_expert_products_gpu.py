@@ -320,6 +320,19 @@ def test_mxfp4_top_scale():
     assert torch.equal(got, lv.to(torch.bfloat16).double())
 
 
+@pytest.mark.parametrize("rows", [1, 9, 40])
+@pytest.mark.parametrize("n,k", [(72, 4128), (520, 2080), (1000, 1056), (2056, 1024), (264, 8192)])
+def test_mxfp4_long_reductions(rows, n, k):
+    """One to many rows an expert, reductions that are split over more and
+    fewer parts and end inside a slice, scales at an odd address."""
+    h = make_handle(routing([rows, 0, rows + 2, 1, 3 * rows]), 5, 1)
+    o = operands("mxfp4", h, n, k, seed=rows + k)
+    odd = torch.empty(o["s"].numel() + 1, dtype=torch.uint8, device="cuda")[1:].view(o["s"].shape)
+    o["s"] = odd.copy_(o["s"])
+    out = torch.full((h.cfg.recv_rows_bound(), n), 7.0, dtype=torch.bfloat16, device="cuda")
+    verify("mxfp4", h, o, call("mxfp4", h, o, out), n, k)
+
+
 def test_gradients_are_differences():
     """Integer operands small enough that every product and sum is exact in
     bf16: the change of <out, g> along a direction equals the gradient's inner
