@@ -32,8 +32,8 @@
 //
 // LDS: a slice of an operand that is contiguous along the reduction is
 // [256 rows][32 k] (64-byte rows); its 16-byte chunk c of row r is stored at
-// c ^ (r / 4 mod 4), so that 16 rows read at one chunk hit all 64 banks once. The
-// other operands are [32 k][256 columns] (512-byte rows) and are read through
+// c ^ row_swizzle16(r), which spreads the 16 lanes that a 16-byte read serves at a
+// time over all 64 banks. The other operands are [32 k][256 columns] (512-byte rows) and are read through
 // the transposing LDS read, 4 k by 16 columns; their 32-byte pair of chunks p of
 // row k is stored at p ^ f(k), f(k) = k mod 4 + 4 (k / 8 mod 2), which spreads the
 // 8 rows that 32 lanes read over the banks.
@@ -129,7 +129,7 @@ struct Operand {
                 off[j] = 8 * c < rows ? (uint32_t)(k * ld + 16 * c) : kOutOfRange;
             } else {
                 const int r = (2 * w + j) * 16 + (lane >> 2);
-                chunk = (lane & 3) ^ ((r >> 2) & 3);
+                chunk = (lane & 3) ^ row_swizzle16(r);
                 off[j] = (uint32_t)(r * ld + 16 * chunk);
             }
         }
@@ -187,9 +187,9 @@ __device__ __forceinline__ void run_tile(const GroupedArgs& a, const Tile& t, ui
     for (int i = 0; i < 4; ++i) {
         const int k = 8 * g + (r16 >> 2);
         if (KA) ra[i] = lds_a + k * 512 + (((2 * i + wm) ^ Operand<true>::swizzle(k)) << 5) + (r16 & 3) * 8;
-        else ra[i] = lds_a + (16 * wm + r16) * 64 + ((g ^ ((r16 >> 2) & 3)) << 4);
+        else ra[i] = lds_a + (16 * wm + r16) * 64 + ((g ^ row_swizzle16(r16)) << 4);
         if (KB) rb[i] = lds_b + k * 512 + (((4 * wn + i) ^ Operand<true>::swizzle(k)) << 5) + (r16 & 3) * 8;
-        else rb[i] = lds_b + (64 * wn + r16) * 64 + ((g ^ ((r16 >> 2) & 3)) << 4);
+        else rb[i] = lds_b + (64 * wn + r16) * 64 + ((g ^ row_swizzle16(r16)) << 4);
     }
 
     f32x4_t acc[MI][4];

@@ -16,7 +16,7 @@
 // operand of MFMA t, whose k are then 32 g + 8 t .. + 7. The rows (the second
 // operand, read in the same order of k) are shared by the block through LDS in
 // slices of KC values of k, two slices deep; 16-byte chunk c of row r is stored at
-// c ^ (r mod 16), so that 16 rows read at one chunk hit all 64 banks once.
+// c ^ row_slot(r), which meets each bank once in every read.
 // S splits the reduction over the waves of a block, so that a small problem
 // still reaches every CU: wave group ks takes the ks-th part of every slice, and
 // the S sums are added in order at the end.
@@ -31,6 +31,8 @@ typedef __bf16 bf16x2_v __attribute__((ext_vector_type(2)));
 
 constexpr int kWaves = 8;
 constexpr int kInFlight = 8;  // weight loads a wave keeps in flight
+
+__device__ __forceinline__ int row_slot(int r) { return (row_swizzle16(r) << 2) | (r & 3); }
 
 // The 8 codes of one word (lowest nibble first) times 2^(e8m0 - 127).
 __device__ __forceinline__ bf16x8_t decode_mxfp4(uint32_t word, float scale) {
@@ -115,7 +117,7 @@ __device__ __forceinline__ void run_tile(const Mxfp4Args& a, const ExpertRows& e
 #pragma unroll
         for (int j = 0; j < XL; ++j) {
             const int q = j * 64 * kWaves + tid, row = q / (KC / 8), c = q % (KC / 8);
-            *(u32x4_t*)(s_x + stage * (TB * KC * 2) + row * (KC * 2) + ((c ^ (row & 15)) << 4)) = xr[j];
+            *(u32x4_t*)(s_x + stage * (TB * KC * 2) + row * (KC * 2) + ((c ^ row_slot(row)) << 4)) = xr[j];
         }
     };
 
@@ -160,7 +162,7 @@ __device__ __forceinline__ void run_tile(const Mxfp4Args& a, const ExpertRows& e
 #pragma unroll
                     for (int n = 0; n < NT; ++n) {
                         const bf16x8_t v =
-                            *(const bf16x8_t*)(x + n * (16 * KC * 2) + sub * 256 + (((4 * g + t) ^ r16) << 4));
+                            *(const bf16x8_t*)(x + n * (16 * KC * 2) + sub * 256 + (((4 * g + t) ^ row_slot(r16)) << 4));
 #pragma unroll
                         for (int c = 0; c < MC; ++c)
                             acc[n][c] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(f[c], v, acc[n][c], 0, 0, 0);

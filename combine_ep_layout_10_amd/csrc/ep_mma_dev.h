@@ -64,6 +64,13 @@ __device__ __forceinline__ bf16x8_t read_transposed(uint32_t lds, int second) {
     return __builtin_bit_cast(bf16x8_t, v);
 }
 
+// Swizzle of 16-byte LDS reads by the operand lanes of a 16 x 16 MFMA (lane
+// (g, r): row r, chunk g). Such a read serves 16 lanes at a time, not in order:
+// rows 0-3 and 12-15 of one g together with rows 4-11 of the next (and the
+// reverse), so a chunk index XORed with -(r / 4) mod 4 meets each bank once;
+// with r / 4 mod 4, half of the LDS cycles were conflicts (SQ_LDS_BANK_CONFLICT).
+__device__ __forceinline__ int row_swizzle16(int r) { return -(r >> 2) & 3; }
+
 typedef __attribute__((address_space(3))) bf16x8_t lds_bf16x8_t;
 __device__ __forceinline__ bf16x8_t read_lds(uint32_t lds) { return *(const lds_bf16x8_t*)lds; }
 
