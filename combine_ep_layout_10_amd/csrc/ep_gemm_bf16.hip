@@ -15,9 +15,9 @@
 //
 // One kernel for the three: a block of 8 waves computes a tile of 256 x 256,
 // wave (wm, wn) the 16-row pieces 2 i + wm of it by the columns 64 wn .. + 63,
-// with v_mfma_f32_16x16x32_bf16. The reduction runs in steps of 32: both
-// operands' slices (16 KiB each) move from memory to LDS by DMA, into a ring of
-// kStages. All tails (rows, columns, reduction) are the buffer resource's range
+// with v_mfma_f32_16x16x32_bf16. The reduction runs in steps of 64: both
+// operands' slices (32 KiB each) move from memory to LDS by DMA, into a ring of
+// five. All tails (rows, columns, reduction) are the buffer resource's range
 // check, which fills zeros.
 //
 // Rows: an expert's rows are cut into ceil(rows / 256) tiles of equal size
@@ -26,17 +26,17 @@
 // with 6 rows a single piece instead of a whole tile.
 //
 // Schedule: the waves form two groups (wm), half a step apart: while one
-// group's MFMAs run, the other reads its operands from LDS and issues DMA,
-// then a barrier exchanges the roles. Each SIMD holds one wave of either group,
-// so its matrix unit always has work.
+// group's MFMAs run, the other reads its operands from LDS, then a barrier
+// exchanges the roles. Each SIMD holds one wave of either group, so its matrix
+// unit always has work.
 //
 // LDS: a slice of an operand that is contiguous along the reduction is
-// [256 rows][32 k] (64-byte rows); its 16-byte chunk c of row r is stored at
-// c ^ row_swizzle16(r), which spreads the 16 lanes that a 16-byte read serves at a
-// time over all 64 banks. The other operands are [32 k][256 columns] (512-byte rows) and are read through
-// the transposing LDS read, 4 k by 16 columns; their 32-byte pair of chunks p of
-// row k is stored at p ^ f(k), f(k) = k mod 4 + 4 (k / 8 mod 2), which spreads the
-// 8 rows that 32 lanes read over the banks.
+// [256 rows][64 k] (128-byte rows, whole cache lines in memory); its 16-byte
+// chunk c of row r is stored at c ^ (r / 2 mod 8). The other operands are
+// [64 k][256 columns] (512-byte rows) and are read through the transposing LDS
+// read, 4 k by 16 columns; their 32-byte pair of chunks p of row k is stored at
+// p ^ f(k), f(k) = k mod 4 + 4 (k / 8 mod 2). Either way a read meets each bank
+// once (SQ_LDS_BANK_CONFLICT 0).
 #include "ep_mma_dev.h"
 #include "ep_rows_dev.h"
 
@@ -45,10 +45,10 @@ namespace ep {
 namespace {
 
 constexpr int kTile = 256;
-constexpr int kStep = 32;                    // reduction of one stage
-constexpr int kStages = 4;
-constexpr int kSlice = kTile * kStep * 2;    // bytes of one operand's slice
-constexpr int kLoads = 4;                    // DMA loads of a wave for a stage: two of A, two of B
+constexpr int kStep = 64;                  // reduction of one step
+constexpr int kSlots = 5;                  // slices in LDS: A and B of step 0, of step 1, ... in turn
+constexpr int kSlice = kTile * kStep * 2;  // bytes of one operand's slice
+constexpr int kLoads = 4;                  // DMA loads of a wave for a slice
 constexpr int kGroupRows = 8;                // row tiles that share column tiles in the block order
 
 struct Tile {
@@ -60,14 +60,15 @@ struct Tile {
 };
 
 // Tile of logical block `local` among an expert's nt_m x nt_n: groups of
-// kGroupRows row tiles, within a group column by column, so that blocks that
+// about kGroupRows row tiles, within a group column by column, so that blocks that
 // run together on an XCD share few operand tiles.
 __device__ __forceinline__ void order_tiles(int local, int nt_m, int nt_n, int* m, int* n) {
-    const int g = local / (kGroupRows * nt_n);
-    const int in_group = min(kGroupRows, nt_m - g * kGroupRows);
-    const int rem = local - g * kGroupRows * nt_n;
+    const int groups = max(1, (nt_m + kGroupRows / 2) / kGroupRows), size = (nt_m + groups - 1) / groups;
+    const int g = local / (size * nt_n);
+    const int in_group = min(size, nt_m - g * size);
+    const int rem = local - g * size * nt_n;
     *n = rem / in_group;
-    *m = g * kGroupRows + rem % in_group;
+    *m = g * size + rem % in_group;
 }
 
 template <int DIR>
@@ -110,57 +111,53 @@ struct Operand {
     const char* base;  // of the tile, reduction step 0
     int ld;            // bytes between rows
     int count, red;
-    uint32_t lds;      // this operand's ring
-    uint32_t off[2];   // byte offsets of this lane's two loads
-    int chunk;         // KMAJOR false: chunk (8 values of k) this lane loads
+    uint32_t off[kLoads];  // byte offsets of this lane's loads
+    int chunk[2];          // KMAJOR false: chunk (8 values of k) of this lane's even and odd loads
 
     __device__ __forceinline__ void init(const uint16_t* src, int64_t ld_values, int r0, int rows, int reduction,
-                                         uint32_t ring, int w, int lane) {
+                                         int w, int lane) {
         ld = (int)(2 * ld_values);
         count = rows;
         red = reduction;
-        lds = ring;
         base = (const char*)src + (KMAJOR ? 2 * (int64_t)r0 : (int64_t)r0 * ld);
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
+        for (int j = 0; j < kLoads; ++j) {
             if (KMAJOR) {
-                const int k = (2 * w + j) * 2 + (lane >> 5), pos = lane & 31;
+                const int k = (kLoads * w + j) * 2 + (lane >> 5), pos = lane & 31;
                 const int c = (((pos >> 1) ^ swizzle(k)) << 1) | (pos & 1);
                 off[j] = 8 * c < rows ? (uint32_t)(k * ld + 16 * c) : kOutOfRange;
             } else {
-                const int r = (2 * w + j) * 16 + (lane >> 2);
-                chunk = (lane & 3) ^ row_swizzle16(r);
-                off[j] = (uint32_t)(r * ld + 16 * chunk);
+                const int r = (kLoads * w + j) * 8 + (lane >> 3);
+                chunk[j & 1] = (lane & 7) ^ ((r >> 1) & 7);
+                off[j] = (uint32_t)(r * ld + 16 * chunk[j & 1]);
             }
         }
     }
     __device__ __forceinline__ static int swizzle(int k) { return (k & 3) | (((k >> 3) & 1) << 2); }
 
-    // Step kb into stage st; steps at or past `steps` load nothing (zeros).
-    __device__ __forceinline__ void issue(int kb, int steps, int st, int w) const {
-        const uint32_t to = lds + st * kSlice + w * 2048;
+    // Step kb's slice to LDS at `to`; steps at or past `steps` load nothing (zeros).
+    __device__ __forceinline__ void issue(int kb, int steps, uint32_t to, int w) const {
+        const int left = red - kb * kStep;
+        to += w * (kLoads * 1024);
         if (KMAJOR) {
             // a lane past the tile's columns is out of range by its offset, a row past the reduction by the size
-            const int left = min(red - kb * kStep, kStep);
-            const int size = kb < steps ? left * ld : 0;
+            const int size = kb < steps ? min(left, kStep) * ld : 0;
             const char* b = base + (int64_t)kb * kStep * ld;
-            dma16(b, size, off[0], to);
-            dma16(b, size, off[1], to + 1024);
+#pragma unroll
+            for (int j = 0; j < kLoads; ++j) dma16(b, size, off[j], to + 1024 * j);
         } else {
             const int size = kb < steps ? count * ld - kb * (2 * kStep) : 0;
             const char* b = base + (int64_t)kb * (2 * kStep);
-            uint32_t o0 = off[0], o1 = off[1];
-            const int left = red - kb * kStep;
-            if (left < kStep && 8 * chunk >= left) o0 = o1 = kOutOfRange;  // the reduction's tail
-            dma16(b, size, o0, to);
-            dma16(b, size, o1, to + 1024);
+#pragma unroll
+            for (int j = 0; j < kLoads; ++j)  // the second case: the reduction's tail
+                dma16(b, size, left >= kStep || 8 * chunk[j & 1] < left ? off[j] : kOutOfRange, to + 1024 * j);
         }
     }
 };
 
 // The tile's product with MI pieces of 16 rows for each wave, and its stores.
 template <int DIR, int MI>
-__device__ __forceinline__ void run_tile(const GroupedArgs& a, const Tile& t, uint32_t lds_a, uint32_t lds_b) {
+__device__ __forceinline__ void run_tile(const GroupedArgs& a, const Tile& t, uint32_t lds) {
     constexpr bool KA = DIR == kGradWeight, KB = DIR != kForward;  // operands whose reduction runs over rows
     const int tid = threadIdx.x, lane = tid & 63, r16 = lane & 15, g = lane >> 4;
     const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -172,24 +169,25 @@ __device__ __forceinline__ void run_tile(const GroupedArgs& a, const Tile& t, ui
     Operand<KA> A;
     Operand<KB> B;
     if (DIR == kGradWeight) {
-        A.init(a.a + (int64_t)t.er.first * a.M, a.M, t.m0, t.rows, red, lds_a, w, lane);
-        B.init(a.b + (int64_t)t.er.first * a.N, a.N, t.n0, cols, red, lds_b, w, lane);
+        A.init(a.a + (int64_t)t.er.first * a.M, a.M, t.m0, t.rows, red, w, lane);
+        B.init(a.b + (int64_t)t.er.first * a.N, a.N, t.n0, cols, red, w, lane);
     } else {
-        A.init(a.a + (int64_t)t.er.first * a.K, a.K, t.m0, t.rows, red, lds_a, w, lane);
-        B.init(a.b + (int64_t)t.e * a.N * a.K, DIR == kForward ? a.K : a.N, t.n0, cols, red, lds_b, w, lane);
+        A.init(a.a + (int64_t)t.er.first * a.K, a.K, t.m0, t.rows, red, w, lane);
+        B.init(a.b + (int64_t)t.e * a.N * a.K, DIR == kForward ? a.K : a.N, t.n0, cols, red, w, lane);
     }
-    // LDS addresses of this lane's operands in stage 0. Contiguous along k: row
-    // 16 p + r16, chunk g; piece p is 1024 p bytes on. Otherwise: k = 8 g + r16 / 4
-    // (and 4 further), values 4 (r16 % 4) of column piece p; pieces that agree
-    // in p mod 8 are 256 bytes apart.
+    // Addresses of this lane's operands within a slice, first half of the step.
+    // Contiguous along k: row 16 p + r16, chunk g (4 further in the second half);
+    // piece p is 2048 p bytes on. Otherwise: k = 8 g + r16 / 4 (and 4 further; 32
+    // in the second half), values 4 (r16 % 4) of column piece p; pieces that
+    // agree in p mod 8 are 256 bytes apart.
     uint32_t ra[4], rb[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const int k = 8 * g + (r16 >> 2);
-        if (KA) ra[i] = lds_a + k * 512 + (((2 * i + wm) ^ Operand<true>::swizzle(k)) << 5) + (r16 & 3) * 8;
-        else ra[i] = lds_a + (16 * wm + r16) * 64 + ((g ^ row_swizzle16(r16)) << 4);
-        if (KB) rb[i] = lds_b + k * 512 + (((4 * wn + i) ^ Operand<true>::swizzle(k)) << 5) + (r16 & 3) * 8;
-        else rb[i] = lds_b + (64 * wn + r16) * 64 + ((g ^ row_swizzle16(r16)) << 4);
+        if (KA) ra[i] = k * 512 + (((2 * i + wm) ^ Operand<true>::swizzle(k)) << 5) + (r16 & 3) * 8;
+        else ra[i] = (16 * wm + r16) * 128 + (((4 * (i & 1) + g) ^ ((r16 >> 1) & 7)) << 4);
+        if (KB) rb[i] = k * 512 + (((4 * wn + i) ^ Operand<true>::swizzle(k)) << 5) + (r16 & 3) * 8;
+        else rb[i] = (64 * wn + r16) * 128 + (((4 * (i & 1) + g) ^ ((r16 >> 1) & 7)) << 4);
     }
 
     f32x4_t acc[MI][4];
@@ -198,45 +196,65 @@ __device__ __forceinline__ void run_tile(const GroupedArgs& a, const Tile& t, ui
 #pragma unroll
         for (int j = 0; j < 4; ++j) acc[i][j] = (f32x4_t){0.0f, 0.0f, 0.0f, 0.0f};
 
-    // Ring: step kb lives in stage kb mod kStages. In its reading half of step
-    // kb a group reads stage kb, then sends step kb + kStages - 1 into the stage of
-    // step kb - 1 (both groups have read it: the other one's reading half lies
-    // a barrier back), then waits until its own loads of step kb + 1 have
-    // landed; the other group's are waited for before a barrier that comes
-    // earlier than the first read of them.
-#pragma unroll
-    for (int kb = 0; kb < kStages - 1; ++kb) {
-        A.issue(kb, steps, kb, w);
-        B.issue(kb, steps, kb, w);
-    }
-    wait_vmcnt<(kStages - 2) * kLoads>();
+    // Ring: slice q (A of step q / 2 when even, B when odd) lives in slot q mod 5.
+    // In interval 2 kb group 0 reads step kb while group 1 computes step kb - 1; in
+    // the next one the roles are exchanged. Step kb - 1 has been read by both when
+    // interval 2 kb begins, so its two slots take slices 2 kb + 3 and 2 kb + 4 then:
+    // all 8 waves send them (group 0 behind its LDS reads, group 1 before its
+    // MFMAs). Slice 2 kb + 3 is needed when interval 2 kb + 2 begins: every wave waits
+    // for its part of it before the barrier that ends interval 2 kb + 1.
+    const auto slot = [&](int q) { return lds + (uint32_t)(q % kSlots) * kSlice; };
+    A.issue(0, steps, slot(0), w);
+    B.issue(0, steps, slot(1), w);
+    A.issue(1, steps, slot(2), w);
+    wait_vmcnt<kLoads>();
     block_barrier();
-    if (wm == 1) block_barrier();  // the second group starts half a step later
-    int st = 0;
+    if (wm == 1) {
+        B.issue(1, steps, slot(3), w);
+        A.issue(2, steps, slot(4), w);
+        block_barrier();
+    }
+    int qa = 0;  // slot of A of step kb
     for (int kb = 0; kb < steps; ++kb) {
-        bf16x8_t fa[MI], fb[4];
-        const uint32_t at = (uint32_t)(st * kSlice);
+        const auto wrap = [](int q) { return q >= kSlots ? q - kSlots : q; };
+        const uint32_t at_a = lds + (uint32_t)qa * kSlice, at_b = lds + (uint32_t)wrap(qa + 1) * kSlice;
+        bf16x8_t fa[2][MI], fb[2][4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) fb[j] = KB ? read_transposed(rb[j] + at, 2048) : read_lds(rb[0] + at + 1024 * j);
+        for (int h = 0; h < 2; ++h) {
 #pragma unroll
-        for (int i = 0; i < MI; ++i)
-            fa[i] = KA ? read_transposed(ra[i & 3] + at + 256 * (i >> 2), 2048) : read_lds(ra[0] + at + 2048 * i);
-        const int into = st == 0 ? kStages - 1 : st - 1;
-        A.issue(kb + kStages - 1, steps, into, w);
-        B.issue(kb + kStages - 1, steps, into, w);
-        wait_vmcnt<(kStages - 2) * kLoads>();
+            for (int j = 0; j < 4; ++j)
+                fb[h][j] = KB ? read_transposed(at_b + rb[j] + 16384 * h, 2048) : read_lds(at_b + rb[h] + 2048 * j);
+#pragma unroll
+            for (int i = 0; i < MI; ++i)
+                fa[h][i] = KA ? read_transposed(at_a + ra[i & 3] + 256 * (i >> 2) + 16384 * h, 2048)
+                              : read_lds(at_a + ra[h] + 4096 * i);
+        }
+        if (wm == 0) {
+            B.issue(kb + 1, steps, lds + (uint32_t)wrap(qa + 3) * kSlice, w);
+            A.issue(kb + 2, steps, lds + (uint32_t)wrap(qa + 4) * kSlice, w);
+        } else {
+            wait_vmcnt<kLoads>();
+        }
         wait_lgkmcnt0();
         block_barrier();
+        qa = wrap(qa + 2);
+        if (wm == 1) {
+            B.issue(kb + 2, steps, lds + (uint32_t)wrap(qa + 3) * kSlice, w);
+            A.issue(kb + 3, steps, lds + (uint32_t)wrap(qa + 4) * kSlice, w);
+        }
         __builtin_amdgcn_s_setprio(1);
         // operands swapped: each 16 x 16 piece comes out transposed, lane (g, r16)
         // holding row r16 and columns 4 g .. 4 g + 3
 #pragma unroll
-        for (int i = 0; i < MI; ++i)
+        for (int h = 0; h < 2; ++h)
 #pragma unroll
-            for (int j = 0; j < 4; ++j) acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fb[j], fa[i], acc[i][j], 0, 0, 0);
+            for (int i = 0; i < MI; ++i)
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fb[h][j], fa[h][i], acc[i][j], 0, 0, 0);
         __builtin_amdgcn_s_setprio(0);
+        if (wm == 0) wait_vmcnt<kLoads>();
         block_barrier();
-        st = st == kStages - 1 ? 0 : st + 1;
     }
     if (wm == 0) block_barrier();
     wait_vmcnt<0>();
@@ -282,20 +300,20 @@ __device__ __forceinline__ void run_tile(const GroupedArgs& a, const Tile& t, ui
 
 template <int DIR>
 __global__ __launch_bounds__(512) void k_grouped_gemm_bf16(GroupedArgs a) {
-    __shared__ __attribute__((aligned(1024))) uint8_t s_ring[2 * kStages * kSlice];
+    __shared__ __attribute__((aligned(1024))) uint8_t s_ring[kSlots * kSlice];
     Tile t;
     if (!find_tile<DIR>(a, &t)) return;
-    const uint32_t lds_a = lds_offset(s_ring), lds_b = lds_a + kStages * kSlice;
+    const uint32_t lds = lds_offset(s_ring);
     asm volatile("" ::"v"(s_ring) : "memory");  // the ring is written by the DMA alone
     switch ((t.rows + 31) / 32) {
-        case 1: return run_tile<DIR, 1>(a, t, lds_a, lds_b);
-        case 2: return run_tile<DIR, 2>(a, t, lds_a, lds_b);
-        case 3: return run_tile<DIR, 3>(a, t, lds_a, lds_b);
-        case 4: return run_tile<DIR, 4>(a, t, lds_a, lds_b);
-        case 5: return run_tile<DIR, 5>(a, t, lds_a, lds_b);
-        case 6: return run_tile<DIR, 6>(a, t, lds_a, lds_b);
-        case 7: return run_tile<DIR, 7>(a, t, lds_a, lds_b);
-        default: return run_tile<DIR, 8>(a, t, lds_a, lds_b);
+        case 1: return run_tile<DIR, 1>(a, t, lds);
+        case 2: return run_tile<DIR, 2>(a, t, lds);
+        case 3: return run_tile<DIR, 3>(a, t, lds);
+        case 4: return run_tile<DIR, 4>(a, t, lds);
+        case 5: return run_tile<DIR, 5>(a, t, lds);
+        case 6: return run_tile<DIR, 6>(a, t, lds);
+        case 7: return run_tile<DIR, 7>(a, t, lds);
+        default: return run_tile<DIR, 8>(a, t, lds);
     }
 }
 
