@@ -40,22 +40,20 @@
 #include "ep_mma_dev.h"
 #include "ep_rows_dev.h"
 
+#include <type_traits>
+
 namespace ep {
 
 namespace {
 
-constexpr int kTile = 256;
-constexpr int kStep = 64;                  // reduction of one step
-constexpr int kSlots = 5;                  // slices in LDS: A and B of step 0, of step 1, ... in turn
-constexpr int kSlice = kTile * kStep * 2;  // bytes of one operand's slice
-constexpr int kLoads = 4;                  // DMA loads of a wave for a slice
+constexpr int kTile = 256;  // rows of a tile
 constexpr int kGroupRows = 8;                // row tiles that share column tiles in the block order
 
 struct Tile {
-    int e;           // expert
-    int m0, n0;      // first row (of the expert's) and column
-    int rows;        // rows of the tile that exist
-    bool last_rows;  // the expert's last row tile
+    int e;          // expert
+    int m0, n0;     // first row (of the expert's) and column
+    int rows;       // rows of the tile that exist
+    int last_rows;  // whether it is the expert's last row tile
     ExpertRows er;
 };
 
@@ -71,9 +69,10 @@ __device__ __forceinline__ void order_tiles(int local, int nt_m, int nt_n, int* 
     *m = g * size + rem % in_group;
 }
 
-template <int DIR>
+// This block's tile of kTile rows by COLS columns; false when it has none.
+template <int DIR, int COLS>
 __device__ __forceinline__ bool find_tile(const GroupedArgs& a, Tile* t) {
-    const int nt_n = (a.N + kTile - 1) / kTile;
+    const int nt_n = (a.N + COLS - 1) / COLS;
     int m, n;
     if (DIR == kGradWeight) {
         const int nt_m = (a.M + kTile - 1) / kTile;
@@ -83,7 +82,7 @@ __device__ __forceinline__ bool find_tile(const GroupedArgs& a, Tile* t) {
         t->er = expert_rows(a.rows, t->e);
         t->m0 = m * kTile;
         t->rows = min(kTile, a.M - t->m0);
-        t->last_rows = false;
+        t->last_rows = 0;
     } else {
         int local;
         if (!find_expert(a.rows, kTile, nt_n, &t->e, &local)) return false;
@@ -95,101 +94,177 @@ __device__ __forceinline__ bool find_tile(const GroupedArgs& a, Tile* t) {
         t->rows = min(each, live - t->m0);
         t->last_rows = m == nt_m - 1;
     }
-    t->n0 = n * kTile;
+    t->n0 = n * COLS;
     t->m0 = __builtin_amdgcn_readfirstlane(t->m0);
     t->n0 = __builtin_amdgcn_readfirstlane(t->n0);
     t->rows = __builtin_amdgcn_readfirstlane(t->rows);
     return true;
 }
 
-// One operand's way from memory to LDS and to the MFMAs. KMAJOR: the reduction
-// runs over the rows in memory (element (r, k) at base[k * ld + r]), otherwise
-// along them (base[r * ld + k]). `count`: rows of the tile that exist; `red`:
-// length of the reduction.
-template <bool KMAJOR>
+// One operand's way from memory to LDS and to the MFMAs: slices of WIDTH rows
+// (or columns) by STEP of the reduction, moved by WAVES waves. KMAJOR: the
+// reduction runs over the rows in memory (element (r, k) at base[k * ld + r]),
+// otherwise along them (base[r * ld + k]). `count`: rows of the tile that exist;
+// `red`: length of the reduction.
+template <bool KMAJOR, int STEP, int WIDTH, int WAVES>
 struct Operand {
-    const char* base;  // of the tile, reduction step 0
-    int ld;            // bytes between rows
+    static constexpr int kSlice = STEP * WIDTH * 2;            // bytes
+    static constexpr int kLoads = kSlice / 1024 / WAVES;       // DMA loads of a wave
+    static constexpr int kRow = 2 * (KMAJOR ? WIDTH : STEP);   // bytes of a row in LDS
+    static constexpr int kPiece = KMAJOR ? 0 : 16 * kRow;      // from a piece of 16 rows to the next
+
+    const char* base;      // of the tile, reduction step 0
+    int ld;                // bytes between rows
     int count, red;
     uint32_t off[kLoads];  // byte offsets of this lane's loads
     int chunk[2];          // KMAJOR false: chunk (8 values of k) of this lane's even and odd loads
+    uint32_t at[KMAJOR ? 1 : 2];  // this lane's first operand within a slice (KMAJOR false: of either half)
 
+    // first: the wave's first piece of 16 rows
     __device__ __forceinline__ void init(const uint16_t* src, int64_t ld_values, int r0, int rows, int reduction,
-                                         int w, int lane) {
+                                         int w, int first) {
+        const int lane = lane_id(), r16 = lane & 15, g = lane >> 4;
         ld = (int)(2 * ld_values);
         count = rows;
         red = reduction;
         base = (const char*)src + (KMAJOR ? 2 * (int64_t)r0 : (int64_t)r0 * ld);
 #pragma unroll
         for (int j = 0; j < kLoads; ++j) {
+            const int byte = (kLoads * w + j) * 1024 + 16 * lane, r = byte / kRow, pos = byte % kRow / 16;
             if (KMAJOR) {
-                const int k = (kLoads * w + j) * 2 + (lane >> 5), pos = lane & 31;
-                const int c = (((pos >> 1) ^ swizzle(k)) << 1) | (pos & 1);
-                off[j] = 8 * c < rows ? (uint32_t)(k * ld + 16 * c) : kOutOfRange;
+                const int c = (((pos >> 1) ^ pair_swizzle(r)) << 1) | (pos & 1);
+                off[j] = 8 * c < rows ? __umul24(r, ld) + 16 * c : kOutOfRange;
             } else {
-                const int r = (kLoads * w + j) * 8 + (lane >> 3);
-                chunk[j & 1] = (lane & 7) ^ ((r >> 1) & 7);
-                off[j] = (uint32_t)(r * ld + 16 * chunk[j & 1]);
+                chunk[j & 1] = pos ^ chunk_swizzle(r);
+                off[j] = __umul24(r, ld) + 16 * chunk[j & 1];
             }
         }
-    }
-    __device__ __forceinline__ static int swizzle(int k) { return (k & 3) | (((k >> 3) & 1) << 2); }
-
-    // Step kb's slice to LDS at `to`; steps at or past `steps` load nothing (zeros).
-    __device__ __forceinline__ void issue(int kb, int steps, uint32_t to, int w) const {
-        const int left = red - kb * kStep;
-        to += w * (kLoads * 1024);
         if (KMAJOR) {
-            // a lane past the tile's columns is out of range by its offset, a row past the reduction by the size
-            const int size = kb < steps ? min(left, kStep) * ld : 0;
-            const char* b = base + (int64_t)kb * kStep * ld;
-#pragma unroll
-            for (int j = 0; j < kLoads; ++j) dma16(b, size, off[j], to + 1024 * j);
+            // k = 8 g + r16 / 4 (and 4 further), values 4 (r16 % 4) of the piece
+            const int k = 8 * g + (r16 >> 2);
+            at[0] = k * kRow + ((first ^ pair_swizzle(k)) << 5) + (r16 & 3) * 8;
         } else {
-            const int size = kb < steps ? count * ld - kb * (2 * kStep) : 0;
-            const char* b = base + (int64_t)kb * (2 * kStep);
+            // row r16 of the first piece, chunk g (of the step's second half: 4 further)
 #pragma unroll
-            for (int j = 0; j < kLoads; ++j)  // the second case: the reduction's tail
-                dma16(b, size, left >= kStep || 8 * chunk[j & 1] < left ? off[j] : kOutOfRange, to + 1024 * j);
+            for (int h = 0; h < 2; ++h)
+                at[h] = first * kPiece + r16 * kRow + (((4 * h + g) ^ chunk_swizzle(r16)) << 4);
         }
     }
+    __device__ __forceinline__ static int pair_swizzle(int k) { return (k & 3) | (((k >> 3) & 1) << 2); }
+    __device__ __forceinline__ static int chunk_swizzle(int r) { return STEP == 64 ? (r >> 1) & 7 : row_swizzle16(r); }
+
+    // Load j of step kb's slice to LDS at `to`; steps at or past `steps` load nothing (zeros).
+    __device__ __forceinline__ void issue(int kb, int steps, uint32_t to, int w, int j) const {
+        const int left = red - kb * STEP;
+        to += (w * kLoads + j) * 1024;
+        if (KMAJOR)  // a lane past the tile's columns is out of range by its offset, a row past the reduction by the size
+            dma16(base + (int64_t)kb * STEP * ld, kb < steps ? min(left, STEP) * ld : 0, off[j], to);
+        else  // the third case: the reduction's tail
+            dma16(base + (int64_t)kb * (2 * STEP), kb < steps ? count * ld - kb * (2 * STEP) : 0,
+                  left >= STEP || 8 * chunk[j & 1] < left ? off[j] : kOutOfRange, to);
+    }
+    __device__ __forceinline__ void issue(int kb, int steps, uint32_t to, int w) const {
+#pragma unroll
+        for (int j = 0; j < kLoads; ++j) issue(kb, steps, to, w, j);
+    }
+
+    // The MFMA operand of the wave's i-th piece, half h (32 of k) of the slice at
+    // `slice`. EVERY: the distance of the wave's pieces. KMAJOR: pieces of one
+    // cycle of 8 differ from the first in bits that it has clear, so the swizzled
+    // place is the first one's XOR the distance; later cycles are 256 bytes on.
+    template <int EVERY>
+    __device__ __forceinline__ bf16x8_t read(uint32_t slice, int h, int i) const {
+        if (KMAJOR) {
+            constexpr int kCycle = 8 / EVERY;
+            return read_transposed(((slice + at[0]) ^ (EVERY * (i % kCycle) << 5)) + 256 * (i / kCycle) + 32 * kRow * h,
+                                   4 * kRow);
+        }
+        return read_lds(slice + at[h] + EVERY * kPiece * i);
+    }
 };
+
+// Stores of a wave's MI x 4 pieces: row piece 2 i + wm, columns col .. col + 63.
+// The MFMA leaves 16 rows in 16 lanes and 4 columns in each of the four lane
+// groups; values are exchanged between lanes first, so that every store writes
+// whole 128-byte lines of 8 rows.
+template <int DIR, int MI>
+__device__ __forceinline__ void store_tile(const GroupedArgs& a, const Tile& t, const f32x4_t (&acc)[MI][4], int wm, int col) {
+    int lane = lane_id();
+    asm volatile("" : "+v"(lane));  // worked out here: kept over the main loop, its terms would cost registers
+    const int r8 = lane & 7, g = lane >> 4;
+    const bool bit3 = lane & 8;
+    const int64_t first = (DIR == kGradWeight ? (int64_t)t.e * a.M : (int64_t)t.er.first) + t.m0;
+#pragma unroll
+    for (int i = 0; i < MI; ++i) {
+        const int row = 16 * (2 * i + wm) + r8;  // and 8 further
+        if (DIR == kGradWeight && a.out_f32) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {  // 32 columns
+                uint32_t v[2][4];
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    v[0][q] = __float_as_uint(acc[i][2 * h][q]);
+                    v[1][q] = __float_as_uint(acc[i][2 * h + 1][q]);
+                    exchange8(v[0][q], v[1][q], bit3);
+                }
+                const int c = col + 32 * h + (bit3 ? 16 : 0) + 4 * g;
+#pragma unroll
+                for (int s = 0; s < 2; ++s)
+                    if (row + 8 * s < t.rows && c < a.N)
+                        *(uint4*)((float*)a.c + (first + row + 8 * s) * a.N + c) =
+                            make_uint4(v[s][0], v[s][1], v[s][2], v[s][3]);
+            }
+        } else {
+            uint32_t v[2][4];  // halves of 32 columns, then rows r8 and r8 + 8
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    v[h][j] = pack_bf16x2(acc[i][2 * h + j][0], acc[i][2 * h + j][1]);
+                    v[h][2 + j] = pack_bf16x2(acc[i][2 * h + j][2], acc[i][2 * h + j][3]);
+                }
+                gather_pairs(v[h][0], v[h][1]);
+                gather_pairs(v[h][2], v[h][3]);
+            }
+#pragma unroll
+            for (int q = 0; q < 4; ++q) exchange8(v[0][q], v[1][q], bit3);
+            const int c = col + (bit3 ? 32 : 0) + 8 * g;
+#pragma unroll
+            for (int s = 0; s < 2; ++s)
+                if (row + 8 * s < t.rows && c < a.N)
+                    *(uint4*)((uint16_t*)a.c + (first + row + 8 * s) * a.N + c) =
+                        make_uint4(v[s][0], v[s][2], v[s][1], v[s][3]);
+        }
+    }
+}
+
+template <int DIR, class OpA, class OpB>
+__device__ __forceinline__ void init_operands(const GroupedArgs& a, const Tile& t, int cols, int red, int w, int wm,
+                                              int wn, OpA& A, OpB& B) {
+    if (DIR == kGradWeight) {
+        A.init(a.a + (int64_t)t.er.first * a.M, a.M, t.m0, t.rows, red, w, wm);
+        B.init(a.b + (int64_t)t.er.first * a.N, a.N, t.n0, cols, red, w, 4 * wn);
+    } else {
+        A.init(a.a + (int64_t)t.er.first * a.K, a.K, t.m0, t.rows, red, w, wm);
+        B.init(a.b + (int64_t)t.e * a.N * a.K, DIR == kForward ? a.K : a.N, t.n0, cols, red, w, 4 * wn);
+    }
+}
+
+// ---------------------------------------------------------------- whole tiles: 8 waves, 256 columns
+
+constexpr int kSlots = 5;  // slices in LDS: A and B of step 0, of step 1, ... in turn
+constexpr int kSlice = kTile * 64 * 2;
 
 // The tile's product with MI pieces of 16 rows for each wave, and its stores.
 template <int DIR, int MI>
 __device__ __forceinline__ void run_tile(const GroupedArgs& a, const Tile& t, uint32_t lds) {
-    constexpr bool KA = DIR == kGradWeight, KB = DIR != kForward;  // operands whose reduction runs over rows
-    const int tid = threadIdx.x, lane = tid & 63, r16 = lane & 15, g = lane >> 4;
-    const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int wm = w >> 2, wn = w & 3;
-    const int cols = min(kTile, a.N - t.n0);
-    const int red = DIR == kGradWeight ? t.er.live : a.K;
-    const int steps = (red + kStep - 1) / kStep;
-
-    Operand<KA> A;
-    Operand<KB> B;
-    if (DIR == kGradWeight) {
-        A.init(a.a + (int64_t)t.er.first * a.M, a.M, t.m0, t.rows, red, w, lane);
-        B.init(a.b + (int64_t)t.er.first * a.N, a.N, t.n0, cols, red, w, lane);
-    } else {
-        A.init(a.a + (int64_t)t.er.first * a.K, a.K, t.m0, t.rows, red, w, lane);
-        B.init(a.b + (int64_t)t.e * a.N * a.K, DIR == kForward ? a.K : a.N, t.n0, cols, red, w, lane);
-    }
-    // Addresses of this lane's operands within a slice, first half of the step.
-    // Contiguous along k: row 16 p + r16, chunk g (4 further in the second half);
-    // piece p is 2048 p bytes on. Otherwise: k = 8 g + r16 / 4 (and 4 further; 32
-    // in the second half), values 4 (r16 % 4) of column piece p; pieces that
-    // agree in p mod 8 are 256 bytes apart.
-    uint32_t ra[4], rb[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int k = 8 * g + (r16 >> 2);
-        if (KA) ra[i] = k * 512 + (((2 * i + wm) ^ Operand<true>::swizzle(k)) << 5) + (r16 & 3) * 8;
-        else ra[i] = (16 * wm + r16) * 128 + (((4 * (i & 1) + g) ^ ((r16 >> 1) & 7)) << 4);
-        if (KB) rb[i] = k * 512 + (((4 * wn + i) ^ Operand<true>::swizzle(k)) << 5) + (r16 & 3) * 8;
-        else rb[i] = (64 * wn + r16) * 128 + (((4 * (i & 1) + g) ^ ((r16 >> 1) & 7)) << 4);
-    }
-
+    constexpr int kStep = 64;
+    const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), wm = w >> 2, wn = w & 3;
+    const int steps = (a.K + kStep - 1) / kStep;
+    Operand<false, kStep, kTile, 8> A;
+    Operand<DIR == kGradInput, kStep, kTile, 8> B;
+    constexpr int kLoads = decltype(A)::kLoads;
+    init_operands<DIR>(a, t, min(kTile, a.N - t.n0), a.K, w, wm, wn, A, B);
     f32x4_t acc[MI][4];
 #pragma unroll
     for (int i = 0; i < MI; ++i)
@@ -200,109 +275,141 @@ __device__ __forceinline__ void run_tile(const GroupedArgs& a, const Tile& t, ui
     // In interval 2 kb group 0 reads step kb while group 1 computes step kb - 1; in
     // the next one the roles are exchanged. Step kb - 1 has been read by both when
     // interval 2 kb begins, so its two slots take slices 2 kb + 3 and 2 kb + 4 then:
-    // all 8 waves send them (group 0 behind its LDS reads, group 1 before its
-    // MFMAs). Slice 2 kb + 3 is needed when interval 2 kb + 2 begins: every wave waits
-    // for its part of it before the barrier that ends interval 2 kb + 1.
+    // all 8 waves send them, group 0 behind its LDS reads, group 1 spread between
+    // its MFMAs (a DMA of 1 KiB occupies the CU's address unit for 16 cycles; sent
+    // together they held up the MFMAs). Slice 2 kb + 3 is needed when interval
+    // 2 kb + 2 begins: every wave waits for its part of it before the barrier that
+    // ends interval 2 kb + 1.
     const auto slot = [&](int q) { return lds + (uint32_t)(q % kSlots) * kSlice; };
+    const auto wrap = [](int q) { return q >= kSlots ? q - kSlots : q; };
+    // load d of the 2 kLoads of slices 2 kb + 3 and 2 kb + 4; qa: slot of slice 2 kb
+    const auto send = [&](int kb, int qa, int d) {
+        if (d < kLoads) B.issue(kb + 1, steps, lds + (uint32_t)wrap(qa + 3) * kSlice, w, d);
+        else A.issue(kb + 2, steps, lds + (uint32_t)wrap(qa + 4) * kSlice, w, d - kLoads);
+    };
+    const auto group = [&](auto second) {
+        constexpr bool kSecond = decltype(second)::value;
+        int qa = 0;  // slot of A of step kb
+        for (int kb = 0; kb < steps; ++kb) {
+            const uint32_t at_a = lds + (uint32_t)qa * kSlice, at_b = lds + (uint32_t)wrap(qa + 1) * kSlice;
+            bf16x8_t fa[2][MI], fb[2][4];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) fb[h][j] = B.template read<1>(at_b, h, j);
+#pragma unroll
+                for (int i = 0; i < MI; ++i) fa[h][i] = A.template read<2>(at_a, h, i);
+            }
+            if (kSecond) {
+                wait_vmcnt<kLoads>();
+            } else {
+#pragma unroll
+                for (int d = 0; d < 2 * kLoads; ++d) send(kb, qa, d);
+            }
+            wait_lgkmcnt0();
+            block_barrier();
+            qa = wrap(qa + 2);
+            __builtin_amdgcn_s_setprio(1);
+            // operands swapped: each 16 x 16 piece comes out transposed, lane (g, r16)
+            // holding row r16 and columns 4 g .. 4 g + 3
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int i = 0; i < MI; ++i) {
+                    if (kSecond) {
+#pragma unroll
+                        for (int d = 0; d < 2 * kLoads; ++d)
+                            if (d * MI / kLoads == h * MI + i) send(kb + 1, qa, d);
+                    }
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fb[h][j], fa[h][i], acc[i][j], 0, 0, 0);
+                    if (kSecond) __builtin_amdgcn_sched_barrier(0);
+                }
+            __builtin_amdgcn_s_setprio(0);
+            if (!kSecond) wait_vmcnt<kLoads>();
+            block_barrier();
+        }
+    };
     A.issue(0, steps, slot(0), w);
     B.issue(0, steps, slot(1), w);
     A.issue(1, steps, slot(2), w);
     wait_vmcnt<kLoads>();
     block_barrier();
-    if (wm == 1) {
-        B.issue(1, steps, slot(3), w);
-        A.issue(2, steps, slot(4), w);
+    if (wm == 0) {
+        group(std::false_type());
         block_barrier();
+    } else {
+#pragma unroll
+        for (int d = 0; d < 2 * kLoads; ++d) send(0, 0, d);
+        block_barrier();  // half a step later
+        group(std::true_type());
     }
-    int qa = 0;  // slot of A of step kb
-    for (int kb = 0; kb < steps; ++kb) {
-        const auto wrap = [](int q) { return q >= kSlots ? q - kSlots : q; };
-        const uint32_t at_a = lds + (uint32_t)qa * kSlice, at_b = lds + (uint32_t)wrap(qa + 1) * kSlice;
-        bf16x8_t fa[2][MI], fb[2][4];
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-                fb[h][j] = KB ? read_transposed(at_b + rb[j] + 16384 * h, 2048) : read_lds(at_b + rb[h] + 2048 * j);
-#pragma unroll
-            for (int i = 0; i < MI; ++i)
-                fa[h][i] = KA ? read_transposed(at_a + ra[i & 3] + 256 * (i >> 2) + 16384 * h, 2048)
-                              : read_lds(at_a + ra[h] + 4096 * i);
-        }
-        if (wm == 0) {
-            B.issue(kb + 1, steps, lds + (uint32_t)wrap(qa + 3) * kSlice, w);
-            A.issue(kb + 2, steps, lds + (uint32_t)wrap(qa + 4) * kSlice, w);
-        } else {
-            wait_vmcnt<kLoads>();
-        }
-        wait_lgkmcnt0();
-        block_barrier();
-        qa = wrap(qa + 2);
-        if (wm == 1) {
-            B.issue(kb + 2, steps, lds + (uint32_t)wrap(qa + 3) * kSlice, w);
-            A.issue(kb + 3, steps, lds + (uint32_t)wrap(qa + 4) * kSlice, w);
-        }
-        __builtin_amdgcn_s_setprio(1);
-        // operands swapped: each 16 x 16 piece comes out transposed, lane (g, r16)
-        // holding row r16 and columns 4 g .. 4 g + 3
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-#pragma unroll
-            for (int i = 0; i < MI; ++i)
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fb[h][j], fa[h][i], acc[i][j], 0, 0, 0);
-        __builtin_amdgcn_s_setprio(0);
-        if (wm == 0) wait_vmcnt<kLoads>();
-        block_barrier();
-    }
-    if (wm == 0) block_barrier();
     wait_vmcnt<0>();
+    store_tile<DIR, MI>(a, t, acc, wm, t.n0 + 64 * wn);
+    if (a.rows.zero_pad && t.last_rows) clear_padding((uint16_t*)a.c, a.N, t.er, t.n0, kTile);
+}
 
-    // Epilogue: the four column pieces of a row are exchanged between the four
-    // lane groups, so that a lane holds 16 adjacent columns.
-    const int col = t.n0 + 64 * wn + 16 * g;
+// ---------------------------------------------------------------- half tiles: 4 waves, 128 columns, two blocks a CU
+
+constexpr int kHalf = 128;       // columns
+constexpr int kHalfStages = 3;
+constexpr int kHalfStage = (kTile + kHalf) * 32 * 2;  // bytes: A's slice, then B's
+
+template <int DIR, int MI>
+__device__ __forceinline__ void run_half(const GroupedArgs& a, const Tile& t, uint32_t lds) {
+    constexpr int kStep = 32;
+    constexpr bool KA = DIR == kGradWeight, KB = DIR != kForward;
+    const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), wm = w >> 1, wn = w & 1;
+    const int red = DIR == kGradWeight ? t.er.live : a.K;
+    const int steps = (red + kStep - 1) / kStep;
+    Operand<KA, kStep, kTile, 4> A;
+    Operand<KB, kStep, kHalf, 4> B;
+    constexpr int kLoads = decltype(A)::kLoads + decltype(B)::kLoads;
+    init_operands<DIR>(a, t, min(kHalf, a.N - t.n0), red, w, wm, wn, A, B);
+    f32x4_t acc[MI][4];
 #pragma unroll
-    for (int i = 0; i < MI; ++i) {
-        const int row = 16 * (2 * i + wm) + r16;
-        const bool live = row < t.rows;
-        const int64_t at = ((DIR == kGradWeight ? (int64_t)t.e * a.M : (int64_t)t.er.first) + t.m0 + row) * a.N + col;
-        if (DIR == kGradWeight && a.out_f32) {
-            uint32_t v[4][4];
+    for (int i = 0; i < MI; ++i)
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                uint32_t r[4];
+        for (int j = 0; j < 4; ++j) acc[i][j] = (f32x4_t){0.0f, 0.0f, 0.0f, 0.0f};
+    const auto issue = [&](int kb, int st) {
+        A.issue(kb, steps, lds + st * kHalfStage, w);
+        B.issue(kb, steps, lds + st * kHalfStage + decltype(A)::kSlice, w);
+    };
+    issue(0, 0);
+    issue(1, 1);
+    int st = 0;
+    for (int kb = 0; kb < steps; ++kb) {
+        // step kb has landed in every wave's part; every wave has read step kb - 1,
+        // whose stage takes step kb + 2. The CU's other block works while this one waits.
+        wait_vmcnt<kLoads>();
+        block_barrier();
+        const uint32_t at = lds + st * kHalfStage;
+        bf16x8_t fa[MI], fb[4];
 #pragma unroll
-                for (int j = 0; j < 4; ++j) r[j] = __float_as_uint(acc[i][j][q]);
-                transpose4(r);
+        for (int j = 0; j < 4; ++j) fb[j] = B.template read<1>(at + decltype(A)::kSlice, 0, j);
 #pragma unroll
-                for (int j = 0; j < 4; ++j) v[j][q] = r[j];
-            }
+        for (int i = 0; i < MI; ++i) fa[i] = A.template read<2>(at, 0, i);
+        issue(kb + 2, st == 0 ? kHalfStages - 1 : st - 1);
+        wait_lgkmcnt0();
+        __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-                if (live && col + 4 * j < a.N)
-                    *(uint4*)((float*)a.c + at + 4 * j) = make_uint4(v[j][0], v[j][1], v[j][2], v[j][3]);
-        } else {
-            uint32_t lo[4], hi[4];
+        for (int i = 0; i < MI; ++i)
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                lo[j] = pack_bf16x2(acc[i][j][0], acc[i][j][1]);
-                hi[j] = pack_bf16x2(acc[i][j][2], acc[i][j][3]);
-            }
-            transpose4(lo);
-            transpose4(hi);
-            if (live && col < a.N) *(uint4*)((uint16_t*)a.c + at) = make_uint4(lo[0], hi[0], lo[1], hi[1]);
-            if (live && col + 8 < a.N) *(uint4*)((uint16_t*)a.c + at + 8) = make_uint4(lo[2], hi[2], lo[3], hi[3]);
-        }
+            for (int j = 0; j < 4; ++j) acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fb[j], fa[i], acc[i][j], 0, 0, 0);
+        st = st == kHalfStages - 1 ? 0 : st + 1;
     }
-    if (DIR != kGradWeight && a.rows.zero_pad && t.last_rows) clear_padding((uint16_t*)a.c, a.N, t.er, t.n0, kTile);
+    wait_vmcnt<0>();
+    store_tile<DIR, MI>(a, t, acc, wm, t.n0 + 64 * wn);
+    if (DIR != kGradWeight && a.rows.zero_pad && t.last_rows)
+        clear_padding((uint16_t*)a.c, a.N, t.er, t.n0, kHalf);
 }
 
 template <int DIR>
 __global__ __launch_bounds__(512) void k_grouped_gemm_bf16(GroupedArgs a) {
     __shared__ __attribute__((aligned(1024))) uint8_t s_ring[kSlots * kSlice];
     Tile t;
-    if (!find_tile<DIR>(a, &t)) return;
+    if (!find_tile<DIR, kTile>(a, &t)) return;
     const uint32_t lds = lds_offset(s_ring);
     asm volatile("" ::"v"(s_ring) : "memory");  // the ring is written by the DMA alone
     switch ((t.rows + 31) / 32) {
@@ -317,23 +424,60 @@ __global__ __launch_bounds__(512) void k_grouped_gemm_bf16(GroupedArgs a) {
     }
 }
 
+template <int DIR>
+__global__ __launch_bounds__(256, 2) void k_grouped_gemm_bf16_half(GroupedArgs a) {
+    __shared__ __attribute__((aligned(1024))) uint8_t s_ring[kHalfStages * kHalfStage];
+    Tile t;
+    if (!find_tile<DIR, kHalf>(a, &t)) return;
+    const uint32_t lds = lds_offset(s_ring);
+    asm volatile("" ::"v"(s_ring) : "memory");
+    switch ((t.rows + 31) / 32) {
+        case 1: return run_half<DIR, 1>(a, t, lds);
+        case 2: return run_half<DIR, 2>(a, t, lds);
+        case 3: return run_half<DIR, 3>(a, t, lds);
+        case 4: return run_half<DIR, 4>(a, t, lds);
+        case 5: return run_half<DIR, 5>(a, t, lds);
+        case 6: return run_half<DIR, 6>(a, t, lds);
+        case 7: return run_half<DIR, 7>(a, t, lds);
+        default: return run_half<DIR, 8>(a, t, lds);
+    }
+}
+
 }  // namespace
 
 hipError_t launch_grouped_gemm_bf16(int dir, const GroupedArgs& a, int64_t pairs, hipStream_t stream) {
-    const int64_t nt_n = (a.N + kTile - 1) / kTile;
+    // Half tiles for the weight gradient: its reductions are a few steps long, and
+    // one block's stores and first loads pass behind the other's MFMAs (4096 tokens
+    // x top-6, 64 experts, 4096 x 4096: 1.12 ms; whole tiles 1.18 ms, and 1.14 ms
+    // with blocks that take tile after tile). Also where whole tiles would leave
+    // half the CUs without one: 16 rows x 4096 x 4096 on 8 experts 63 against 77 us,
+    // 480 rows x 2240 x 2832 on 8 experts 36 against 49 us; with 144 whole tiles 29
+    // against 27 us. Otherwise whole tiles, which read and move half as much a MFMA:
+    // 65,536 rows x 4096 x 7168 on 32 experts 3.2 against 4.7 ms. Never by the
+    // device's real CU count: the order of the sums must not depend on it.
+    const int64_t row_tiles = pairs / kTile > a.rows.E ? pairs / kTile : pairs < a.rows.E ? pairs : a.rows.E;
+    const bool half = dir == kGradWeight || row_tiles * ((a.N + kTile - 1) / kTile) <= 128;
+    const int cols = half ? kHalf : kTile, threads = half ? 256 : 512;
+    const int64_t nt_n = (a.N + cols - 1) / cols;
     const int64_t mtiles = dir == kGradWeight ? (int64_t)a.rows.E * ((a.M + kTile - 1) / kTile)
                                               : max_row_tiles(a.rows, kTile, pairs);
     const int64_t blocks = mtiles * nt_n;
     if (blocks == 0) return hipSuccess;
-    if (blocks > 0x7FFFFF) return hipErrorInvalidValue;  // 2^32 threads a launch
-    const dim3 grid((unsigned)blocks), block(512);
-    if (launch_debug()) launch_debug_print("k_grouped_gemm_bf16", grid, block, "direction %d n %d", dir, a.N);
-    if (dir == kForward)
+    if (blocks > 0xFFFFFFFFll / threads) return hipErrorInvalidValue;  // 2^32 threads a launch
+    const dim3 grid((unsigned)blocks), block(threads);
+    if (launch_debug())
+        launch_debug_print(half ? "k_grouped_gemm_bf16_half" : "k_grouped_gemm_bf16", grid, block, "direction %d n %d",
+                           dir, a.N);
+    if (dir == kGradWeight)
+        hipLaunchKernelGGL(k_grouped_gemm_bf16_half<kGradWeight>, grid, block, 0, stream, a);
+    else if (dir == kForward && half)
+        hipLaunchKernelGGL(k_grouped_gemm_bf16_half<kForward>, grid, block, 0, stream, a);
+    else if (dir == kGradInput && half)
+        hipLaunchKernelGGL(k_grouped_gemm_bf16_half<kGradInput>, grid, block, 0, stream, a);
+    else if (dir == kForward)
         hipLaunchKernelGGL(k_grouped_gemm_bf16<kForward>, grid, block, 0, stream, a);
-    else if (dir == kGradInput)
-        hipLaunchKernelGGL(k_grouped_gemm_bf16<kGradInput>, grid, block, 0, stream, a);
     else
-        hipLaunchKernelGGL(k_grouped_gemm_bf16<kGradWeight>, grid, block, 0, stream, a);
+        hipLaunchKernelGGL(k_grouped_gemm_bf16<kGradInput>, grid, block, 0, stream, a);
     return hipGetLastError();
 }
 

@@ -37,14 +37,18 @@ constexpr uint32_t kOutOfRange = 0x7FFFFFF0u;
 // read as zeros without touching memory, which is how tails and rows past an
 // expert's last are cut off. Inline assembly, because for the intrinsic the
 // compiler waits for all outstanding DMA before any LDS read; the waits are
-// explicit here. m0 goes in as an operand (the asm never writes it); the s_nop
-// is the wait state an m0 write needs before a DMA reads it.
+// explicit here. m0 goes in as an operand (the asm never writes it). The compiler
+// does not see that the asm is a memory instruction, so the asm itself brings the
+// wait states that one needs behind a write of its scalar operands: five where a
+// vector instruction wrote them (v_readfirstlane, or v_readlane where a scalar
+// was spilled), one behind a scalar write of m0. Without them a descriptor
+// restored just before the load is read stale, and the load goes astray.
 __device__ __forceinline__ void dma16(const void* base, int size, uint32_t off, uint32_t lds) {
     const uint64_t b = (uint64_t)(uintptr_t)base;
     const i32x4_t r = {__builtin_amdgcn_readfirstlane((int)(uint32_t)b),
                        __builtin_amdgcn_readfirstlane((int)(uint32_t)(b >> 32)), __builtin_amdgcn_readfirstlane(size),
                        kBufferFlags};
-    asm volatile("s_nop 0\n\tbuffer_load_dwordx4 %0, %1, 0 offen lds" ::"v"(off), "s"(r), "{m0}"(lds) : "memory");
+    asm volatile("s_nop 4\n\tbuffer_load_dwordx4 %0, %1, 0 offen lds" ::"v"(off), "s"(r), "{m0}"(lds) : "memory");
 }
 
 __device__ __forceinline__ uint32_t lds_offset(const void* p) { return (uint32_t)(uintptr_t)p; }
@@ -74,18 +78,24 @@ __device__ __forceinline__ int row_swizzle16(int r) { return -(r >> 2) & 3; }
 typedef __attribute__((address_space(3))) bf16x8_t lds_bf16x8_t;
 __device__ __forceinline__ bf16x8_t read_lds(uint32_t lds) { return *(const lds_bf16x8_t*)lds; }
 
-// Transposes 4 x 4 words between four registers and the four groups of 16
-// lanes: afterwards register a of group g holds what register g of group a did.
-__device__ __forceinline__ void transpose4(uint32_t r[4]) {
+// Rearranges words r[0], r[1] of the four groups of 16 lanes, word j of group g
+// being unit 4 j + g, so that group g holds units 2 g and 2 g + 1.
+__device__ __forceinline__ void gather_pairs(uint32_t& r0, uint32_t& r1) {
     typedef unsigned int u32x2_t __attribute__((ext_vector_type(2)));
-    const u32x2_t x02 = __builtin_amdgcn_permlane32_swap(r[0], r[2], false, false);
-    const u32x2_t x13 = __builtin_amdgcn_permlane32_swap(r[1], r[3], false, false);
-    const u32x2_t y01 = __builtin_amdgcn_permlane16_swap(x02[0], x13[0], false, false);
-    const u32x2_t y23 = __builtin_amdgcn_permlane16_swap(x02[1], x13[1], false, false);
-    r[0] = y01[0];
-    r[1] = y01[1];
-    r[2] = y23[0];
-    r[3] = y23[1];
+    const u32x2_t x = __builtin_amdgcn_permlane32_swap(r0, r1, false, false);
+    const u32x2_t y = __builtin_amdgcn_permlane16_swap(x[0], x[1], false, false);
+    r0 = y[0];
+    r1 = y[1];
+}
+
+// Exchanges word r1 of the lanes with bit 3 clear with word r0 of those with it
+// set: register s then holds what the lanes with bit 3 equal to s held, words 0
+// and 1 in the lanes with bit 3 clear and set.
+__device__ __forceinline__ void exchange8(uint32_t& r0, uint32_t& r1, bool bit3) {
+    const uint32_t give = bit3 ? r0 : r1;
+    const uint32_t take = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)give, 0x128, 0xF, 0xF, false);  // row_ror:8
+    r0 = bit3 ? take : r0;
+    r1 = bit3 ? r1 : take;
 }
 
 }  // namespace ep

@@ -12,6 +12,7 @@ struct ExpertRows {
     int first, live, owned;
 };
 
+// e is the same in every lane, and so is the result (moved to scalar registers).
 __device__ __forceinline__ ExpertRows expert_rows(const RowsArgs& a, int e) {
     ExpertRows r;
     if (a.mode == EP_MODE_COMPACT) {
@@ -23,17 +24,26 @@ __device__ __forceinline__ ExpertRows expert_rows(const RowsArgs& a, int e) {
         r.live = a.pad[e];  // min(cnt, C)
         r.owned = r.live;
     }
+    r.first = __builtin_amdgcn_readfirstlane(r.first);
+    r.live = __builtin_amdgcn_readfirstlane(r.live);
+    r.owned = __builtin_amdgcn_readfirstlane(r.owned);
     return r;
 }
 
-// Logical block of this block among `total` that have work: each XCD gets a
-// contiguous range (block b runs on XCD b mod 8 as its (b / 8)-th), so that
-// neighbours share operands in one XCD's L2.
-__device__ __forceinline__ int logical_block(int total) {
-    constexpr int kXcds = 8;
+// Pieces of work 0 .. total - 1 are dealt to the 8 XCDs in contiguous ranges
+// (block b runs on XCD b mod 8), so that neighbours share operands in one XCD's
+// L2: the first piece of this block's XCD.
+constexpr int kXcds = 8;
+
+__device__ __forceinline__ int xcd_begin(int total, int xcd) {
     const int q = total / kXcds, r = total % kXcds;
-    const int xcd = (int)blockIdx.x % kXcds, idx = (int)blockIdx.x / kXcds;
-    return (xcd < r ? xcd * (q + 1) : r * (q + 1) + (xcd - r) * q) + idx;
+    return xcd < r ? xcd * (q + 1) : r * (q + 1) + (xcd - r) * q;
+}
+
+// This block's piece where every piece has a block of its own: the XCD's
+// (b / 8)-th.
+__device__ __forceinline__ int logical_block(int total) {
+    return xcd_begin(total, (int)blockIdx.x % kXcds) + (int)blockIdx.x / kXcds;
 }
 
 // Blocks are numbered expert by expert: an expert with c live rows has
