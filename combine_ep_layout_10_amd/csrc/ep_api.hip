@@ -714,7 +714,8 @@ ep_status ep_rms_norm(int32_t num_tokens, int32_t hidden, int32_t dtype, const v
 size_t ep_rms_norm_workspace_bytes(int32_t num_tokens, int32_t hidden) {
     if (check_norm(num_tokens, hidden) != EP_OK) return 0;
     // never 0 for valid sizes, so that 0 means an error
-    return round_up(4 * (size_t)hidden * (size_t)(num_tokens > 0 ? ep::norm_backward_parts(num_tokens) : 1), 256);
+    const int parts = num_tokens < 1 ? 1 : num_tokens < ep::kNormParts ? num_tokens : ep::kNormParts;
+    return round_up(4 * (size_t)hidden * (size_t)parts, 256);
 }
 
 ep_status ep_rms_norm_backward(int32_t num_tokens, int32_t hidden, const void* total, const void* weight,

@@ -182,17 +182,16 @@ struct NormBackwardArgs {
     const uint16_t* grad_total;  // or NULL
     uint16_t* grad_x;
     float* grad_weight;
-    float* partial;  // [norm_backward_parts(T), H]
+    float* partial;  // [min(T, kNormParts), H]
     int T, H;
 };
 
 // Channels of a norm's row: at most 4 vectors of 8 for each of 1,024 lanes.
 constexpr int kMaxNormHidden = 1 << 15;
-// Row groups of the norm's backward, each with its own partial sum of the
-// weight gradient: a function of T alone, so that results never depend on the
-// launch geometry.
+// Blocks of the norm's backward at most, each with its own partial sum of the
+// weight gradient: two a CU of 256, a constant, so that results never depend on
+// the device's CU count.
 constexpr int kNormParts = 512;
-inline int norm_backward_parts(int T) { return T < kNormParts ? T : kNormParts; }
 
 // Padding rows per zero-fill piece (a piece of one expert's padding): in the
 // dispatch kernel, and in the single-launch layout + dispatch, where every

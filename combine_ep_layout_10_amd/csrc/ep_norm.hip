@@ -35,18 +35,19 @@ __device__ __forceinline__ uint4 pack8(const float f[8]) {
                       pack_bf16x2(f[6], f[7]));
 }
 
-// Sum over the block (at most 16 waves), the same in every thread: a butterfly
-// over each wave, then the waves in order. `tmp`: 16 floats of LDS, free again
-// after the next barrier of the caller.
-__device__ __forceinline__ float block_sum(float v, float* tmp) {
+// Sum over the threads of a row (the block's x; whole waves), the same in each of
+// them: a butterfly over each wave, then the row's waves in order. `tmp` is LDS
+// for one float a wave of the block, free again behind the caller's next barrier. Every thread of the block calls it.
+__device__ __forceinline__ float row_sum(float v, float* tmp) {
+    const int row_waves = blockDim.x >> 6;
 #pragma unroll
     for (int o = 32; o > 0; o >>= 1) v += __shfl_xor(v, o, kWave);
-    const int nw = blockDim.x >> 6;
-    if (nw == 1) return v;
-    if ((threadIdx.x & 63) == 0) tmp[threadIdx.x >> 6] = v;
+    if (row_waves == 1) return v;
+    const int first = threadIdx.y * row_waves;
+    if ((threadIdx.x & 63) == 0) tmp[first + (threadIdx.x >> 6)] = v;
     __syncthreads();
     float s = 0.0f;
-    for (int i = 0; i < nw; ++i) s += tmp[i];
+    for (int i = 0; i < row_waves; ++i) s += tmp[first + i];
     return s;
 }
 
@@ -57,17 +58,58 @@ __device__ __forceinline__ float max16_dpp(float v) {
     return fmaxf(v, __int_as_float(__builtin_amdgcn_update_dpp(0, x, 0x140, 0xF, 0xF, false)));  // row_mirror
 }
 
-// V vectors of 8 channels a lane: vector i of lane l is i * blockDim + l.
+// v = f / q, correctly rounded, for |f| <= 448 q (1 + 2^-23). With r the rounded
+// reciprocal, the product f r is off by at most two units of the last place; one
+// correction by the exact remainder brings it within one, and by Markstein's
+// theorem (a quotient within one unit, and a correctly rounded reciprocal) the
+// second makes it the rounded quotient. Five operations instead of a division's
+// dozen. The remainder keeps f's zeros' sign (y - rem * r), and is exact while
+// nothing underflows: |f / q| >= 2^-10, below which every code is a signed zero,
+// and q >= 2^-80 leave its last bit at 2^-136. Smaller and huge q divide.
+__device__ __forceinline__ void quotients(const float f[8], float q, float v[8]) {
+    if (q >= 0x1p-80f && q <= 0x1p100f) {
+        const float r = 1.0f / q;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            float y = f[j] * r;
+            y = __builtin_fmaf(-__builtin_fmaf(y, q, -f[j]), r, y);
+            v[j] = __builtin_fmaf(-__builtin_fmaf(y, q, -f[j]), r, y);
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = fminf(fmaxf(f[j] / q, -448.0f), 448.0f);
+    }
+}
+
+// A row's threads: whole waves, one vector of 8 channels each (V of them for rows
+// of more than 8192 channels), at most 1024. Short rows share a block.
+struct RowShape {
+    int threads, rows, v;  // of a row; rows of a block; vectors a thread
+};
+
+RowShape row_shape(int H) {
+    RowShape s;
+    const int t = (H / 8 + 63) / 64 * 64;
+    s.threads = t < 1024 ? t : 1024;
+    s.rows = s.threads <= 256 ? 512 / s.threads : 1;
+    s.v = (H / 8 + 1023) / 1024;
+    return s;
+}
+
+// V vectors of 8 channels a lane: vector i of thread l of a row is i * threads + l.
 template <int V, bool FP8>
 __global__ __launch_bounds__(1024) void k_rms_norm(NormArgs a) {
     __shared__ float s_sum[16];
-    const int64_t row = (int64_t)blockIdx.x * a.H;
-    const int nv = a.H / 8;
+    const int tid = threadIdx.x, threads = blockDim.x;
+    const int t = V == 1 ? (int)(blockIdx.x * blockDim.y + threadIdx.y) : (int)blockIdx.x;
+    const bool live = t < a.T;
+    const int64_t row = (int64_t)t * a.H;
+    const int nv = live ? a.H / 8 : 0;
     uint4 s[V];
     float sum = 0.0f;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-        const int c = i * blockDim.x + threadIdx.x;
+        const int c = i * threads + tid;
         s[i] = make_uint4(0u, 0u, 0u, 0u);
         if (c >= nv) continue;
         s[i] = *(const uint4*)(a.x + row + 8 * c);
@@ -85,12 +127,12 @@ __global__ __launch_bounds__(1024) void k_rms_norm(NormArgs a) {
 #pragma unroll
         for (int j = 0; j < 8; ++j) sum = __builtin_fmaf(f[j], f[j], sum);
     }
-    sum = block_sum(sum, s_sum);
+    sum = row_sum(sum, s_sum);
     const float rstd = 1.0f / sqrtf(sum / (float)a.H + a.eps);
-    if (threadIdx.x == 0) a.rstd[blockIdx.x] = rstd;
+    if (live && tid == 0) a.rstd[t] = rstd;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-        const int c = i * blockDim.x + threadIdx.x;
+        const int c = i * threads + tid;
         if (c >= nv) continue;  // whole groups of 16 lanes: H % 128 == 0 for FP8
         float f[8], w[8];
         unpack8(s[i], f);
@@ -109,8 +151,7 @@ __global__ __launch_bounds__(1024) void k_rms_norm(NormArgs a) {
             uint32_t code[2] = {0u, 0u};
             if (q > 0.0f) {
                 float v[8];
-#pragma unroll
-                for (int j = 0; j < 8; ++j) v[j] = fminf(fmaxf(f[j] / q, -448.0f), 448.0f);
+                quotients(f, q, v);
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
                     int p = __builtin_amdgcn_cvt_pk_fp8_f32(v[4 * j], v[4 * j + 1], 0, false);
@@ -119,64 +160,102 @@ __global__ __launch_bounds__(1024) void k_rms_norm(NormArgs a) {
                 }
             }
             *(uint2*)((uint8_t*)a.y + row + 8 * c) = make_uint2(code[0], code[1]);
-            if ((threadIdx.x & 15) == 0) a.scales[(int64_t)blockIdx.x * (a.H / 128) + c / 16] = q * rstd;
+            if ((tid & 15) == 0) a.scales[(int64_t)t * (a.H / 128) + c / 16] = q * rstd;
         }
     }
 }
 
-template <int V>
+// A row's threads sum the weight gradient of their channels over the rows they
+// take, in registers; the rows of a block that share its channels are added
+// through LDS at the end, so a block leaves one partial sum of H channels. The
+// next row's values are loaded before the present row's sum is waited for.
+template <int V, bool BRANCH>
 __global__ __launch_bounds__(1024) void k_rms_norm_backward(NormBackwardArgs a) {
     __shared__ float s_sum[2][16];
-    const int nv = a.H / 8;
+    __shared__ float s_part[V == 1 ? 8 * 512 : 1];  // several rows a block only with V == 1 and 512 threads
+    const int tid = threadIdx.x, threads = blockDim.x;
+    const int sub = V == 1 ? threadIdx.y : 0, rows = V == 1 ? blockDim.y : 1;  // long rows have blocks of their own
+    const int nv = a.H / 8, step = gridDim.x * rows;
+    constexpr bool kAhead = V == 1;  // longer rows have no registers for it, and loads enough in flight
     float gw[V][8];
+    uint4 vs[V], vg[V], vt[V];
+    float rstd = 0.0f;
+    const auto load = [&](int t) {
+        const int64_t row = (int64_t)t * a.H;
+        if (t < a.T) rstd = a.rstd[t];
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            const int c = i * threads + tid;
+            vs[i] = vg[i] = vt[i] = make_uint4(0u, 0u, 0u, 0u);
+            if (c >= nv || t >= a.T) continue;
+            vs[i] = *(const uint4*)(a.total + row + 8 * c);
+            vg[i] = *(const uint4*)(a.grad_y + row + 8 * c);
+            if (BRANCH && kAhead) vt[i] = *(const uint4*)(a.grad_total + row + 8 * c);
+        }
+    };
 #pragma unroll
     for (int i = 0; i < V; ++i)
 #pragma unroll
         for (int j = 0; j < 8; ++j) gw[i][j] = 0.0f;
-    int turn = 0;  // two buffers for the block's sums, so that one barrier a row is enough
-    for (int t = blockIdx.x; t < a.T; t += gridDim.x, turn ^= 1) {
-        const int64_t row = (int64_t)t * a.H;
-        const float rstd = a.rstd[t];
-        uint4 vs[V], vg[V];
+    int t = (int)blockIdx.x * rows + sub;
+    if (kAhead) load(t);
+    int turn = 0;  // two buffers for the rows' sums, so that one barrier a row is enough
+    for (int t0 = (int)blockIdx.x * rows; t0 < a.T; t0 += step, t += step, turn ^= 1) {
+        if (!kAhead) load(t);
+        uint4 s4[V], g4[V], t4[V];
+        const float r = rstd;
         float dot = 0.0f;
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-            const int c = i * blockDim.x + threadIdx.x;
-            vs[i] = vg[i] = make_uint4(0u, 0u, 0u, 0u);
+            s4[i] = vs[i];
+            g4[i] = vg[i];
+            t4[i] = vt[i];
+            const int c = i * threads + tid;
             if (c >= nv) continue;
-            vs[i] = *(const uint4*)(a.total + row + 8 * c);
-            vg[i] = *(const uint4*)(a.grad_y + row + 8 * c);
-            float s[8], g[8], w[8];
-            unpack8(vs[i], s);
-            unpack8(vg[i], g);
-            unpack8(*(const uint4*)(a.weight + 8 * c), w);
+            float s[8], g[8], x[8];
+            unpack8(s4[i], s);
+            unpack8(g4[i], g);
+            unpack8(*(const uint4*)(a.weight + 8 * c), x);
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-                const float x = s[j] * rstd;
-                dot = __builtin_fmaf(g[j] * w[j], x, dot);
-                gw[i][j] = __builtin_fmaf(g[j], x, gw[i][j]);
+                const float xhat = s[j] * r;
+                dot = __builtin_fmaf(g[j] * x[j], xhat, dot);
+                gw[i][j] = __builtin_fmaf(g[j], xhat, gw[i][j]);
             }
         }
-        const float mean = block_sum(dot, s_sum[turn]) / (float)a.H;
+        if (kAhead) load(t + step);
+        const float mean = row_sum(dot, s_sum[turn]) / (float)a.H;
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-            const int c = i * blockDim.x + threadIdx.x;
-            if (c >= nv) continue;
-            float s[8], g[8], w[8], r[8];
-            unpack8(vs[i], s);
-            unpack8(vg[i], g);
-            unpack8(*(const uint4*)(a.weight + 8 * c), w);
+            const int c = i * threads + tid;
+            if (c >= nv || t >= a.T) continue;
+            const int64_t at = (int64_t)t * a.H + 8 * c;
+            float s[8], g[8], x[8], o[8];
+            unpack8(V < 4 ? s4[i] : *(const uint4*)(a.total + at), s);  // V = 4 has no registers to keep them
+            unpack8(V < 4 ? g4[i] : *(const uint4*)(a.grad_y + at), g);
+            unpack8(*(const uint4*)(a.weight + 8 * c), x);
+            if (BRANCH) unpack8(kAhead ? t4[i] : *(const uint4*)(a.grad_total + at), o);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) r[j] = 0.0f;
-            if (a.grad_total != nullptr) unpack8(*(const uint4*)(a.grad_total + row + 8 * c), r);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) r[j] += rstd * (g[j] * w[j] - s[j] * rstd * mean);
-            *(uint4*)(a.grad_x + row + 8 * c) = pack8(r);
+            for (int j = 0; j < 8; ++j) {
+                const float v = r * (g[j] * x[j] - s[j] * r * mean);
+                o[j] = BRANCH ? v + o[j] : v;
+            }
+            *(uint4*)(a.grad_x + at) = pack8(o);
         }
+    }
+    if (V == 1 && rows > 1) {  // rows sub > 0 of the block, in order
+        float* p = s_part + (sub * threads + tid) * 8;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) p[j] = gw[0][j];
+        __syncthreads();
+        if (sub > 0) return;
+        for (int k = 1; k < rows; ++k)
+#pragma unroll
+            for (int j = 0; j < 8; ++j) gw[0][j] += s_part[(k * threads + tid) * 8 + j];
     }
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-        const int c = i * blockDim.x + threadIdx.x;
+        const int c = i * threads + tid;
         if (c >= nv) continue;
         float4* p = (float4*)(a.partial + (int64_t)blockIdx.x * a.H + 8 * c);
         p[0] = make_float4(gw[i][0], gw[i][1], gw[i][2], gw[i][3]);
@@ -184,62 +263,77 @@ __global__ __launch_bounds__(1024) void k_rms_norm_backward(NormBackwardArgs a) 
     }
 }
 
-// grad_weight[c]: the groups' partial sums, 16 strands in order, then the strands.
-__global__ __launch_bounds__(256) void k_rms_norm_grad_weight(const float* partial, float* grad_weight, int parts, int H) {
-    __shared__ float s_part[16][17];
+// grad_weight[c]: the blocks' partial sums in 64 strands (partial p in strand
+// p mod 64, in order), then the strands in order.
+__global__ __launch_bounds__(1024) void k_rms_norm_grad_weight(const float* partial, float* grad_weight, int parts, int H) {
+    __shared__ float s_part[64][17];
     const int x = threadIdx.x & 15, y = threadIdx.x >> 4;
     const int c = (int)blockIdx.x * 16 + x;
+    float v[kNormParts / 64];
+#pragma unroll
+    for (int i = 0; i < kNormParts / 64; ++i)
+        v[i] = c < H && i * 64 + y < parts ? partial[(int64_t)(i * 64 + y) * H + c] : 0.0f;
     float sum = 0.0f;
-    if (c < H)
-        for (int p = y; p < parts; p += 16) sum += partial[(int64_t)p * H + c];
+#pragma unroll
+    for (int i = 0; i < kNormParts / 64; ++i) sum += v[i];
     s_part[y][x] = sum;
     __syncthreads();
     if (y == 0 && c < H) {
         sum = 0.0f;
-        for (int i = 0; i < 16; ++i) sum += s_part[i][x];
+        for (int i = 0; i < 64; ++i) sum += s_part[i][x];
         grad_weight[c] = sum;
     }
 }
 
-int norm_threads(int H) {
-    const int v = (H / 8 + 63) / 64 * 64;
-    return v < 1024 ? v : 1024;
-}
-
 template <int V>
-void norm_launch(const NormArgs& a, hipStream_t stream) {
-    const dim3 grid((unsigned)a.T), block((unsigned)norm_threads(a.H));
+void norm_launch(const NormArgs& a, const RowShape& s, dim3 grid, hipStream_t stream) {
+    const dim3 block((unsigned)s.threads, (unsigned)s.rows);
     if (a.scales != nullptr)
         hipLaunchKernelGGL((k_rms_norm<V, true>), grid, block, 0, stream, a);
     else
         hipLaunchKernelGGL((k_rms_norm<V, false>), grid, block, 0, stream, a);
 }
 
+template <int V>
+void norm_backward_launch(const NormBackwardArgs& a, const RowShape& s, dim3 grid, hipStream_t stream) {
+    const dim3 block((unsigned)s.threads, (unsigned)s.rows);
+    if (a.grad_total != nullptr)
+        hipLaunchKernelGGL((k_rms_norm_backward<V, true>), grid, block, 0, stream, a);
+    else
+        hipLaunchKernelGGL((k_rms_norm_backward<V, false>), grid, block, 0, stream, a);
+}
+
 }  // namespace
 
 hipError_t launch_rms_norm(const NormArgs& a, hipStream_t stream) {
     if (a.T == 0) return hipSuccess;
-    const int v = (a.H / 8 + 1023) / 1024;
+    const RowShape s = row_shape(a.H);
+    const int64_t blocks = ((int64_t)a.T + s.rows - 1) / s.rows;
+    if (blocks * s.threads * s.rows > 0xFFFFFFFFll) return hipErrorInvalidValue;  // 2^32 threads a launch
+    const dim3 grid((unsigned)blocks);
     if (launch_debug())
-        launch_debug_print("k_rms_norm", dim3((unsigned)a.T), dim3((unsigned)norm_threads(a.H)), "hidden %d", a.H);
-    if (v <= 1) norm_launch<1>(a, stream);
-    else if (v <= 2) norm_launch<2>(a, stream);
-    else norm_launch<4>(a, stream);
+        launch_debug_print("k_rms_norm", grid, dim3((unsigned)(s.threads * s.rows)), "hidden %d", a.H);
+    if (s.v <= 1) norm_launch<1>(a, s, grid, stream);
+    else if (s.v <= 2) norm_launch<2>(a, s, grid, stream);
+    else norm_launch<4>(a, s, grid, stream);
     return hipGetLastError();
 }
 
 hipError_t launch_rms_norm_backward(const NormBackwardArgs& a, hipStream_t stream) {
-    const int v = (a.H / 8 + 1023) / 1024, parts = norm_backward_parts(a.T);
-    const dim3 grid((unsigned)parts), block((unsigned)norm_threads(a.H));
-    if (launch_debug()) launch_debug_print("k_rms_norm_backward", grid, block, "hidden %d", a.H);
+    const RowShape s = row_shape(a.H);
+    const int64_t need = ((int64_t)a.T + s.rows - 1) / s.rows;
+    const int parts = (int)(need < kNormParts ? need : kNormParts);
+    const dim3 grid((unsigned)parts);
+    if (launch_debug())
+        launch_debug_print("k_rms_norm_backward", grid, dim3((unsigned)(s.threads * s.rows)), "hidden %d", a.H);
     if (parts > 0) {
-        if (v <= 1) hipLaunchKernelGGL(k_rms_norm_backward<1>, grid, block, 0, stream, a);
-        else if (v <= 2) hipLaunchKernelGGL(k_rms_norm_backward<2>, grid, block, 0, stream, a);
-        else hipLaunchKernelGGL(k_rms_norm_backward<4>, grid, block, 0, stream, a);
+        if (s.v <= 1) norm_backward_launch<1>(a, s, grid, stream);
+        else if (s.v <= 2) norm_backward_launch<2>(a, s, grid, stream);
+        else norm_backward_launch<4>(a, s, grid, stream);
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
     }
-    hipLaunchKernelGGL(k_rms_norm_grad_weight, dim3((unsigned)((a.H + 15) / 16)), dim3(256), 0, stream, a.partial,
+    hipLaunchKernelGGL(k_rms_norm_grad_weight, dim3((unsigned)((a.H + 15) / 16)), dim3(1024), 0, stream, a.partial,
                        a.grad_weight, parts, a.H);
     return hipGetLastError();
 }
