@@ -660,10 +660,10 @@ ep_status ep_grouped_gemm_mxfp4(const ep_handle* h, const void* a, const void* b
         return fail(EP_ERR_INVALID_ARG, "a, b, b_scales and out must be non-NULL");
     if (!aligned(a, 16) || !aligned(b, 16) || !aligned(out, 16))
         return fail(EP_ERR_INVALID_ARG, "a, b and out must be 16-byte aligned");
-    ep::Mxfp4Args g;
+    ep::StreamArgs g;
     g.rows = rows_args(h);
     g.x = (const uint16_t*)a;
-    g.b = (const uint8_t*)b;
+    g.b = b;
     g.b_scales = (const uint8_t*)b_scales;
     g.out = (uint16_t*)out;
     g.N = n;

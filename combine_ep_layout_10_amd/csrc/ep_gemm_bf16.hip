@@ -13,12 +13,12 @@
 // bf16 products are exact in binary32 and the MFMA accumulates in binary32, so
 // the only rounding is the output's.
 //
-// One kernel for the three: a block of 8 waves computes a tile of 256 x 256,
-// wave (wm, wn) the 16-row pieces 2 i + wm of it by the columns 64 wn .. + 63,
-// with v_mfma_f32_16x16x32_bf16. The reduction runs in steps of 64: both
-// operands' slices (32 KiB each) move from memory to LDS by DMA, into a ring of
-// five. All tails (rows, columns, reduction) are the buffer resource's range
-// check, which fills zeros.
+// Whole tiles (forward, grad_input): a block of 8 waves computes 256 x 256, wave
+// (wm, wn) the 16-row pieces 2 i + wm of it by the columns 64 wn .. + 63, with
+// v_mfma_f32_16x16x32_bf16. The reduction runs in steps of 64: both operands'
+// slices (32 KiB each) move from memory to LDS by DMA, into a ring that fills the
+// CU's 160 KiB. All tails (rows, columns, reduction) are the buffer resource's
+// range check, which fills zeros.
 //
 // Rows: an expert's rows are cut into ceil(rows / 256) tiles of equal size
 // (rounded up to 32), and the loop is compiled for every number MI of 32-row
@@ -30,24 +30,33 @@
 // exchanges the roles. Each SIMD holds one wave of either group, so its matrix
 // unit always has work.
 //
-// LDS: a slice of an operand that is contiguous along the reduction is
-// [256 rows][64 k] (128-byte rows, whole cache lines in memory); its 16-byte
-// chunk c of row r is stored at c ^ (r / 2 mod 8). The other operands are
-// [64 k][256 columns] (512-byte rows) and are read through the transposing LDS
-// read, 4 k by 16 columns; their 32-byte pair of chunks p of row k is stored at
-// p ^ f(k), f(k) = k mod 4 + 4 (k / 8 mod 2). Either way a read meets each bank
-// once (SQ_LDS_BANK_CONFLICT 0).
+// LDS: a slice of an operand that is contiguous along the reduction has rows of 64
+// k (128 bytes, whole cache lines in memory; with steps of 32, half lines, the
+// product took 7 % longer); its 16-byte chunk c of row r is stored at
+// c ^ (r / 2 mod 8). The other operands have a row of columns for each k and are
+// read through the transposing LDS read, 4 k by 16 columns; their 32-byte pair of
+// chunks p of row k is stored at p ^ f(k), f(k) = k mod 4 + 4 (k / 8 mod 2). Either
+// way a read meets each bank once (SQ_LDS_BANK_CONFLICT 0).
+//
+// Half tiles (grad_weight, few tiles): 4 waves, 256 x 128, steps of 32, two blocks
+// a CU; described with them. Few rows an expert: ep_gemm_stream.hip.
+//
+// What bounds it, on MI355X: 65,536 rows x 4096 x 7168 on 32 experts take 3.2 ms
+// (1.20 PFLOP/s; a library product of 8192^3 reaches 1.46), the matrix units busy 61 %
+// of the cycles at the 1.7 GHz that the card holds under this load. In an interval
+// of the loop 512 cycles of MFMA stand in about 650; with operands that never leave
+// L2 the same loop takes 2.8 ms. The rest is tiles that are not full, and a tile's
+// first loads and stores. One wave a SIMD with 128 x 128 pieces and the
+// accumulators in AGPRs measured 3.6 ms, a ring of five steps of 32 as four.
 #include "ep_mma_dev.h"
 #include "ep_rows_dev.h"
-
-#include <type_traits>
 
 namespace ep {
 
 namespace {
 
-constexpr int kTile = 256;  // rows of a tile
-constexpr int kGroupRows = 8;                // row tiles that share column tiles in the block order
+constexpr int kTile = 256;     // rows of a tile
+constexpr int kGroupRows = 8;  // row tiles that share column tiles in the block order
 
 struct Tile {
     int e;          // expert
@@ -252,98 +261,142 @@ __device__ __forceinline__ void init_operands(const GroupedArgs& a, const Tile& 
 
 // ---------------------------------------------------------------- whole tiles: 8 waves, 256 columns
 
-constexpr int kSlots = 5;  // slices in LDS: A and B of step 0, of step 1, ... in turn
-constexpr int kSlice = kTile * 64 * 2;
+// The ring of a tile's slices in 160 KiB of LDS. Steps are read by group 0 in
+// interval 2 kb (while group 1 computes step kb - 1) and by group 1 in the next one
+// (while group 0 computes step kb); step kb - 1 has been read by both when interval
+// 2 kb begins, and its place is filled again from then on.
+//   256 rows: five slots of 32 KiB; slice q (A of step q / 2 when even, B when odd)
+//   lives in slot q mod 5, and interval 2 kb sends slices 2 kb + 3 and 2 kb + 4.
+//   Fewer rows leave room for more steps: 128 rows three, 64 rows four (step kb in
+//   place kb mod kSteps), and interval 2 kb sends step kb + kSteps - 1.
+template <class OpA, class OpB>
+struct Ring {
+    static constexpr bool kSlots = OpA::kSlice == OpB::kSlice;
+    static constexpr int kBytes = 160 * 1024;
+    static constexpr int kStepBytes = OpA::kSlice + OpB::kSlice, kSteps = kBytes / kStepBytes;
+    static constexpr int kSend = OpA::kLoads + OpB::kLoads;  // loads of a wave for an interval
+    // a wave's loads that may be on their way when step kb + 1 has landed, those of interval 2 kb sent
+    static constexpr int kKeep = kSlots ? OpA::kLoads : (kSteps - 2) * kSend;
+
+    const OpA& A;
+    const OpB& B;
+    int steps;
+    uint32_t lds;
+    int w;
+
+    __device__ __forceinline__ static int wrap(int q, int n) { return q >= n ? q - n : q; }
+    // place: of step kb (slots: that of its slice of A)
+    __device__ __forceinline__ uint32_t at_a(int place) const { return lds + place * (kSlots ? OpA::kSlice : kStepBytes); }
+    __device__ __forceinline__ uint32_t at_b(int place) const {
+        return kSlots ? lds + wrap(place + 1, 5) * OpA::kSlice : at_a(place) + OpA::kSlice;
+    }
+    __device__ __forceinline__ static int next(int place) { return kSlots ? wrap(place + 2, 5) : wrap(place + 1, kSteps); }
+    __device__ __forceinline__ void send_step(int kb) const {
+        A.issue(kb, steps, at_a(kb), w);
+        B.issue(kb, steps, at_a(kb) + OpA::kSlice, w);
+    }
+    // ahead of interval 0; step 0 has landed in this wave's part on return
+    __device__ __forceinline__ void first() const {
+        if (kSlots) {
+            A.issue(0, steps, lds, w);
+            B.issue(0, steps, lds + OpA::kSlice, w);
+            A.issue(1, steps, lds + 2 * OpA::kSlice, w);
+        } else {
+#pragma unroll
+            for (int kb = 0; kb < kSteps - 1; ++kb) send_step(kb);
+        }
+        wait_vmcnt<kKeep>();
+    }
+    // load d of interval 2 kb
+    __device__ __forceinline__ void send(int kb, int place, int d) const {
+        if (kSlots) {
+            if (d < OpB::kLoads) B.issue(kb + 1, steps, lds + wrap(place + 3, 5) * OpA::kSlice, w, d);
+            else A.issue(kb + 2, steps, lds + wrap(place + 4, 5) * OpA::kSlice, w, d - OpB::kLoads);
+        } else {
+            const uint32_t to = at_a(wrap(place + kSteps - 1, kSteps));
+            if (d < OpB::kLoads) B.issue(kb + kSteps - 1, steps, to + OpA::kSlice, w, d);
+            else A.issue(kb + kSteps - 1, steps, to, w, d - OpB::kLoads);
+        }
+    }
+};
+
+// The loop of one group of waves over all steps. Every wave sends its part of an
+// interval's loads: group 0 behind its LDS reads, group 1 (SECOND) spread between
+// its MFMAs, since a DMA of 1 KiB occupies the CU's address unit for 16 cycles and
+// all of them together held up the MFMAs. The loads that step kb + 1 needs are
+// waited for by every wave before the barrier that ends interval 2 kb + 1.
+template <bool SECOND, int MI, class OpA, class OpB>
+__device__ __forceinline__ void multiply(const Ring<OpA, OpB>& ring, f32x4_t (&acc)[MI][4]) {
+    using R = Ring<OpA, OpB>;
+    int place = 0;
+    for (int kb = 0; kb < ring.steps; ++kb) {
+        const uint32_t at_a = ring.at_a(place), at_b = ring.at_b(place);
+        bf16x8_t fa[2][MI], fb[2][4];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) fb[h][j] = ring.B.template read<1>(at_b, h, j);
+#pragma unroll
+            for (int i = 0; i < MI; ++i) fa[h][i] = ring.A.template read<2>(at_a, h, i);
+        }
+        if (SECOND) {
+            wait_vmcnt<R::kKeep>();
+        } else {
+#pragma unroll
+            for (int d = 0; d < R::kSend; ++d) ring.send(kb, place, d);
+        }
+        wait_lgkmcnt0();
+        block_barrier();
+        place = R::next(place);
+        __builtin_amdgcn_s_setprio(1);
+        // operands swapped: each 16 x 16 piece comes out transposed, lane (g, r16)
+        // holding row r16 and columns 4 g .. 4 g + 3
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int i = 0; i < MI; ++i) {
+                if (SECOND) {
+#pragma unroll
+                    for (int d = 0; d < R::kSend; ++d)
+                        if (d * 2 * MI / R::kSend == h * MI + i) ring.send(kb + 1, place, d);
+                }
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fb[h][j], fa[h][i], acc[i][j], 0, 0, 0);
+                if (SECOND) __builtin_amdgcn_sched_barrier(0);
+            }
+        __builtin_amdgcn_s_setprio(0);
+        if (!SECOND) wait_vmcnt<R::kKeep>();
+        block_barrier();
+    }
+}
 
 // The tile's product with MI pieces of 16 rows for each wave, and its stores.
 template <int DIR, int MI>
 __device__ __forceinline__ void run_tile(const GroupedArgs& a, const Tile& t, uint32_t lds) {
-    constexpr int kStep = 64;
+    constexpr int kStep = 64, kRows = MI <= 2 ? 64 : MI <= 4 ? 128 : 256;
     const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), wm = w >> 2, wn = w & 3;
-    const int steps = (a.K + kStep - 1) / kStep;
-    Operand<false, kStep, kTile, 8> A;
-    Operand<DIR == kGradInput, kStep, kTile, 8> B;
-    constexpr int kLoads = decltype(A)::kLoads;
+    using OpA = Operand<false, kStep, kRows, 8>;
+    using OpB = Operand<DIR == kGradInput, kStep, kTile, 8>;
+    OpA A;
+    OpB B;
     init_operands<DIR>(a, t, min(kTile, a.N - t.n0), a.K, w, wm, wn, A, B);
     f32x4_t acc[MI][4];
 #pragma unroll
     for (int i = 0; i < MI; ++i)
 #pragma unroll
         for (int j = 0; j < 4; ++j) acc[i][j] = (f32x4_t){0.0f, 0.0f, 0.0f, 0.0f};
-
-    // Ring: slice q (A of step q / 2 when even, B when odd) lives in slot q mod 5.
-    // In interval 2 kb group 0 reads step kb while group 1 computes step kb - 1; in
-    // the next one the roles are exchanged. Step kb - 1 has been read by both when
-    // interval 2 kb begins, so its two slots take slices 2 kb + 3 and 2 kb + 4 then:
-    // all 8 waves send them, group 0 behind its LDS reads, group 1 spread between
-    // its MFMAs (a DMA of 1 KiB occupies the CU's address unit for 16 cycles; sent
-    // together they held up the MFMAs). Slice 2 kb + 3 is needed when interval
-    // 2 kb + 2 begins: every wave waits for its part of it before the barrier that
-    // ends interval 2 kb + 1.
-    const auto slot = [&](int q) { return lds + (uint32_t)(q % kSlots) * kSlice; };
-    const auto wrap = [](int q) { return q >= kSlots ? q - kSlots : q; };
-    // load d of the 2 kLoads of slices 2 kb + 3 and 2 kb + 4; qa: slot of slice 2 kb
-    const auto send = [&](int kb, int qa, int d) {
-        if (d < kLoads) B.issue(kb + 1, steps, lds + (uint32_t)wrap(qa + 3) * kSlice, w, d);
-        else A.issue(kb + 2, steps, lds + (uint32_t)wrap(qa + 4) * kSlice, w, d - kLoads);
-    };
-    const auto group = [&](auto second) {
-        constexpr bool kSecond = decltype(second)::value;
-        int qa = 0;  // slot of A of step kb
-        for (int kb = 0; kb < steps; ++kb) {
-            const uint32_t at_a = lds + (uint32_t)qa * kSlice, at_b = lds + (uint32_t)wrap(qa + 1) * kSlice;
-            bf16x8_t fa[2][MI], fb[2][4];
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-#pragma unroll
-                for (int j = 0; j < 4; ++j) fb[h][j] = B.template read<1>(at_b, h, j);
-#pragma unroll
-                for (int i = 0; i < MI; ++i) fa[h][i] = A.template read<2>(at_a, h, i);
-            }
-            if (kSecond) {
-                wait_vmcnt<kLoads>();
-            } else {
-#pragma unroll
-                for (int d = 0; d < 2 * kLoads; ++d) send(kb, qa, d);
-            }
-            wait_lgkmcnt0();
-            block_barrier();
-            qa = wrap(qa + 2);
-            __builtin_amdgcn_s_setprio(1);
-            // operands swapped: each 16 x 16 piece comes out transposed, lane (g, r16)
-            // holding row r16 and columns 4 g .. 4 g + 3
-#pragma unroll
-            for (int h = 0; h < 2; ++h)
-#pragma unroll
-                for (int i = 0; i < MI; ++i) {
-                    if (kSecond) {
-#pragma unroll
-                        for (int d = 0; d < 2 * kLoads; ++d)
-                            if (d * MI / kLoads == h * MI + i) send(kb + 1, qa, d);
-                    }
-#pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fb[h][j], fa[h][i], acc[i][j], 0, 0, 0);
-                    if (kSecond) __builtin_amdgcn_sched_barrier(0);
-                }
-            __builtin_amdgcn_s_setprio(0);
-            if (!kSecond) wait_vmcnt<kLoads>();
-            block_barrier();
-        }
-    };
-    A.issue(0, steps, slot(0), w);
-    B.issue(0, steps, slot(1), w);
-    A.issue(1, steps, slot(2), w);
-    wait_vmcnt<kLoads>();
+    const Ring<OpA, OpB> ring = {A, B, (a.K + kStep - 1) / kStep, lds, w};
+    ring.first();
     block_barrier();
     if (wm == 0) {
-        group(std::false_type());
+        multiply<false, MI>(ring, acc);
         block_barrier();
     } else {
 #pragma unroll
-        for (int d = 0; d < 2 * kLoads; ++d) send(0, 0, d);
+        for (int d = 0; d < Ring<OpA, OpB>::kSend; ++d) ring.send(0, 0, d);
         block_barrier();  // half a step later
-        group(std::true_type());
+        multiply<true, MI>(ring, acc);
     }
     wait_vmcnt<0>();
     store_tile<DIR, MI>(a, t, acc, wm, t.n0 + 64 * wn);
@@ -407,7 +460,7 @@ __device__ __forceinline__ void run_half(const GroupedArgs& a, const Tile& t, ui
 
 template <int DIR>
 __global__ __launch_bounds__(512) void k_grouped_gemm_bf16(GroupedArgs a) {
-    __shared__ __attribute__((aligned(1024))) uint8_t s_ring[kSlots * kSlice];
+    __shared__ __attribute__((aligned(1024))) uint8_t s_ring[160 * 1024];
     Tile t;
     if (!find_tile<DIR, kTile>(a, &t)) return;
     const uint32_t lds = lds_offset(s_ring);
@@ -446,6 +499,22 @@ __global__ __launch_bounds__(256, 2) void k_grouped_gemm_bf16_half(GroupedArgs a
 }  // namespace
 
 hipError_t launch_grouped_gemm_bf16(int dir, const GroupedArgs& a, int64_t pairs, hipStream_t stream) {
+    // Few rows an expert: the kernel that streams the weights through registers.
+    // 64 tokens x top-6, 64 experts, 4096 x 4096: 346 against 375 us; one token on
+    // two experts, 1440 x 3608: 10.6 against 33 us (split reduction); 64 rows x
+    // 4096 x 4096 on 8 experts 54 against 63 us, 512 rows on 64 experts 353 against
+    // 375 us; at a mean of 15 rows, unevenly spread, 377 us either way.
+    if (dir == kForward && pairs <= 16 * (int64_t)a.rows.E) {
+        StreamArgs s;
+        s.rows = a.rows;
+        s.x = a.a;
+        s.b = a.b;
+        s.b_scales = nullptr;
+        s.out = (uint16_t*)a.c;
+        s.N = a.N;
+        s.K = a.K;
+        return launch_grouped_gemm_bf16_stream(s, pairs, stream);
+    }
     // Half tiles for the weight gradient: its reductions are a few steps long, and
     // one block's stores and first loads pass behind the other's MFMAs (4096 tokens
     // x top-6, 64 experts, 4096 x 4096: 1.12 ms; whole tiles 1.18 ms, and 1.14 ms

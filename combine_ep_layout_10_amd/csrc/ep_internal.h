@@ -151,12 +151,12 @@ struct GroupedArgs {
     int out_f32;  // kGradWeight: binary32 output
 };
 
-// Products with MXFP4 weights (ep_gemm_mxfp4.hip).
-struct Mxfp4Args {
+// Products that stream their weights for few rows (ep_gemm_stream.hip).
+struct StreamArgs {
     RowsArgs rows;
     const uint16_t* x;        // bf16 [rows, K]
-    const uint8_t* b;         // [E, N, K / 2]
-    const uint8_t* b_scales;  // [E, N, K / 32]
+    const void* b;            // MXFP4 codes [E, N, K / 2], or bf16 [E, N, K]
+    const uint8_t* b_scales;  // MXFP4: [E, N, K / 32]
     uint16_t* out;            // bf16 [rows, N]
     int N, K;
 };
@@ -224,7 +224,8 @@ hipError_t launch_weight_grad(const WeightGradArgs& a, hipStream_t stream);
 hipError_t launch_grouped_gemm_fp8(const GemmArgs& a, int64_t rows_bound, hipStream_t stream);
 // pairs: num_tokens * num_topk, the most rows that hold a pair.
 hipError_t launch_grouped_gemm_bf16(int dir, const GroupedArgs& a, int64_t pairs, hipStream_t stream);
-hipError_t launch_grouped_gemm_mxfp4(const Mxfp4Args& a, int64_t pairs, hipStream_t stream);
+hipError_t launch_grouped_gemm_bf16_stream(const StreamArgs& a, int64_t pairs, hipStream_t stream);
+hipError_t launch_grouped_gemm_mxfp4(const StreamArgs& a, int64_t pairs, hipStream_t stream);
 hipError_t launch_rms_norm(const NormArgs& a, hipStream_t stream);
 hipError_t launch_rms_norm_backward(const NormBackwardArgs& a, hipStream_t stream);
 // Kernel arguments of the single-launch layout + dispatch, packed into the

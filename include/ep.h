@@ -339,8 +339,9 @@ ep_status ep_grouped_gemm_fp8(const ep_handle* h, const void* a, const float* a_
  * (output channels) and k (input channels; not tied to cfg.hidden, so that an
  * expert's second layer is the same call) are multiples of 8, at most 2^20
  * (EP_ERR_UNSUPPORTED above). Products of bf16 values are summed in binary32
- * by the MFMA, in an order that depends on n, k and the live rows alone, and
- * rounded once, to nearest even.
+ * by the MFMA and rounded once, to nearest even. The order of a sum depends on
+ * n, k, the config, num_tokens and the counts, never on the device, the launch
+ * or other experts' rows: the same call gives the same bits again.
  *
  * Forward: for every live row r of expert e and c < n,
  *   out[r, c] = bf16( sum_j a[r, j] * b[e, c, j] ),  j < k.
