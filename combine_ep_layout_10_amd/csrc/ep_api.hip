@@ -233,6 +233,14 @@ ep_status check_product(const ep_handle* h, int32_t n, int32_t k, int k_multiple
     return EP_OK;
 }
 
+// A launcher returns hipErrorInvalidConfiguration, and launches nothing, when the
+// product's tiles are more than one launch holds.
+ep_status product_fail(hipError_t e, const char* what) {
+    if (e == hipErrorInvalidConfiguration)
+        return fail(EP_ERR_UNSUPPORTED, "the product has more tiles than one launch holds (2^32 threads)");
+    return hip_fail(e, what);
+}
+
 // Checks a BF16 product and launches it. x, y: the operands; xn, yn, cn: what the
 // caller calls them and the output.
 ep_status do_grouped_gemm_bf16(int dir, const ep_handle* h, const void* x, const char* xn, const void* y,
@@ -258,12 +266,14 @@ ep_status do_grouped_gemm_bf16(int dir, const ep_handle* h, const void* x, const
     a.K = dir == ep::kForward ? k : n;
     a.out_f32 = out_f32;
     hipError_t e = ep::launch_grouped_gemm_bf16(dir, a, pairs, stream);
-    if (e != hipSuccess) return hip_fail(e, "BF16 grouped GEMM launch");
+    if (e != hipSuccess) return product_fail(e, "BF16 grouped GEMM launch");
     return EP_OK;
 }
 
 ep_status check_norm(int32_t num_tokens, int32_t hidden) {
     if (num_tokens < 0) return fail(EP_ERR_INVALID_ARG, "num_tokens %d must not be negative", num_tokens);
+    if (num_tokens > ep::kMaxNormTokens)
+        return fail(EP_ERR_UNSUPPORTED, "num_tokens %d exceeds %d", num_tokens, ep::kMaxNormTokens);
     if (hidden < 8 || hidden % 8 != 0)
         return fail(EP_ERR_INVALID_ARG, "hidden %d must be a positive multiple of 8", hidden);
     if (hidden > ep::kMaxNormHidden)
@@ -669,7 +679,7 @@ ep_status ep_grouped_gemm_mxfp4(const ep_handle* h, const void* a, const void* b
     g.N = n;
     g.K = k;
     hipError_t e = ep::launch_grouped_gemm_mxfp4(g, pairs, (hipStream_t)stream);
-    if (e != hipSuccess) return hip_fail(e, "MXFP4 grouped GEMM launch");
+    if (e != hipSuccess) return product_fail(e, "MXFP4 grouped GEMM launch");
     return EP_OK;
 }
 

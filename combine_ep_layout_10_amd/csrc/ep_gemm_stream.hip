@@ -303,7 +303,7 @@ template <template <int, int> class WT, int TB, int MC, int S>
 hipError_t launch(const StreamArgs& a, int64_t pairs, hipStream_t stream) {
     constexpr int kCols = 16 * MC * kWaves / S;
     const int64_t blocks = max_row_tiles(a.rows, TB, pairs) * ((a.N + kCols - 1) / kCols);
-    if (blocks > 0x7FFFFF) return hipErrorInvalidValue;  // 2^32 threads a launch
+    if (blocks > 0x7FFFFF) return hipErrorInvalidConfiguration;
     if (launch_debug())
         launch_debug_print("k_grouped_gemm_stream", dim3((unsigned)blocks), dim3(64 * kWaves),
                            "rows %d split %d n %d k %d", TB, S, a.N, a.K);

@@ -188,6 +188,8 @@ struct NormBackwardArgs {
 
 // Channels of a norm's row: at most 4 vectors of 8 for each of 1,024 lanes.
 constexpr int kMaxNormHidden = 1 << 15;
+// Tokens: a launch holds less than 2^32 threads, and a row takes up to 1,024.
+constexpr int kMaxNormTokens = (1 << 22) - 1;
 // Blocks of the norm's backward at most, each with its own partial sum of the
 // weight gradient: two a CU of 256, a constant, so that results never depend on
 // the device's CU count.

@@ -308,9 +308,7 @@ void norm_backward_launch(const NormBackwardArgs& a, const RowShape& s, dim3 gri
 hipError_t launch_rms_norm(const NormArgs& a, hipStream_t stream) {
     if (a.T == 0) return hipSuccess;
     const RowShape s = row_shape(a.H);
-    const int64_t blocks = ((int64_t)a.T + s.rows - 1) / s.rows;
-    if (blocks * s.threads * s.rows > 0xFFFFFFFFll) return hipErrorInvalidValue;  // 2^32 threads a launch
-    const dim3 grid((unsigned)blocks);
+    const dim3 grid((unsigned)((a.T + s.rows - 1) / s.rows));
     if (launch_debug())
         launch_debug_print("k_rms_norm", grid, dim3((unsigned)(s.threads * s.rows)), "hidden %d", a.H);
     if (s.v <= 1) norm_launch<1>(a, s, grid, stream);
@@ -321,8 +319,7 @@ hipError_t launch_rms_norm(const NormArgs& a, hipStream_t stream) {
 
 hipError_t launch_rms_norm_backward(const NormBackwardArgs& a, hipStream_t stream) {
     const RowShape s = row_shape(a.H);
-    const int64_t need = ((int64_t)a.T + s.rows - 1) / s.rows;
-    const int parts = (int)(need < kNormParts ? need : kNormParts);
+    const int need = (a.T + s.rows - 1) / s.rows, parts = need < kNormParts ? need : kNormParts;
     const dim3 grid((unsigned)parts);
     if (launch_debug())
         launch_debug_print("k_rms_norm_backward", grid, dim3((unsigned)(s.threads * s.rows)), "hidden %d", a.H);

@@ -350,7 +350,9 @@ ep_status ep_grouped_gemm_fp8(const ep_handle* h, const void* a, const float* a_
  *        ep_grouped_gemm_fp8's.
  *   out  device bf16 [rows bound, n]. COMPACT padding rows are zero-filled
  *        unless EP_FLAG_NO_ZERO_PAD; no other row is touched. Must not overlap
- *        an operand (also below). */
+ *        an operand (also below).
+ * A product of more tiles than one launch holds (2^32 threads: about 8 million
+ * tiles of 256 rows by 256 columns) is EP_ERR_UNSUPPORTED (also below). */
 ep_status ep_grouped_gemm_bf16(const ep_handle* h, const void* a, const void* b, int32_t n, int32_t k, void* out,
                                void* stream);
 
@@ -409,8 +411,8 @@ ep_status ep_grouped_gemm_mxfp4(const ep_handle* h, const void* a, const void* b
  *   y         device bf16 or E4M3FN [num_tokens, hidden].
  *   y_scales  device binary32 [num_tokens, hidden / 128] for FP8, else NULL.
  *   rstd      device binary32 [num_tokens].
- * hidden is a multiple of 8 (FP8: of 128), at most 32768 (EP_ERR_UNSUPPORTED
- * above). */
+ * hidden is a multiple of 8 (FP8: of 128), at most 32768, num_tokens below 2^22
+ * (EP_ERR_UNSUPPORTED above). y must not overlap an input. */
 ep_status ep_rms_norm(int32_t num_tokens, int32_t hidden, int32_t dtype, const void* x, const void* residual,
                       const void* weight, float eps, void* total, void* y, float* y_scales, float* rstd,
                       void* stream);

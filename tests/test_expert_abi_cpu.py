@@ -68,6 +68,24 @@ def test_empty_batch_needs_no_pointers():
     assert l.ep_rms_norm(0, 64, F.EP_BF16, None, None, None, 1e-6, None, None, None, None, None) == F.EP_OK
 
 
+def test_more_tiles_than_a_launch_holds():
+    """Refused on the host, before anything is launched."""
+    l, big = F.lib(), 1 << 20
+    many = fake_handle(max_tokens=1 << 26, num_experts=1024, num_topk=16)
+    many.num_tokens = 1 << 26
+    h = ctypes.byref(many)
+    assert l.ep_grouped_gemm_bf16(h, FAKE, FAKE, big, 64, FAKE, None) == UNSUP
+    assert "tiles" in F.last_error_message()
+    assert l.ep_grouped_gemm_bf16_grad_input(h, FAKE, FAKE, 64, big, FAKE, None) == UNSUP
+    assert l.ep_grouped_gemm_bf16_grad_weight(h, FAKE, FAKE, big, big, 1, FAKE, None) == UNSUP
+    assert l.ep_grouped_gemm_mxfp4(h, FAKE, FAKE, FAKE, big, 64, FAKE, None) == UNSUP
+    few = fake_handle(max_tokens=1 << 13, num_experts=1024, num_topk=1)
+    few.num_tokens = 1 << 13                                  # 8 rows an expert: the streaming kernel
+    assert l.ep_grouped_gemm_bf16(ctypes.byref(few), FAKE, FAKE, big, 64, FAKE, None) == UNSUP
+    assert l.ep_rms_norm(1 << 22, 64, F.EP_BF16, FAKE, None, FAKE, 1e-6, None, FAKE, None, FAKE, None) == UNSUP
+    assert l.ep_rms_norm_workspace_bytes(1 << 22, 64) == 0
+
+
 def test_mxfp4_products():
     f, h = F.lib().ep_grouped_gemm_mxfp4, ctypes.byref(fake_handle())
     assert f(None, FAKE, FAKE, FAKE, 64, 64, FAKE, None) == BAD

@@ -410,6 +410,28 @@ def test_two_streams_at_once(direction):
             assert torch.equal(x[rows], w[rows])
 
 
+@pytest.mark.parametrize("direction", DIRS)
+def test_widest(direction):
+    """The widest rows of either side that are accepted. (The tolerance's K 2^-23
+    is 1/8 here: gamma = K u / (1 - K u) in its place.)"""
+    W = 1 << 20
+    gamma = W * 2.0 ** -23 / (1 - W * 2.0 ** -23)
+    h = make_handle(routing([1, 0, 2]), 3, 1)
+    for n, k in ((8, W), (W, 32)):
+        o = operands(direction, h, n, k)
+        got = call(direction, h, o)
+        for e, (first, live, _) in enumerate(o["rr"]):
+            rows = slice(first, first + live)
+            if direction == "grad_weight":
+                check(got[e], o["g"][rows].double().t(), o["a"][rows].double(), live, e)
+            elif live:
+                x = o["g" if direction == "grad_input" else "a"][rows].double()
+                w = o["w64"](e) if direction == "grad_input" else o["w64"](e).t()
+                want, size = x @ w, gamma * (x.abs() @ w.abs())
+                err = (got[rows].double() - want).abs()
+                assert bool((err <= size + 2.0 ** -8 * (want.abs() + size)).all()), e
+
+
 def test_far_offsets():
     """Operands and outputs past 2^32 bytes: the last experts of a wide stack."""
     E, n, k = 40, 4096, 16384                      # 5.4 GB of weights
