@@ -41,13 +41,12 @@
 // Half tiles (grad_weight, few tiles): 4 waves, 256 x 128, steps of 32, two blocks
 // a CU; described with them. Few rows an expert: ep_gemm_stream.hip.
 //
-// What bounds it, on MI355X: 65,536 rows x 4096 x 7168 on 32 experts take 3.2 ms
-// (1.20 PFLOP/s; a library product of 8192^3 reaches 1.46), the matrix units busy 61 %
-// of the cycles at the 1.7 GHz that the card holds under this load. In an interval
-// of the loop 512 cycles of MFMA stand in about 650; with operands that never leave
-// L2 the same loop takes 2.8 ms. The rest is tiles that are not full, and a tile's
-// first loads and stores. One wave a SIMD with 128 x 128 pieces and the
-// accumulators in AGPRs measured 3.6 ms, a ring of five steps of 32 as four.
+// What bounds it, on MI355X: 65,536 rows x 4096 x 7168 on 32 experts take 3.0 ms
+// (1.28 PFLOP/s; a library product of 8192^3 reaches 1.46) at the 1.7 GHz that the
+// card holds under this load. What is left: the LDS reads and DMA of one group that
+// take longer than the other's MFMAs, tiles that are not full, and a tile's first
+// loads and stores. One wave a SIMD with 128 x 128 pieces and the accumulators in
+// AGPRs measured 3.6 ms, a ring of five steps of 32 as four.
 #include "ep_mma_dev.h"
 #include "ep_rows_dev.h"
 
@@ -56,7 +55,7 @@ namespace ep {
 namespace {
 
 constexpr int kTile = 256;     // rows of a tile
-constexpr int kGroupRows = 8;  // row tiles that share column tiles in the block order
+constexpr int kGroupRows = 4;  // row tiles that share column tiles in the block order
 
 struct Tile {
     int e;          // expert
@@ -67,15 +66,17 @@ struct Tile {
 };
 
 // Tile of logical block `local` among an expert's nt_m x nt_n: groups of
-// about kGroupRows row tiles, within a group column by column, so that blocks that
-// run together on an XCD share few operand tiles.
+// kGroupRows row tiles, within a group column by column, so that blocks that run
+// together on an XCD share few operand tiles; a last, shorter row tile comes in a
+// group of its own or with few others, and does not put the long ones out of step.
+// 65,536 rows x 4096 x 7168 on 32 experts: groups of 4, 8, 16 fetch 9.4, 12.0, 14.9
+// GB into L2 in 3.24, 3.24, 3.28 ms.
 __device__ __forceinline__ void order_tiles(int local, int nt_m, int nt_n, int* m, int* n) {
-    const int groups = max(1, (nt_m + kGroupRows / 2) / kGroupRows), size = (nt_m + groups - 1) / groups;
-    const int g = local / (size * nt_n);
-    const int in_group = min(size, nt_m - g * size);
-    const int rem = local - g * size * nt_n;
+    const int g = local / (kGroupRows * nt_n);
+    const int in_group = min(kGroupRows, nt_m - g * kGroupRows);
+    const int rem = local - g * kGroupRows * nt_n;
     *n = rem / in_group;
-    *m = g * size + rem % in_group;
+    *m = g * kGroupRows + rem % in_group;
 }
 
 // This block's tile of kTile rows by COLS columns; false when it has none.
@@ -277,16 +278,16 @@ __device__ __forceinline__ void init_operands(const GroupedArgs& a, const Tile& 
 // (while group 0 computes step kb); step kb - 1 has been read by both when interval
 // 2 kb begins, and its place is filled again from then on.
 //   256 rows: five slots of 32 KiB; slice q (A of step q / 2 when even, B when odd)
-//   lives in slot q mod 5, and interval 2 kb sends slices 2 kb + 3 and 2 kb + 4.
+//   lives in slot q mod 5; interval 2 kb sends slice 2 kb + 3, the next 2 kb + 4.
 //   Fewer rows leave room for more steps: 128 rows three, 64 rows four (step kb in
-//   place kb mod kSteps), and interval 2 kb sends step kb + kSteps - 1.
+//   place kb mod kSteps); interval 2 kb sends B of step kb + kSteps - 1, the next A.
 template <class OpA, class OpB>
 struct Ring {
     static constexpr bool kSlots = OpA::kSlice == OpB::kSlice;
     static constexpr int kBytes = 160 * 1024;
     static constexpr int kStepBytes = OpA::kSlice + OpB::kSlice, kSteps = kBytes / kStepBytes;
     static constexpr int kSend = OpA::kLoads + OpB::kLoads;  // loads of a wave for an interval
-    // a wave's loads that may be on their way when step kb + 1 has landed, those of interval 2 kb sent
+    // a wave's loads that may be on their way when step kb + 1 has landed, those of interval 2 kb + 1 sent
     static constexpr int kKeep = kSlots ? OpA::kLoads : (kSteps - 2) * kSend;
 
     const OpA& A;
@@ -318,27 +319,28 @@ struct Ring {
         }
         wait_vmcnt<kKeep>();
     }
-    // load d of interval 2 kb
-    __device__ __forceinline__ void send(int kb, int place, int d) const {
-        if (kSlots) {
-            if (d < OpB::kLoads) B.issue(kb + 1, steps, lds + wrap(place + 3, 5) * OpA::kSlice, w, d);
-            else A.issue(kb + 2, steps, lds + wrap(place + 4, 5) * OpA::kSlice, w, d - OpB::kLoads);
-        } else {
-            const uint32_t to = at_a(wrap(place + kSteps - 1, kSteps));
-            if (d < OpB::kLoads) B.issue(kb + kSteps - 1, steps, to + OpA::kSlice, w, d);
-            else A.issue(kb + kSteps - 1, steps, to, w, d - OpB::kLoads);
-        }
+    // load d of what interval 2 kb sends (a slice of B), and the next one (a slice of A)
+    __device__ __forceinline__ void send_b(int kb, int place, int d) const {
+        if (kSlots) B.issue(kb + 1, steps, lds + wrap(place + 3, 5) * OpA::kSlice, w, d);
+        else B.issue(kb + kSteps - 1, steps, at_a(wrap(place + kSteps - 1, kSteps)) + OpA::kSlice, w, d);
+    }
+    __device__ __forceinline__ void send_a(int kb, int place, int d) const {
+        if (kSlots) A.issue(kb + 2, steps, lds + wrap(place + 4, 5) * OpA::kSlice, w, d);
+        else A.issue(kb + kSteps - 1, steps, at_a(wrap(place + kSteps - 1, kSteps)), w, d);
     }
 };
 
 // The loop of one group of waves over all steps. Every wave sends its part of an
-// interval's loads: group 0 behind its LDS reads, group 1 (SECOND) spread between
-// its MFMAs, since a DMA of 1 KiB occupies the CU's address unit for 16 cycles and
-// all of them together held up the MFMAs. The loads that step kb + 1 needs are
-// waited for by every wave before the barrier that ends interval 2 kb + 1.
+// interval's loads: the group that reads LDS behind its reads, the one that
+// computes spread between its MFMAs. A DMA of 1 KiB occupies the CU's address unit
+// for 16 cycles, so the loads of a step take 1024 of its 2048 cycles there: sent
+// in one interval of the two, they held up the MFMAs (clock reads in the loop:
+// 1,400 to 1,800 cycles for 1,024 of MFMA). What step kb + 1 needs is waited for by
+// every wave before the barrier that ends interval 2 kb + 1.
 template <bool SECOND, int MI, class OpA, class OpB>
 __device__ __forceinline__ void multiply(const Ring<OpA, OpB>& ring, f32x4_t (&acc)[MI][4]) {
     using R = Ring<OpA, OpB>;
+    constexpr int kSpread = SECOND ? OpB::kLoads : OpA::kLoads;
     int place = 0;
     for (int kb = 0; kb < ring.steps; ++kb) {
         const uint32_t at_a = ring.at_a(place), at_b = ring.at_b(place);
@@ -351,13 +353,16 @@ __device__ __forceinline__ void multiply(const Ring<OpA, OpB>& ring, f32x4_t (&a
             for (int i = 0; i < MI; ++i) fa[h][i] = ring.A.template read<2>(at_a, h, i);
         }
         if (SECOND) {
+#pragma unroll
+            for (int d = 0; d < OpA::kLoads; ++d) ring.send_a(kb, place, d);
             wait_vmcnt<R::kKeep>();
         } else {
 #pragma unroll
-            for (int d = 0; d < R::kSend; ++d) ring.send(kb, place, d);
+            for (int d = 0; d < OpB::kLoads; ++d) ring.send_b(kb, place, d);
         }
         wait_lgkmcnt0();
         block_barrier();
+        const int here = place;
         place = R::next(place);
         __builtin_amdgcn_s_setprio(1);
         // operands swapped: each 16 x 16 piece comes out transposed, lane (g, r16)
@@ -366,15 +371,16 @@ __device__ __forceinline__ void multiply(const Ring<OpA, OpB>& ring, f32x4_t (&a
         for (int h = 0; h < 2; ++h)
 #pragma unroll
             for (int i = 0; i < MI; ++i) {
-                if (SECOND) {
 #pragma unroll
-                    for (int d = 0; d < R::kSend; ++d)
-                        if (d * 2 * MI / R::kSend == h * MI + i) ring.send(kb + 1, place, d);
-                }
+                for (int d = 0; d < kSpread; ++d)
+                    if (d * 2 * MI / kSpread == h * MI + i) {
+                        if (SECOND) ring.send_b(kb + 1, place, d);
+                        else ring.send_a(kb, here, d);
+                    }
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
                     acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fb[h][j], fa[h][i], acc[i][j], 0, 0, 0);
-                if (SECOND) __builtin_amdgcn_sched_barrier(0);
+                __builtin_amdgcn_sched_barrier(0);
             }
         __builtin_amdgcn_s_setprio(0);
         if (!SECOND) wait_vmcnt<R::kKeep>();
@@ -405,7 +411,7 @@ __device__ __forceinline__ void run_tile(const GroupedArgs& a, const Tile& t, ui
         block_barrier();
     } else {
 #pragma unroll
-        for (int d = 0; d < Ring<OpA, OpB>::kSend; ++d) ring.send(0, 0, d);
+        for (int d = 0; d < OpB::kLoads; ++d) ring.send_b(0, 0, d);
         block_barrier();  // half a step later
         multiply<true, MI>(ring, acc);
     }
@@ -543,7 +549,7 @@ hipError_t launch_grouped_gemm_bf16(int dir, const GroupedArgs& a, int64_t pairs
                                               : max_row_tiles(a.rows, kTile, pairs);
     const int64_t blocks = mtiles * nt_n;
     if (blocks == 0) return hipSuccess;
-    if (blocks > 0xFFFFFFFFll / threads) return hipErrorInvalidValue;  // 2^32 threads a launch
+    if (blocks > 0xFFFFFFFFll / threads) return hipErrorInvalidConfiguration;
     const dim3 grid((unsigned)blocks), block(threads);
     if (launch_debug())
         launch_debug_print(half ? "k_grouped_gemm_bf16_half" : "k_grouped_gemm_bf16", grid, block, "direction %d n %d",
