@@ -193,68 +193,51 @@ struct Operand {
     }
 };
 
-// `past_cache`: a weight gradient larger than the 256 MB that the memory side
-// caches. Its stores do not stay in L2, where they would take the operands' place
-// (24,576 rows, 64 experts, 4096 x 4096: bf16 1.06 against 1.14 ms, binary32 1.52
-// against 1.73 ms); a smaller one is better kept (91 MB: 38 against 41 us), and so
-// are rows, which the next call reads.
-__device__ __forceinline__ void store16(void* to, bool past_cache, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
-    const u32x4_t v = {x, y, z, w};
-    if (past_cache) __builtin_nontemporal_store(v, (u32x4_t*)to);
-    else *(u32x4_t*)to = v;
-}
-
 // Stores of a wave's MI x 4 pieces: row piece 2 i + wm, columns col .. col + 63.
 // The MFMA leaves 16 rows in 16 lanes and 4 columns in each of the four lane
-// groups; values are exchanged between lanes first, so that every store writes
-// whole 128-byte lines of 8 rows.
+// groups; each 16 rows are turned through the wave's own kStoreLds bytes of LDS at
+// `lds`, so that neighbouring lanes store neighbouring columns (a weight gradient of
+// 64 x 4096 x 4096 from 24,576 rows: 1.06 ms, binary32 1.43; by exchanges between
+// lanes that leave 8 rows side by side, in whole lines as well, 1.09 and 1.49). A
+// wave's LDS accesses stay in order. 16-byte chunks are stored XORed with the row
+// (binary32), with half the row (bf16, two rows in the 64 banks): reads and writes
+// without conflicts.
+constexpr int kStoreLds = 4096;
+
 template <int DIR, int MI>
-__device__ __forceinline__ void store_tile(const GroupedArgs& a, const Tile& t, const f32x4_t (&acc)[MI][4], int wm, int col) {
+__device__ __forceinline__ void store_tile(const GroupedArgs& a, const Tile& t, const f32x4_t (&acc)[MI][4], int wm, int col,
+                                           uint32_t lds) {
     int lane = lane_id();
     asm volatile("" : "+v"(lane));  // worked out here: kept over the main loop, its terms would cost registers
-    const int r8 = lane & 7, g = lane >> 4;
-    const bool bit3 = lane & 8;
-    const bool past_cache =
-        DIR == kGradWeight && (int64_t)a.rows.E * a.M * a.N * (a.out_f32 ? 4 : 2) > (int64_t)(256 << 20);
+    const int r16 = lane & 15, g = lane >> 4;
     const int64_t first = (DIR == kGradWeight ? (int64_t)t.e * a.M : (int64_t)t.er.first) + t.m0;
 #pragma unroll
     for (int i = 0; i < MI; ++i) {
-        const int row = 16 * (2 * i + wm) + r8;  // and 8 further
+        const int row = 16 * (2 * i + wm);
         if (DIR == kGradWeight && a.out_f32) {
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {  // 32 columns
-                uint32_t v[2][4];
+            for (int j = 0; j < 4; ++j)
+                write_lds(lds + r16 * 256 + (((4 * j + g) ^ r16) << 4), __builtin_bit_cast(u32x4_t, acc[i][j]));
+            const int c = col + 4 * r16;  // lane (g, r16) stores row 4 s + g, chunk r16
 #pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    v[0][q] = __float_as_uint(acc[i][2 * h][q]);
-                    v[1][q] = __float_as_uint(acc[i][2 * h + 1][q]);
-                    exchange8(v[0][q], v[1][q], bit3);
-                }
-                const int c = col + 32 * h + (bit3 ? 16 : 0) + 4 * g;
-#pragma unroll
-                for (int s = 0; s < 2; ++s)
-                    if (row + 8 * s < t.rows && c < a.N)
-                        store16((float*)a.c + (first + row + 8 * s) * a.N + c, past_cache, v[s][0], v[s][1], v[s][2], v[s][3]);
+            for (int s = 0; s < 4; ++s) {
+                const int r = 4 * s + g;
+                const u32x4_t v = read_lds_words(lds + r * 256 + ((r16 ^ r) << 4));
+                if (row + r < t.rows && c < a.N) *(u32x4_t*)((float*)a.c + (first + row + r) * a.N + c) = v;
             }
         } else {
-            uint32_t v[2][4];  // halves of 32 columns, then rows r8 and r8 + 8
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-#pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    v[h][j] = pack_bf16x2(acc[i][2 * h + j][0], acc[i][2 * h + j][1]);
-                    v[h][2 + j] = pack_bf16x2(acc[i][2 * h + j][2], acc[i][2 * h + j][3]);
-                }
-                gather_pairs(v[h][0], v[h][1]);
-                gather_pairs(v[h][2], v[h][3]);
+            for (int j = 0; j < 4; ++j) {
+                const u32x2_t v = {pack_bf16x2(acc[i][j][0], acc[i][j][1]), pack_bf16x2(acc[i][j][2], acc[i][j][3])};
+                write_lds(lds + r16 * 128 + (((2 * j + (g >> 1)) ^ (r16 >> 1)) << 4) + (g & 1) * 8, v);
             }
+            const int c = col + 8 * (lane & 7);  // lane stores row 8 s + lane / 8, chunk lane % 8
 #pragma unroll
-            for (int q = 0; q < 4; ++q) exchange8(v[0][q], v[1][q], bit3);
-            const int c = col + (bit3 ? 32 : 0) + 8 * g;
-#pragma unroll
-            for (int s = 0; s < 2; ++s)
-                if (row + 8 * s < t.rows && c < a.N)
-                    store16((uint16_t*)a.c + (first + row + 8 * s) * a.N + c, past_cache, v[s][0], v[s][2], v[s][1], v[s][3]);
+            for (int s = 0; s < 2; ++s) {
+                const int r = 8 * s + (lane >> 3);
+                const u32x4_t v = read_lds_words(lds + r * 128 + (((lane & 7) ^ (r >> 1)) << 4));
+                if (row + r < t.rows && c < a.N) *(u32x4_t*)((uint16_t*)a.c + (first + row + r) * a.N + c) = v;
+            }
         }
     }
 }
@@ -416,7 +399,8 @@ __device__ __forceinline__ void run_tile(const GroupedArgs& a, const Tile& t, ui
         multiply<true, MI>(ring, acc);
     }
     wait_vmcnt<0>();
-    store_tile<DIR, MI>(a, t, acc, wm, t.n0 + 64 * wn);
+    block_barrier();  // no wave reads or fills the ring any more
+    store_tile<DIR, MI>(a, t, acc, wm, t.n0 + 64 * wn, lds + w * kStoreLds);
     if (a.rows.zero_pad && t.last_rows) clear_padding((uint16_t*)a.c, a.N, t.er, t.n0, kTile);
 }
 
@@ -470,7 +454,8 @@ __device__ __forceinline__ void run_half(const GroupedArgs& a, const Tile& t, ui
         st = st == kHalfStages - 1 ? 0 : st + 1;
     }
     wait_vmcnt<0>();
-    store_tile<DIR, MI>(a, t, acc, wm, t.n0 + 64 * wn);
+    block_barrier();  // no wave reads or fills the ring any more
+    store_tile<DIR, MI>(a, t, acc, wm, t.n0 + 64 * wn, lds + w * kStoreLds);
     if (DIR != kGradWeight && a.rows.zero_pad && t.last_rows)
         clear_padding((uint16_t*)a.c, a.N, t.er, t.n0, kHalf);
 }

@@ -78,24 +78,12 @@ __device__ __forceinline__ int row_swizzle16(int r) { return -(r >> 2) & 3; }
 typedef __attribute__((address_space(3))) bf16x8_t lds_bf16x8_t;
 __device__ __forceinline__ bf16x8_t read_lds(uint32_t lds) { return *(const lds_bf16x8_t*)lds; }
 
-// Rearranges words r[0], r[1] of the four groups of 16 lanes, word j of group g
-// being unit 4 j + g, so that group g holds units 2 g and 2 g + 1.
-__device__ __forceinline__ void gather_pairs(uint32_t& r0, uint32_t& r1) {
-    typedef unsigned int u32x2_t __attribute__((ext_vector_type(2)));
-    const u32x2_t x = __builtin_amdgcn_permlane32_swap(r0, r1, false, false);
-    const u32x2_t y = __builtin_amdgcn_permlane16_swap(x[0], x[1], false, false);
-    r0 = y[0];
-    r1 = y[1];
-}
-
-// Exchanges word r1 of the lanes with bit 3 clear with word r0 of those with it
-// set: register s then holds what the lanes with bit 3 equal to s held, words 0
-// and 1 in the lanes with bit 3 clear and set.
-__device__ __forceinline__ void exchange8(uint32_t& r0, uint32_t& r1, bool bit3) {
-    const uint32_t give = bit3 ? r0 : r1;
-    const uint32_t take = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)give, 0x128, 0xF, 0xF, false);  // row_ror:8
-    r0 = bit3 ? take : r0;
-    r1 = bit3 ? r1 : take;
-}
+// Words to and from LDS at a byte address; any of these may alias.
+typedef unsigned int u32x2_t __attribute__((ext_vector_type(2)));
+typedef u32x2_t __attribute__((address_space(3), may_alias)) lds_u32x2_t;
+typedef u32x4_t __attribute__((address_space(3), may_alias)) lds_u32x4_t;
+__device__ __forceinline__ void write_lds(uint32_t lds, u32x2_t v) { *(lds_u32x2_t*)lds = v; }
+__device__ __forceinline__ void write_lds(uint32_t lds, u32x4_t v) { *(lds_u32x4_t*)lds = v; }
+__device__ __forceinline__ u32x4_t read_lds_words(uint32_t lds) { return *(const lds_u32x4_t*)lds; }
 
 }  // namespace ep
