@@ -36,17 +36,18 @@
 // c ^ (r / 2 mod 8). The other operands have a row of columns for each k and are
 // read through the transposing LDS read, 4 k by 16 columns; their 32-byte pair of
 // chunks p of row k is stored at p ^ f(k), f(k) = k mod 4 + 4 (k / 8 mod 2). Either
-// way a read meets each bank once (SQ_LDS_BANK_CONFLICT 0).
+// way a read meets each bank once (no cycle of SQ_LDS_BANK_CONFLICT).
 //
 // Half tiles (grad_weight, few tiles): 4 waves, 256 x 128, steps of 32, two blocks
 // a CU; described with them. Few rows an expert: ep_gemm_stream.hip.
 //
-// What bounds it, on MI355X: 65,536 rows x 4096 x 7168 on 32 experts take 3.0 ms
-// (1.28 PFLOP/s; a library product of 8192^3 reaches 1.46) at the 1.7 GHz that the
-// card holds under this load. What is left: the LDS reads and DMA of one group that
-// take longer than the other's MFMAs, tiles that are not full, and a tile's first
-// loads and stores. One wave a SIMD with 128 x 128 pieces and the accumulators in
-// AGPRs measured 3.6 ms, a ring of five steps of 32 as four.
+// What bounds it, on MI355X: 65,536 rows x 4096 x 7168 on 32 experts take 2.9 to 3.0
+// ms (1.3 PFLOP/s; a library product of 8192^3 reaches 1.46), the matrix units busy
+// 73 % of the cycles at the 1.7 GHz that the card holds under this load. The rest is
+// the LDS reads and DMA of one group that take longer than the other's MFMAs, tiles
+// that are not full, and a tile's first loads and stores. One wave a SIMD with 128 x
+// 128 pieces and the accumulators in AGPRs measured 3.6 ms (3.4 then), a ring of five
+// steps of 32 as four.
 #include "ep_mma_dev.h"
 #include "ep_rows_dev.h"
 
@@ -70,7 +71,7 @@ struct Tile {
 // together on an XCD share few operand tiles; a last, shorter row tile comes in a
 // group of its own or with few others, and does not put the long ones out of step.
 // 65,536 rows x 4096 x 7168 on 32 experts: groups of 4, 8, 16 fetch 9.4, 12.0, 14.9
-// GB into L2 in 3.24, 3.24, 3.28 ms.
+// GB into L2 (in 3.24, 3.24, 3.28 ms then).
 __device__ __forceinline__ void order_tiles(int local, int nt_m, int nt_n, int* m, int* n) {
     const int g = local / (kGroupRows * nt_n);
     const int in_group = min(kGroupRows, nt_m - g * kGroupRows);
@@ -200,8 +201,8 @@ struct Operand {
 // 64 x 4096 x 4096 from 24,576 rows: 1.06 ms, binary32 1.43; by exchanges between
 // lanes that leave 8 rows side by side, in whole lines as well, 1.09 and 1.49). A
 // wave's LDS accesses stay in order. 16-byte chunks are stored XORed with the row
-// (binary32), with half the row (bf16, two rows in the 64 banks): reads and writes
-// without conflicts.
+// (binary32), with half the row (bf16, two rows in the 64 banks), so that a read
+// meets each bank once (512 cycles of bank conflicts a tile are left, of the writes).
 constexpr int kStoreLds = 4096;
 
 template <int DIR, int MI>
@@ -518,13 +519,15 @@ hipError_t launch_grouped_gemm_bf16(int dir, const GroupedArgs& a, int64_t pairs
         return launch_grouped_gemm_bf16_stream(s, pairs, stream);
     }
     // Half tiles for the weight gradient: its reductions are a few steps long, and
-    // one block's stores and first loads pass behind the other's MFMAs (4096 tokens
-    // x top-6, 64 experts, 4096 x 4096: 1.12 ms; whole tiles 1.18 ms, and 1.14 ms
-    // with blocks that take tile after tile). Also where whole tiles would leave
+    // one block's first loads pass behind the other's MFMAs (4096 tokens x top-6, 64
+    // experts, 4096 x 4096: 1.06 ms; whole tiles 1.10 ms; blocks that take a run of
+    // half tiles and send the next one's first steps ahead of their stores 1.18 ms:
+    // the loop alone takes 0.69 ms and the stores alone 0.36 ms, one after the
+    // other or side by side). Also where whole tiles would leave
     // half the CUs without one: 16 rows x 4096 x 4096 on 8 experts 63 against 77 us,
     // 480 rows x 2240 x 2832 on 8 experts 36 against 49 us; with 144 whole tiles 29
     // against 27 us. Otherwise whole tiles, which read and move half as much a MFMA:
-    // 65,536 rows x 4096 x 7168 on 32 experts 3.2 against 4.7 ms. Never by the
+    // 65,536 rows x 4096 x 7168 on 32 experts 3.0 against 4.7 ms. Never by the
     // device's real CU count: the order of the sums must not depend on it.
     const int64_t row_tiles = pairs / kTile > a.rows.E ? pairs / kTile : pairs < a.rows.E ? pairs : a.rows.E;
     const bool half = dir == kGradWeight || row_tiles * ((a.N + kTile - 1) / kTile) <= 128;
