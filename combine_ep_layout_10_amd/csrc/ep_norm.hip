@@ -51,11 +51,22 @@ __device__ __forceinline__ float row_sum(float v, float* tmp) {
     return s;
 }
 
-// max over 16 consecutive lanes
-__device__ __forceinline__ float max16_dpp(float v) {
-    v = max8_dpp(v);
-    const int x = __float_as_int(v);
-    return fmaxf(v, __int_as_float(__builtin_amdgcn_update_dpp(0, x, 0x140, 0xF, 0xF, false)));  // row_mirror
+// max|f| over the channels of a block: the 8 of each of 16 consecutive lanes, NaN
+// when one of them is (fmaxf would drop it). Magnitudes order like their bit
+// patterns, with NaN above infinity.
+template <int CTRL>
+__device__ __forceinline__ uint32_t max_with(uint32_t v) {
+    return max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, 0xF, 0xF, false));
+}
+__device__ __forceinline__ float block_max(const float f[8]) {
+    uint32_t m = 0;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) m = max(m, __float_as_uint(f[j]) & 0x7FFFFFFFu);
+    m = max_with<0xB1>(m);   // quad_perm [1,0,3,2]
+    m = max_with<0x4E>(m);   // quad_perm [2,3,0,1]
+    m = max_with<0x141>(m);  // row_half_mirror
+    m = max_with<0x140>(m);  // row_mirror
+    return __uint_as_float(m);
 }
 
 // v = f / q, correctly rounded, for |f| <= 448 q (1 + 2^-23). With r the rounded
@@ -65,7 +76,8 @@ __device__ __forceinline__ float max16_dpp(float v) {
 // second makes it the rounded quotient. Five operations instead of a division's
 // dozen. The remainder keeps f's zeros' sign (y - rem * r), and is exact while
 // nothing underflows: |f / q| >= 2^-10, below which every code is a signed zero,
-// and q >= 2^-80 leave its last bit at 2^-136. Smaller and huge q divide.
+// and q >= 2^-80 leave its last bit at 2^-136. Smaller and huge q divide, and NaN
+// and infinite ones, whose NaN quotients stay NaN: only numbers are held to 448.
 __device__ __forceinline__ void quotients(const float f[8], float q, float v[8]) {
     if (q >= 0x1p-80f && q <= 0x1p100f) {
         const float r = 1.0f / q;
@@ -77,7 +89,10 @@ __device__ __forceinline__ void quotients(const float f[8], float q, float v[8])
         }
     } else {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] = fminf(fmaxf(f[j] / q, -448.0f), 448.0f);
+        for (int j = 0; j < 8; ++j) {
+            const float y = f[j] / q;
+            v[j] = y > 448.0f ? 448.0f : y < -448.0f ? -448.0f : y;
+        }
     }
 }
 
@@ -144,12 +159,9 @@ __global__ __launch_bounds__(1024) void k_rms_norm(NormArgs a) {
             for (int j = 0; j < 8; ++j) f[j] *= rstd;
             *(uint4*)((uint16_t*)a.y + row + 8 * c) = pack8(f);
         } else {
-            float amax = 0.0f;
-#pragma unroll
-            for (int j = 0; j < 8; ++j) amax = fmaxf(amax, fabsf(f[j]));
-            const float q = max16_dpp(amax) / 448.0f;
+            const float q = block_max(f) / 448.0f;
             uint32_t code[2] = {0u, 0u};
-            if (q > 0.0f) {
+            if (q != 0.0f) {
                 float v[8];
                 quotients(f, q, v);
 #pragma unroll

@@ -404,6 +404,10 @@ ep_status ep_grouped_gemm_mxfp4(const ep_handle* h, const void* a, const void* b
  *   y[t, c] = E4M3FN(u[c] / q) rounded to nearest even and saturated to +-448,
  *   y_scales = q * rstd[t] (q = 0: zero codes, scale 0). rstd multiplies a
  *   whole row and so enters the scale alone.
+ *   Infinities and NaN go by the same formulas, a NaN among the |u| being their
+ *   maximum: its 128 channels have NaN codes and a NaN scale; beside an infinite
+ *   u, which has a NaN code, the others have zero codes, and the scale is q * rstd
+ *   likewise, infinite (NaN where rstd is 0).
  *   x, residual, total  device bf16 [num_tokens, hidden]; total may be x's or
  *                       residual's own buffer.
  *   weight    device bf16 [hidden].
