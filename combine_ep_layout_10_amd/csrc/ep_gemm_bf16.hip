@@ -402,7 +402,7 @@ __device__ __forceinline__ void run_tile(const GroupedArgs& a, const Tile& t, ui
     wait_vmcnt<0>();
     block_barrier();  // no wave reads or fills the ring any more
     store_tile<DIR, MI>(a, t, acc, wm, t.n0 + 64 * wn, lds + w * kStoreLds);
-    if (a.rows.zero_pad && t.last_rows) clear_padding((uint16_t*)a.c, a.N, t.er, t.n0, kTile);
+    if (a.rows.zero_pad && t.last_rows) clear_padding<kTile>((uint16_t*)a.c, a.N, t.er, t.n0);
 }
 
 // ---------------------------------------------------------------- half tiles: 4 waves, 128 columns, two blocks a CU
@@ -458,7 +458,7 @@ __device__ __forceinline__ void run_half(const GroupedArgs& a, const Tile& t, ui
     block_barrier();  // no wave reads or fills the ring any more
     store_tile<DIR, MI>(a, t, acc, wm, t.n0 + 64 * wn, lds + w * kStoreLds);
     if (DIR != kGradWeight && a.rows.zero_pad && t.last_rows)
-        clear_padding((uint16_t*)a.c, a.N, t.er, t.n0, kHalf);
+        clear_padding<kHalf>((uint16_t*)a.c, a.N, t.er, t.n0);
 }
 
 template <int DIR>

@@ -290,7 +290,7 @@ __global__ __launch_bounds__(64 * kWaves) void k_grouped_gemm_stream(StreamArgs 
     const int m0 = __builtin_amdgcn_readfirstlane(m * each);
     const int rows = __builtin_amdgcn_readfirstlane(min(each, er.live - m0));
     const int n0 = __builtin_amdgcn_readfirstlane(local / nt_m * kCols);
-    if (a.rows.zero_pad && m == nt_m - 1) clear_padding(a.out, a.N, er, n0, kCols);
+    if (a.rows.zero_pad && m == nt_m - 1) clear_padding<kCols>(a.out, a.N, er, n0);
     switch ((rows + 15) / 16) {
         case 1: return run_tile<W, TB, MC, S, 1>(a, er, e, m0, rows, n0, s_x);
         case 2: if (TB >= 32) return run_tile<W, TB, MC, S, TB >= 32 ? 2 : 1>(a, er, e, m0, rows, n0, s_x); break;

@@ -94,15 +94,19 @@ inline int64_t max_row_tiles(const RowsArgs& a, int bm, int64_t pairs) {
     return pairs / bm + (pairs < a.E ? pairs : a.E);
 }
 
-// Zeros into columns [n0, n0 + width) of the expert's padding rows (bf16
-// output of N columns), by the whole block.
-__device__ __forceinline__ void clear_padding(uint16_t* out, int N, const ExpertRows& er, int n0, int width) {
-    const int per = width / 8;
-    for (int i = threadIdx.x; i < (er.owned - er.live) * per; i += blockDim.x) {
-        const int col = n0 + (i % per) * 8;
-        if (col < N)
-            *(uint4*)(out + ((int64_t)er.first + er.live + i / per) * N + col) = make_uint4(0u, 0u, 0u, 0u);
-    }
+// Zeros into columns [n0, n0 + WIDTH) of the expert's padding rows (bf16
+// output of N columns), by the whole block: a thread keeps its 8 columns and
+// steps over the rows. Rows are counted unsigned: there are less than 2^31 of
+// them, so a count one step past the last still fits, where a product of rows
+// and columns would not.
+template <int WIDTH>
+__device__ __forceinline__ void clear_padding(uint16_t* out, int N, const ExpertRows& er, int n0) {
+    constexpr int kPer = WIDTH / 8;  // threads of a row; divides the block
+    const int col = n0 + (int)threadIdx.x % kPer * 8;
+    if (col >= N) return;
+    const uint32_t rows = (uint32_t)(er.owned - er.live), step = blockDim.x / kPer;
+    uint16_t* at = out + ((int64_t)er.first + er.live) * N + col;
+    for (uint32_t r = threadIdx.x / kPer; r < rows; r += step) *(uint4*)(at + (int64_t)r * N) = make_uint4(0u, 0u, 0u, 0u);
 }
 
 }  // namespace ep
