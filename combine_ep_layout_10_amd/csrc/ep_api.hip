@@ -221,6 +221,9 @@ ep::RowsArgs rows_args(const ep_handle* h) {
 // Widths of a grouped product's rows: kernels take the byte offsets within a
 // tile of rows as 32-bit values.
 constexpr int kMaxProductWidth = 1 << 20;
+// Pairs of a BF16 product: kernels add an expert's rows, the number of its row
+// tiles (a 256th of them) and a step in 32 bits. (MXFP4: fewer fit a launch.)
+constexpr int64_t kMaxProductPairs = (1ll << 31) - (1 << 24);
 
 ep_status check_product(const ep_handle* h, int32_t n, int32_t k, int k_multiple) {
     ep_status s = check_handle(h);
@@ -249,6 +252,9 @@ ep_status do_grouped_gemm_bf16(int dir, const ep_handle* h, const void* x, const
     ep_status s = check_product(h, n, k, 8);
     if (s != EP_OK) return s;
     const int64_t pairs = (int64_t)h->num_tokens * h->cfg.num_topk;
+    if (pairs > kMaxProductPairs)
+        return fail(EP_ERR_UNSUPPORTED, "%lld token-expert pairs exceed %lld", (long long)pairs,
+                    (long long)kMaxProductPairs);
     const bool rows = pairs > 0;  // without a pair no operand is read, and only grad_weight writes
     if ((rows && x == nullptr) || !aligned(x, 16))
         return fail(EP_ERR_INVALID_ARG, "%s must be non-NULL and 16-byte aligned", xn);

@@ -352,7 +352,8 @@ ep_status ep_grouped_gemm_fp8(const ep_handle* h, const void* a, const float* a_
  *        unless EP_FLAG_NO_ZERO_PAD; no other row is touched. Must not overlap
  *        an operand (also below).
  * A product of more tiles than one launch holds (2^32 threads: about 8 million
- * tiles of 256 rows by 256 columns) is EP_ERR_UNSUPPORTED (also below). */
+ * tiles of 256 rows by 256 columns) is EP_ERR_UNSUPPORTED (also below), and so is
+ * one of more than 2^31 - 2^24 pairs (num_tokens * num_topk). */
 ep_status ep_grouped_gemm_bf16(const ep_handle* h, const void* a, const void* b, int32_t n, int32_t k, void* out,
                                void* stream);
 
