@@ -351,9 +351,11 @@ ep_status ep_grouped_gemm_fp8(const ep_handle* h, const void* a, const float* a_
  *   out  device bf16 [rows bound, n]. COMPACT padding rows are zero-filled
  *        unless EP_FLAG_NO_ZERO_PAD; no other row is touched. Must not overlap
  *        an operand (also below).
- * A product of more tiles than one launch holds (2^32 threads: about 8 million
- * tiles of 256 rows by 256 columns) is EP_ERR_UNSUPPORTED (also below), and so is
- * one of more than 2^31 - 2^24 pairs (num_tokens * num_topk). */
+ * More than 2^31 - 2^24 pairs (P = num_tokens * num_topk) are EP_ERR_UNSUPPORTED
+ * (also below), and so is a product of more tiles than one launch holds: with
+ * tiles of R rows, P / R + min(P, E) row tiles times the column tiles may be at
+ * most 2^23 - 1. Forward: for P <= 16 E tiles are 128 columns by R = 16 (32 for
+ * P > 6 E), otherwise 256 columns by R = 256. */
 ep_status ep_grouped_gemm_bf16(const ep_handle* h, const void* a, const void* b, int32_t n, int32_t k, void* out,
                                void* stream);
 
@@ -362,7 +364,8 @@ ep_status ep_grouped_gemm_bf16(const ep_handle* h, const void* a, const void* b,
  *   grad_a[r, j] = bf16( sum_c grad_out[r, c] * b[e, c, j] ),  c < n.
  *   grad_out  device bf16 [rows bound, n].
  *   b         device bf16 [E, n, k], the forward's.
- *   grad_a    device bf16 [rows bound, k]; padding rows as the forward's. */
+ *   grad_a    device bf16 [rows bound, k]; padding rows as the forward's.
+ * Tiles: 256 columns (of k) by R = 256. */
 ep_status ep_grouped_gemm_bf16_grad_input(const ep_handle* h, const void* grad_out, const void* b, int32_t n,
                                           int32_t k, void* grad_a, void* stream);
 
@@ -372,7 +375,8 @@ ep_status ep_grouped_gemm_bf16_grad_input(const ep_handle* h, const void* grad_o
  * zero for an expert without a live row.
  *   grad_out  device bf16 [rows bound, n].
  *   a         device bf16 [rows bound, k], the forward's.
- *   grad_b    device [E, n, k]: binary32 when grad_b_f32 is 1, bf16 when 0. */
+ *   grad_b    device [E, n, k]: binary32 when grad_b_f32 is 1, bf16 when 0.
+ * Tiles: E * ceil(n / 256) * ceil(k / 128), at most 2^24 - 1. */
 ep_status ep_grouped_gemm_bf16_grad_weight(const ep_handle* h, const void* grad_out, const void* a, int32_t n,
                                            int32_t k, int32_t grad_b_f32, void* grad_b, void* stream);
 
@@ -389,7 +393,8 @@ ep_status ep_grouped_gemm_bf16_grad_weight(const ep_handle* h, const void* grad_
  *   out       as ep_grouped_gemm_bf16's, and likewise n.
  * A weight is a bf16 value (weights past bf16's largest finite value are
  * infinite, as in binary32), products are summed in binary32 by the MFMA and
- * rounded once. */
+ * rounded once. Tiles: 128 columns by R = 16 for P <= 6 E, 256 columns by 32 for
+ * P <= 20 E, otherwise 256 columns by 64. */
 ep_status ep_grouped_gemm_mxfp4(const ep_handle* h, const void* a, const void* b, const void* b_scales, int32_t n,
                                 int32_t k, void* out, void* stream);
 
