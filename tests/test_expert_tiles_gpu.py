@@ -1,0 +1,135 @@
+"""The experts' products on each of their kernels: whole tiles (8 waves, 256 x
+256), half tiles and the kernel that streams the weights, which the launchers
+choose by sizes alone. Every test names the kernel that it is about and fails
+when another one ran, so that a change of the rules cannot move it elsewhere.
+
+Values are held to the tolerance of test_expert_products_gpu.py's docstring; the
+widest reductions to equality, on integers whose sums are exact in any order."""
+import re
+
+import numpy as np
+import pytest
+import torch
+
+from ep_workloads import random_routing_table
+from test_expert_products_gpu import call, check, make_handle, operands, ranges, routing, verify
+
+pytestmark = pytest.mark.gpu
+
+if torch.cuda.is_available():
+    from combine_ep_layout_10_amd import ops
+
+
+@pytest.fixture
+def launched(monkeypatch, capfd):
+    """A function that returns the launches of the products since the last call
+    of it, as (kernel, the launcher's remarks)."""
+    monkeypatch.setenv("EP_BUFFER_DEBUG", "1")
+
+    def read():
+        return re.findall(r"\[ep\] (k_grouped_gemm\w*) grid \d+ block \d+ (.*)", capfd.readouterr().err)
+
+    yield read
+
+
+def output(direction, h, n, k, f32=True):
+    R, E = h.cfg.recv_rows_bound(), h.cfg.num_experts
+    if direction == "grad_weight":
+        return torch.full((E, n, k), 7.0, device="cuda", dtype=torch.float32 if f32 else torch.bfloat16)
+    return torch.full((R, k if direction == "grad_input" else n), 7.0, device="cuda", dtype=torch.bfloat16)
+
+
+def run_case(direction, h, n, k, launched, kernel, seed=0, remark=""):
+    o = operands(direction, h, n, k, seed)
+    out = output(direction, h, n, k)
+    launched()
+    call(direction, h, o, out)
+    torch.cuda.synchronize()
+    ran = launched()
+    assert [r[0] for r in ran] == [kernel] and remark in ran[0][1], ran
+    verify(direction, h, o, out, n, k)
+
+
+def wide(direction, width, reduction):
+    """n and k for an output of `width` columns."""
+    return (width, reduction) if direction == "forward" else (reduction, width)
+
+
+# every number of 32-row steps that a whole tile is compiled for (1 to 8), experts of one tile, two, three, and
+# more than a group of the block order, empty ones first, in the middle and last
+WHOLE_COUNTS = [0, 1, 15, 32, 33, 64, 65, 96, 97, 0, 128, 129, 160, 161, 192, 193, 224, 225, 255, 256, 257, 300, 513,
+                1100, 2, 2306, 0]
+
+
+@pytest.mark.parametrize("direction", ("forward", "grad_input"))
+@pytest.mark.parametrize("A", [1, 300])
+@pytest.mark.parametrize("reduction", [8, 64, 72, 136, 328, 1056])
+def test_whole_tiles(direction, A, reduction, launched):
+    """Whole tiles of every height and ring, reductions below, at and past the
+    64 of a step, a last column tile of 8."""
+    h = make_handle(routing(WHOLE_COUNTS), len(WHOLE_COUNTS), A)
+    n, k = wide(direction, 2056, reduction)
+    run_case(direction, h, n, k, launched, "k_grouped_gemm_bf16", seed=reduction)
+
+
+@pytest.mark.parametrize("direction", ("forward", "grad_input"))
+def test_whole_tiles_fixed_capacity(direction, launched):
+    """FIXED: experts that overflow, rows past each count left as they were."""
+    h = make_handle(random_routing_table(np.random.default_rng(9), 1500, 6, 2), 6, 1, mode=ops.MODE_FIXED, C=499)
+    n, k = wide(direction, 5640, 200)
+    run_case(direction, h, n, k, launched, "k_grouped_gemm_bf16")
+
+
+@pytest.mark.parametrize("direction", ("forward", "grad_input"))
+def test_whole_tiles_no_zero_pad_masked_and_bad_ids(direction, launched):
+    idx = random_routing_table(np.random.default_rng(10), 1500, 6, 2, masked_frac=0.2, bad_frac=0.05)
+    h = make_handle(idx, 6, 32, flags=ops.FLAG_NO_ZERO_PAD)
+    n, k = wide(direction, 5640, 200)
+    run_case(direction, h, n, k, launched, "k_grouped_gemm_bf16")
+
+
+@pytest.mark.parametrize("direction", ("forward", "grad_input"))
+def test_whole_tiles_infinite_and_nan_values(direction, launched):
+    """Infinities and NaN reach exactly the outputs that the formula says."""
+    h = make_handle(routing([300, 40, 700]), 3, 1)
+    n, k = wide(direction, 11272, 136)
+    o = operands(direction, h, n, k)
+    x = o["g" if direction == "grad_input" else "a"]
+    x[3, 5] = float("inf")
+    x[301, 7] = float("-inf")
+    x[340 + 511] = float("nan")
+    launched()
+    got = call(direction, h, o)
+    torch.cuda.synchronize()
+    assert [r[0] for r in launched()] == ["k_grouped_gemm_bf16"]
+    for e, (first, live, _) in enumerate(o["rr"]):
+        rows = slice(first, first + live)
+        w = o["w64"](e)
+        g, want = got[rows], x[rows].double() @ (w if direction == "grad_input" else w.t().contiguous())
+        assert torch.equal(torch.isnan(g), torch.isnan(want)), e
+        assert torch.equal(torch.isinf(g), torch.isinf(want)), e
+        assert torch.equal(g[torch.isinf(want)].double(), want[torch.isinf(want)]), e
+
+
+@pytest.mark.parametrize("direction", ("forward", "grad_input"))
+def test_whole_tiles_far_rows(direction, launched):
+    """Rows whose output stands past 2^32 bytes, behind a long padding that is
+    cleared: experts 2^18 rows apart, 8200 columns."""
+    if torch.cuda.mem_get_info()[0] < 60 << 30:
+        pytest.skip("needs 60 GB of device memory")
+    A, counts = 1 << 18, [260, 1, 40, 129, 300]
+    h = make_handle(routing(counts), len(counts), A)
+    n, k = wide(direction, 8200, 24)
+    o = operands(direction, h, n, k)
+    x = o["g" if direction == "grad_input" else "a"]
+    launched()
+    got = call(direction, h, o)
+    torch.cuda.synchronize()
+    assert [r[0] for r in launched()] == ["k_grouped_gemm_bf16"]
+    for e, (first, live, owned) in enumerate(ranges(h)):
+        assert first == e * A and owned == A
+        w = o["w64"](e)
+        check(got[first:first + live], x[first:first + live].double(), w if direction == "grad_input" else w.t(), 24, e)
+        for r in range(first + live, first + owned, 1 << 15):
+            end = min(r + (1 << 15), first + owned)
+            assert int(torch.count_nonzero(got[r:end].view(torch.int16))) == 0, (e, r)
