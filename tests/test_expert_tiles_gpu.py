@@ -133,3 +133,47 @@ def test_whole_tiles_far_rows(direction, launched):
         for r in range(first + live, first + owned, 1 << 15):
             end = min(r + (1 << 15), first + owned)
             assert int(torch.count_nonzero(got[r:end].view(torch.int16))) == 0, (e, r)
+
+
+# ---------------------------------------------------------------- BF16 weights streamed
+
+# rows of five experts: one each, the most that 16-row tiles take on the mean, the least and the most of 32-row
+# tiles, and one expert with nearly everything (several row tiles of it)
+FEW = {"one": ([1, 0, 1, 1, 2], 16), "six": ([6, 3, 9, 0, 12], 16), "seven": ([0, 7, 16, 1, 11], 32),
+       "sixteen": ([16, 31, 1, 0, 32], 32), "hot16": ([0, 28, 0, 1, 0], 16), "hot32": ([0, 0, 79, 0, 1], 32)}
+# n, k and the parts the reduction is split in; k ends inside a slice (512 or 1024) and off every chunk of 128
+SPLITS = [(72, 4104, 8), (1416, 4104, 4), (264, 2088, 4), (2600, 1032, 2), (40, 1032, 2), (5200, 1032, 1), (264, 8, 1),
+          (1000, 520, 1)]
+
+
+@pytest.mark.parametrize("rows", sorted(FEW))
+@pytest.mark.parametrize("n,k,split", SPLITS)
+def test_streamed_weights(rows, n, k, split, launched):
+    counts, tile = FEW[rows]
+    h = make_handle(routing(counts), 5, 4)
+    run_case("forward", h, n, k, launched, "k_grouped_gemm_stream", seed=n + k,
+             remark="rows %d split %d n %d k %d" % (tile, split, n, k))
+
+
+def test_streamed_weights_fixed_capacity(launched):
+    """FIXED: experts that overflow; rows past each count left as they were."""
+    h = make_handle(random_routing_table(np.random.default_rng(9), 40, 6, 2), 6, 1, mode=ops.MODE_FIXED, C=11)
+    run_case("forward", h, 520, 1096, launched, "k_grouped_gemm_stream", remark="rows 32 split 2")
+
+
+def test_streamed_weights_infinite_and_nan_values(launched):
+    h = make_handle(routing([6, 14, 2]), 3, 1)
+    o = operands("forward", h, 72, 2088)
+    o["a"][2, 2087] = float("inf")
+    o["a"][7] = float("nan")
+    o["b"][2, 5, 1000] = float("nan")
+    launched()
+    got = call("forward", h, o)
+    torch.cuda.synchronize()
+    assert [r[0] for r in launched()] == ["k_grouped_gemm_stream"]
+    for e, (first, live, _) in enumerate(o["rr"]):
+        rows = slice(first, first + live)
+        want = o["a"][rows].double() @ o["w64"](e).t().contiguous()
+        assert torch.equal(torch.isnan(got[rows]), torch.isnan(want)), e
+        assert torch.equal(torch.isinf(got[rows]), torch.isinf(want)), e
+        assert torch.equal(got[rows][torch.isinf(want)].double(), want[torch.isinf(want)]), e
