@@ -12,7 +12,8 @@ import pytest
 import torch
 
 from ep_workloads import random_routing_table
-from test_expert_products_gpu import call, check, make_handle, operands, ranges, routing, verify
+from gpu_common import log
+from test_expert_products_gpu import call, check, decode_mxfp4, make_handle, operands, ranges, routing, verify
 
 pytestmark = pytest.mark.gpu
 
@@ -177,3 +178,42 @@ def test_streamed_weights_infinite_and_nan_values(launched):
         assert torch.equal(torch.isnan(got[rows]), torch.isnan(want)), e
         assert torch.equal(torch.isinf(got[rows]), torch.isinf(want)), e
         assert torch.equal(got[rows][torch.isinf(want)].double(), want[torch.isinf(want)]), e
+
+
+# ---------------------------------------------------------------- the widest reductions, exactly
+
+@pytest.mark.parametrize("direction", ("forward", "grad_input", "mxfp4"))
+@pytest.mark.parametrize("counts", [[1, 0, 2], [9, 40, 2]])
+def test_widest_exact(direction, counts, launched):
+    """Reductions of 2^20, the widest that are accepted. Operands are -1, 0 and 1
+    (4-bit weights: every code, in halves up to 6), so every partial sum is a
+    multiple of 1/2 of at most 6 * 2^20 < 2^23: exact in binary32 in any order.
+    The outputs are the exact sums rounded to bf16, bit for bit."""
+    W = 1 << 20
+    h = make_handle(routing(counts), 3, 1)
+    n, k = (W, 32) if direction == "grad_input" else (8, W)
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(sum(counts))
+    R, rr = h.cfg.recv_rows_bound(), ranges(h)
+    ints = lambda *shape: torch.randint(-1, 2, shape, device="cuda", generator=gen).to(torch.bfloat16)
+    o = dict(rr=rr)
+    x = o["g" if direction == "grad_input" else "a"] = ints(R, W)
+    if direction == "mxfp4":
+        o["b"] = torch.randint(0, 256, (3, n, k // 2), dtype=torch.uint8, device="cuda", generator=gen)
+        o["s"] = torch.full((3, n, k // 32), 127, dtype=torch.uint8, device="cuda")
+        w64 = lambda e: decode_mxfp4(o["b"][e], o["s"][e])
+    else:
+        o["b"] = ints(3, n, k)
+        w64 = lambda e: o["b"][e].double()
+    launched()
+    out = output(direction, h, n, k)
+    got = call(direction, h, o, out)
+    torch.cuda.synchronize()
+    log("%s %s: %s" % (direction, counts, launched()))
+    for e, (first, live, _) in enumerate(rr):
+        if live == 0:
+            continue
+        rows, w = slice(first, first + live), w64(e)
+        want = x[rows].double() @ (w if direction == "grad_input" else w.t().contiguous())
+        assert float(want.abs().max()) > 256.0     # sums that the output's rounding has to round
+        assert torch.equal(got[rows], want.to(torch.bfloat16)), e
