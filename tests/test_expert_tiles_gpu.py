@@ -12,7 +12,7 @@ import pytest
 import torch
 
 from ep_workloads import random_routing_table
-from gpu_common import log
+from gpu_common import log, to_dev
 from test_expert_products_gpu import call, check, decode_mxfp4, make_handle, operands, ranges, routing, verify
 
 pytestmark = pytest.mark.gpu
@@ -217,3 +217,105 @@ def test_widest_exact(direction, counts, launched):
         want = x[rows].double() @ (w if direction == "grad_input" else w.t().contiguous())
         assert float(want.abs().max()) > 256.0     # sums that the output's rounding has to round
         assert torch.equal(got[rows], want.to(torch.bfloat16)), e
+
+
+# ---------------------------------------------------------------- the same bits: again, captured, on two streams
+
+# direction, tokens, experts, top-k, n, k, kernel, the launcher's remark
+KERNELS = {
+    "whole forward": ("forward", 600, 6, 2, 5640, 200, "k_grouped_gemm_bf16", ""),
+    "whole grad_input": ("grad_input", 600, 6, 2, 200, 5640, "k_grouped_gemm_bf16", ""),
+    "half forward": ("forward", 600, 6, 2, 520, 544, "k_grouped_gemm_bf16_half", ""),
+    "bf16 16 rows split 8": ("forward", 12, 8, 2, 264, 4104, "k_grouped_gemm_stream", "rows 16 split 8"),
+    "bf16 16 rows split 4": ("forward", 12, 8, 2, 1032, 2088, "k_grouped_gemm_stream", "rows 16 split 4"),
+    "bf16 16 rows split 2": ("forward", 12, 8, 2, 2056, 1032, "k_grouped_gemm_stream", "rows 16 split 2"),
+    "bf16 32 rows split 8": ("forward", 40, 8, 2, 264, 4104, "k_grouped_gemm_stream", "rows 32 split 8"),
+    "bf16 32 rows split 4": ("forward", 40, 8, 2, 1032, 2088, "k_grouped_gemm_stream", "rows 32 split 4"),
+    "bf16 32 rows split 2": ("forward", 40, 8, 2, 2056, 1032, "k_grouped_gemm_stream", "rows 32 split 2"),
+    "bf16 32 rows split 1": ("forward", 40, 8, 2, 4104, 136, "k_grouped_gemm_stream", "rows 32 split 1"),
+    "mxfp4 16 rows split 8": ("mxfp4", 12, 8, 2, 264, 4128, "k_grouped_gemm_stream", "rows 16 split 8"),
+    "mxfp4 16 rows split 4": ("mxfp4", 12, 8, 2, 1032, 2080, "k_grouped_gemm_stream", "rows 16 split 4"),
+    "mxfp4 32 rows split 2": ("mxfp4", 40, 8, 2, 2056, 1056, "k_grouped_gemm_stream", "rows 32 split 2"),
+    "mxfp4 32 rows split 1": ("mxfp4", 40, 8, 2, 4104, 160, "k_grouped_gemm_stream", "rows 32 split 1"),
+    "mxfp4 64 rows": ("mxfp4", 300, 8, 2, 520, 544, "k_grouped_gemm_stream", "rows 64 split 1"),
+}
+
+
+def live_rows(o):
+    return torch.cat([torch.arange(f, f + l) for f, l, _ in o["rr"]]).cuda()
+
+
+@pytest.mark.parametrize("name", sorted(KERNELS))
+def test_same_bits_again(name, launched):
+    """A second call, with other work on the card between, gives the same bits."""
+    direction, T, E, top, n, k, kernel, remark = KERNELS[name]
+    h = make_handle(random_routing_table(np.random.default_rng(13), T, E, top), E)
+    o = operands(direction, h, n, k)
+    launched()
+    first = call(direction, h, o, output(direction, h, n, k))
+    for _ in range(2):
+        torch.randn((1 << 24,), device="cuda").sort()
+        assert torch.equal(call(direction, h, o, output(direction, h, n, k)), first)
+    torch.cuda.synchronize()
+    ran = launched()
+    assert len(ran) == 3 and all(r[0] == kernel and remark in r[1] for r in ran), ran
+    verify(direction, h, o, first, n, k)
+
+
+@pytest.mark.parametrize("name", sorted(KERNELS))
+def test_graph_replay(name, launched):
+    """Captured once with its layout and replayed on new routing and operands,
+    with eager calls between the replays."""
+    direction, T, E, top, n, k, kernel, remark = KERNELS[name]
+    rng = np.random.default_rng(15)
+    h = make_handle(random_routing_table(rng, T, E, top), E, 16)
+    idx = h.topk_idx
+    o = operands(direction, h, n, k)
+    out = output(direction, h, n, k)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        call(direction, h, o, out)
+    torch.cuda.current_stream().wait_stream(s)
+    graph = torch.cuda.CUDAGraph()
+    launched()
+    with torch.cuda.graph(graph):
+        h2 = ops.layout(h.cfg, idx, workspace=h.workspace)
+        call(direction, h2, o, out)
+    ran = launched()
+    assert [r[0] for r in ran] == [kernel] and remark in ran[0][1], ran
+    for rep in range(3):
+        idx.copy_(to_dev(random_routing_table(rng, T, E, top)))
+        he = ops.layout(h.cfg, idx)
+        new = operands(direction, he, n, k, seed=rep)
+        for key in ("a", "g", "b", "s"):
+            if key in o:
+                o[key].copy_(new[key])
+        out.fill_(7.0)
+        graph.replay()
+        torch.cuda.synchronize()
+        eager = output(direction, he, n, k)
+        call(direction, he, new, eager)
+        assert torch.equal(out, eager), rep
+        verify(direction, he, new, out, n, k)
+
+
+@pytest.mark.parametrize("name", sorted(KERNELS))
+def test_two_streams_at_once(name):
+    """Two calls on two streams share nothing."""
+    direction, T, E, top, n, k, _, _ = KERNELS[name]
+    rng = np.random.default_rng(16)
+    hs = [make_handle(random_routing_table(rng, T, E, top), E) for _ in range(2)]
+    os_ = [operands(direction, h, n, k, seed=i) for i, h in enumerate(hs)]
+    want = [call(direction, h, o) for h, o in zip(hs, os_)]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    got = []
+    for s, h, o in zip(streams, hs, os_):
+        with torch.cuda.stream(s):
+            got.append([call(direction, h, o) for _ in range(4)])
+    torch.cuda.synchronize()
+    for w, g, o in zip(want, got, os_):
+        rows = live_rows(o)
+        for x in g:
+            assert torch.equal(x[rows], w[rows])
