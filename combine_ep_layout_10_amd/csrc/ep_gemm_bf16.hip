@@ -36,7 +36,8 @@
 // c ^ (r / 2 mod 8). The other operands have a row of columns for each k and are
 // read through the transposing LDS read, 4 k by 16 columns; their 32-byte pair of
 // chunks p of row k is stored at p ^ f(k), f(k) = k mod 4 + 4 (k / 8 mod 2). Either
-// way a read meets each bank once (no cycle of SQ_LDS_BANK_CONFLICT).
+// way a read meets each bank once: the loop has no cycle of SQ_LDS_BANK_CONFLICT
+// (what a launch counts, about 1,000 a tile, are the stores' writes).
 //
 // Half tiles (grad_weight, few tiles): 4 waves, 256 x 128, steps of 32, two blocks
 // a CU; described with them. Few rows an expert: ep_gemm_stream.hip.
@@ -202,7 +203,8 @@ struct Operand {
 // lanes that leave 8 rows side by side, in whole lines as well, 1.09 and 1.49). A
 // wave's LDS accesses stay in order. 16-byte chunks are stored XORed with the row
 // (binary32), with half the row (bf16, two rows in the 64 banks), so that a read
-// meets each bank once (512 cycles of bank conflicts a tile are left, of the writes).
+// meets each bank once. (bf16's writes leave 16 cycles of bank conflicts a wave and
+// piece: 512 a half tile, 1,024 a whole one; binary32's none.)
 constexpr int kStoreLds = 4096;
 
 template <int DIR, int MI>

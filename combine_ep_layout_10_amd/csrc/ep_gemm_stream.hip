@@ -337,7 +337,17 @@ hipError_t launch_split(const StreamArgs& a, int64_t pairs, hipStream_t stream) 
 }  // namespace
 
 // Rows of a tile: enough for nearly every expert's, so that its weights are read
-// once (an expert's rows scatter around their mean).
+// once (an expert's rows scatter around their mean); smaller tiles hold less LDS
+// and fewer registers. Top-8 of 64 experts, us:
+//   BF16, 4096 x 4096    mean 4    6    8   10   12   16
+//     16 rows               341  347  349  375  372  443
+//     32 rows               343  350  353  352  355  355
+//   MXFP4, 4096 x 7168   mean 4    6    8   10   12   16   20   24   28   32   48
+//     16 rows               190  196  199  217  223
+//     32 rows               206  207  207  209  211  216  219  223  262  300  375
+//     64 rows                         209       212  216  220  226  236  245  277
+// A limit keeps some distance from where it crosses, for counts that scatter more
+// than these (uneven routing reads the weights twice for a tile that is too small).
 hipError_t launch_grouped_gemm_mxfp4(const StreamArgs& a, int64_t pairs, hipStream_t stream) {
     if (pairs == 0) return hipSuccess;
     const int64_t mean = (pairs + a.rows.E - 1) / a.rows.E;
