@@ -24,6 +24,9 @@ EP_BF16 = 0
 EP_FP8_QUANTIZE = 1
 EP_FP8_PREQUANT = 2
 
+EP_SCORE_SOFTMAX = 0
+EP_SCORE_SIGMOID = 1
+
 EP_FLAG_NO_ZERO_PAD = 1
 EP_ERRFLAG_BAD_ID = 1
 EP_ERRFLAG_OVERFLOW = 2
@@ -60,6 +63,21 @@ class ep_handle(ctypes.Structure):
         ("err_flags", ctypes.c_void_p),
         ("internal", ctypes.c_void_p),
         ("topk_idx", ctypes.c_void_p),
+    ]
+
+
+class ep_router(ctypes.Structure):
+    _fields_ = [
+        ("num_experts", ctypes.c_int32),
+        ("num_topk", ctypes.c_int32),
+        ("score", ctypes.c_int32),
+        ("num_groups", ctypes.c_int32),
+        ("topk_groups", ctypes.c_int32),
+        ("group_best", ctypes.c_int32),
+        ("renormalize", ctypes.c_int32),
+        ("idx_bits", ctypes.c_int32),
+        ("logits_f32", ctypes.c_int32),
+        ("scale", ctypes.c_float),
     ]
 
 
@@ -101,6 +119,12 @@ _SIGNATURES = {
     "ep_rms_norm_workspace_bytes": (ctypes.c_size_t, [ctypes.c_int32, ctypes.c_int32]),
     "ep_rms_norm_backward": (ctypes.c_int, [ctypes.c_int32, ctypes.c_int32, _P, _P, _P, _P, _P, _P, _P, _P,
                                             ctypes.c_size_t, _P]),
+    "ep_route": (ctypes.c_int, [ctypes.POINTER(ep_router), ctypes.c_int32, _P, _P, _P, _P, _P, _P]),
+    "ep_balance_loss_workspace_bytes": (ctypes.c_size_t, [ctypes.POINTER(ep_router), ctypes.c_int32, ctypes.c_int32]),
+    "ep_balance_loss": (ctypes.c_int, [ctypes.POINTER(ep_router), ctypes.c_int32, _P, _P, _P, ctypes.c_int32, _P, _P, _P,
+                                       _P, ctypes.c_size_t, _P]),
+    "ep_route_backward": (ctypes.c_int, [ctypes.POINTER(ep_router), ctypes.c_int32, _P, _P, _P, _P, _P, _P, _P,
+                                         ctypes.c_int32, _P, _P]),
     "ep_handle_read_counts": (ctypes.c_int, [ctypes.POINTER(ep_handle), _P, _P, _P, _P]),
     "ep_handle_check": (ctypes.c_int, [ctypes.POINTER(ep_handle), _P, _P]),
     "ep_status_string": (ctypes.c_char_p, [ctypes.c_int32]),
@@ -244,6 +268,33 @@ def ep_rms_norm_backward(num_tokens: int, hidden: int, total: int, weight: int, 
                                               grad_weight, workspace, workspace_bytes, stream)
     if st != EP_OK:
         _check(st, "ep_rms_norm_backward")
+
+
+def ep_route(r: ep_router, num_tokens: int, logits: int, bias, token_mask, topk_idx: int, topk_w: int,
+             stream: int) -> None:
+    st = (_lib or lib()).ep_route(ctypes.byref(r), num_tokens, logits, bias, token_mask, topk_idx, topk_w, stream)
+    if st != EP_OK:
+        _check(st, "ep_route")
+
+
+def ep_balance_loss_workspace_bytes(r: ep_router, num_tokens: int, num_seqs: int) -> int:
+    return int(lib().ep_balance_loss_workspace_bytes(ctypes.byref(r), int(num_tokens), int(num_seqs)))
+
+
+def ep_balance_loss(r: ep_router, num_tokens: int, logits: int, topk_idx: int, seq_off, num_seqs: int, loss: int,
+                    counts: int, coef: int, workspace: int, workspace_bytes: int, stream: int) -> None:
+    st = (_lib or lib()).ep_balance_loss(ctypes.byref(r), num_tokens, logits, topk_idx, seq_off, num_seqs, loss, counts,
+                                         coef, workspace, workspace_bytes, stream)
+    if st != EP_OK:
+        _check(st, "ep_balance_loss")
+
+
+def ep_route_backward(r: ep_router, num_tokens: int, logits: int, topk_idx: int, grad_topk_w, counts, coef, grad_loss,
+                      seq_off, num_seqs: int, grad_logits: int, stream: int) -> None:
+    st = (_lib or lib()).ep_route_backward(ctypes.byref(r), num_tokens, logits, topk_idx, grad_topk_w, counts, coef,
+                                           grad_loss, seq_off, num_seqs, grad_logits, stream)
+    if st != EP_OK:
+        _check(st, "ep_route_backward")
 
 
 def ep_handle_read_counts(h: ep_handle, cnt, pad, rows, stream: int) -> None:

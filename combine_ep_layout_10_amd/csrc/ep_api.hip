@@ -287,6 +287,84 @@ ep_status check_norm(int32_t num_tokens, int32_t hidden) {
     return EP_OK;
 }
 
+ep_status check_router(const ep_router* r, int32_t num_tokens) {
+    if (r == nullptr) return fail(EP_ERR_INVALID_ARG, "router is NULL");
+    const int E = r->num_experts;
+    if (E < 1 || E > ep::kMaxExperts)
+        return fail(EP_ERR_INVALID_ARG, "num_experts %d outside [1, %d]", E, ep::kMaxExperts);
+    if (r->num_topk < 1 || r->num_topk > ep::kMaxTopk)
+        return fail(EP_ERR_INVALID_ARG, "num_topk %d outside [1, %d]", r->num_topk, ep::kMaxTopk);
+    if (r->score != EP_SCORE_SOFTMAX && r->score != EP_SCORE_SIGMOID)
+        return fail(EP_ERR_INVALID_ARG, "score %d is not EP_SCORE_SOFTMAX or EP_SCORE_SIGMOID", r->score);
+    if (r->num_groups < 1 || r->num_groups > ep::kMaxRouteGroups || E % r->num_groups != 0)
+        return fail(EP_ERR_INVALID_ARG, "num_groups %d must divide num_experts %d and be at most %d", r->num_groups, E,
+                    ep::kMaxRouteGroups);
+    const int size = E / r->num_groups;
+    if (r->topk_groups < 1 || r->topk_groups > r->num_groups)
+        return fail(EP_ERR_INVALID_ARG, "topk_groups %d outside [1, %d]", r->topk_groups, r->num_groups);
+    if (r->group_best < 1 || r->group_best > 2 || r->group_best > size)
+        return fail(EP_ERR_INVALID_ARG, "group_best %d must be 1 or 2, and at most a group's %d experts",
+                    r->group_best, size);
+    if (r->num_topk > r->topk_groups * size)
+        return fail(EP_ERR_INVALID_ARG, "num_topk %d exceeds the %d experts to choose from", r->num_topk,
+                    r->topk_groups * size);
+    if (r->renormalize != 0 && r->renormalize != 1)
+        return fail(EP_ERR_INVALID_ARG, "renormalize %d must be 0 or 1", r->renormalize);
+    if (r->idx_bits != 32 && r->idx_bits != 64)
+        return fail(EP_ERR_INVALID_ARG, "idx_bits %d must be 32 or 64", r->idx_bits);
+    if (r->logits_f32 != 0 && r->logits_f32 != 1)
+        return fail(EP_ERR_INVALID_ARG, "logits_f32 %d must be 0 or 1", r->logits_f32);
+    if (!(r->scale >= -3.402823466e+38f && r->scale <= 3.402823466e+38f))
+        return fail(EP_ERR_INVALID_ARG, "scale must be finite");
+    if (num_tokens < 0) return fail(EP_ERR_INVALID_ARG, "num_tokens %d must not be negative", num_tokens);
+    if (num_tokens > ep::kMaxRouteTokens)
+        return fail(EP_ERR_UNSUPPORTED, "num_tokens %d exceeds %d", num_tokens, ep::kMaxRouteTokens);
+    return EP_OK;
+}
+
+// Logits (or their gradient) and ids of a router's call.
+ep_status check_router_buffers(const ep_router* r, int32_t num_tokens, const void* logits, const void* topk_idx) {
+    const size_t size = r->logits_f32 ? 4 : 2, id = r->idx_bits / 8;
+    if ((num_tokens > 0 && logits == nullptr) || !aligned(logits, size))
+        return fail(EP_ERR_INVALID_ARG, "logits must be non-NULL and aligned to their element size");
+    if ((num_tokens > 0 && topk_idx == nullptr) || !aligned(topk_idx, id))
+        return fail(EP_ERR_INVALID_ARG, "topk_idx must be non-NULL and aligned to its element size");
+    return EP_OK;
+}
+
+ep_status check_sequences(const int32_t* seq_off, int32_t num_seqs) {
+    if (num_seqs < 1) return fail(EP_ERR_INVALID_ARG, "num_seqs %d must be positive", num_seqs);
+    if (num_seqs > ep::kMaxRouteSequences)
+        return fail(EP_ERR_UNSUPPORTED, "num_seqs %d exceeds %d", num_seqs, ep::kMaxRouteSequences);
+    if (seq_off == nullptr && num_seqs != 1)
+        return fail(EP_ERR_INVALID_ARG, "seq_off is required for %d sequences", num_seqs);
+    if (!aligned(seq_off, 4)) return fail(EP_ERR_INVALID_ARG, "seq_off must be 4-byte aligned");
+    return EP_OK;
+}
+
+// Workspace of a balance loss: the pieces' partial results, the sequences' terms.
+struct BalanceMap {
+    size_t sums, pairs, tokens, unit, term, total;
+};
+
+BalanceMap balance_map(int E, int32_t num_tokens, int32_t num_seqs) {
+    const size_t places = (size_t)(num_tokens + ep::kBalanceTile - 1) / ep::kBalanceTile + num_seqs;
+    BalanceMap m;
+    size_t o = 0;
+    auto take = [&](size_t bytes) {
+        size_t at = o;
+        o = round_up(o + bytes, 256);
+        return at;
+    };
+    m.sums = take(4 * places * E);
+    m.pairs = take(4 * places * E);
+    m.tokens = take(4 * places);
+    m.unit = take(8 * (size_t)num_seqs);
+    m.term = take(8 * (size_t)num_seqs);
+    m.total = o;
+    return m;
+}
+
 // Bytes of the multi-block layout's per-block partials for one call
 // (counts [nblk][E], distinct tokens [nblk][D], error bits [nblk]; regions
 // 256-byte aligned), and their offsets from the start of that scratch.
@@ -765,6 +843,132 @@ ep_status ep_rms_norm_backward(int32_t num_tokens, int32_t hidden, const void* t
     a.H = hidden;
     hipError_t e = ep::launch_rms_norm_backward(a, (hipStream_t)stream);
     if (e != hipSuccess) return hip_fail(e, "RMS norm backward launch");
+    return EP_OK;
+}
+
+ep_status ep_route(const ep_router* r, int32_t num_tokens, const void* logits, const float* bias,
+                   const uint8_t* token_mask, void* topk_idx, float* topk_w, void* stream) {
+    ep_status s = check_router(r, num_tokens);
+    if (s != EP_OK) return s;
+    s = check_router_buffers(r, num_tokens, logits, topk_idx);
+    if (s != EP_OK) return s;
+    if (!aligned(bias, 4)) return fail(EP_ERR_INVALID_ARG, "bias must be 4-byte aligned");
+    if ((num_tokens > 0 && topk_w == nullptr) || !aligned(topk_w, 4))
+        return fail(EP_ERR_INVALID_ARG, "topk_w must be non-NULL and 4-byte aligned");
+    ep::RouteArgs a;
+    a.logits = logits;
+    a.bias = bias;
+    a.mask = token_mask;
+    a.idx = topk_idx;
+    a.w = topk_w;
+    a.T = num_tokens;
+    a.E = r->num_experts;
+    a.k = r->num_topk;
+    a.G = r->topk_groups < r->num_groups ? r->num_groups : 1;  // all groups stay: none are needed
+    a.keep = r->topk_groups;
+    a.best = r->group_best;
+    a.score = r->score;
+    a.renormalize = r->renormalize;
+    a.idx_bits = r->idx_bits;
+    a.f32 = r->logits_f32;
+    a.scale = r->scale;
+    hipError_t e = ep::launch_route(a, (hipStream_t)stream);
+    if (e != hipSuccess) return hip_fail(e, "router launch");
+    return EP_OK;
+}
+
+size_t ep_balance_loss_workspace_bytes(const ep_router* r, int32_t num_tokens, int32_t num_seqs) {
+    if (check_router(r, num_tokens) != EP_OK) return 0;
+    if (num_seqs < 1 || num_seqs > ep::kMaxRouteSequences) {
+        fail(EP_ERR_INVALID_ARG, "num_seqs %d outside [1, %d]", num_seqs, ep::kMaxRouteSequences);
+        return 0;
+    }
+    return balance_map(r->num_experts, num_tokens, num_seqs).total;
+}
+
+ep_status ep_balance_loss(const ep_router* r, int32_t num_tokens, const void* logits, const void* topk_idx,
+                          const int32_t* seq_off, int32_t num_seqs, float* loss, int32_t* counts, float* coef,
+                          void* workspace, size_t workspace_bytes, void* stream) {
+    ep_status s = check_router(r, num_tokens);
+    if (s != EP_OK) return s;
+    s = check_router_buffers(r, num_tokens, logits, topk_idx);
+    if (s != EP_OK) return s;
+    s = check_sequences(seq_off, num_seqs);
+    if (s != EP_OK) return s;
+    if (loss == nullptr || counts == nullptr || coef == nullptr || !aligned(loss, 4) || !aligned(counts, 4) ||
+        !aligned(coef, 4))
+        return fail(EP_ERR_INVALID_ARG, "loss, counts and coef must be non-NULL and 4-byte aligned");
+    if (workspace == nullptr || !aligned(workspace, 256))
+        return fail(EP_ERR_INVALID_ARG, "workspace must be non-NULL and 256-byte aligned");
+    const BalanceMap m = balance_map(r->num_experts, num_tokens, num_seqs);
+    if (workspace_bytes < m.total)
+        return fail(EP_ERR_WORKSPACE, "workspace has %zu bytes, the balance loss needs %zu", workspace_bytes, m.total);
+    char* ws = (char*)workspace;
+    ep::BalanceArgs a;
+    a.logits = logits;
+    a.idx = topk_idx;
+    a.seq_off = seq_off;
+    a.loss = loss;
+    a.counts = counts;
+    a.coef = coef;
+    a.sums = (float*)(ws + m.sums);
+    a.pairs = (int32_t*)(ws + m.pairs);
+    a.tokens = (int32_t*)(ws + m.tokens);
+    a.unit = (double*)(ws + m.unit);
+    a.term = (double*)(ws + m.term);
+    a.T = num_tokens;
+    a.E = r->num_experts;
+    a.k = r->num_topk;
+    a.S = num_seqs;
+    a.score = r->score;
+    a.idx_bits = r->idx_bits;
+    a.f32 = r->logits_f32;
+    hipError_t e = ep::launch_balance_loss(a, (hipStream_t)stream);
+    if (e != hipSuccess) return hip_fail(e, "balance loss launch");
+    return EP_OK;
+}
+
+ep_status ep_route_backward(const ep_router* r, int32_t num_tokens, const void* logits, const void* topk_idx,
+                            const float* grad_topk_w, const int32_t* counts, const float* coef,
+                            const float* grad_loss, const int32_t* seq_off, int32_t num_seqs, void* grad_logits,
+                            void* stream) {
+    ep_status s = check_router(r, num_tokens);
+    if (s != EP_OK) return s;
+    s = check_router_buffers(r, num_tokens, logits, topk_idx);
+    if (s != EP_OK) return s;
+    s = check_sequences(seq_off, num_seqs);
+    if (s != EP_OK) return s;
+    const bool loss = counts != nullptr;
+    if (loss != (coef != nullptr) || loss != (grad_loss != nullptr))
+        return fail(EP_ERR_INVALID_ARG, "counts, coef and grad_loss must be given together");
+    if (!loss && (seq_off != nullptr || num_seqs != 1))
+        return fail(EP_ERR_INVALID_ARG, "seq_off is read only with counts");
+    if (num_tokens > 0 && grad_topk_w == nullptr && !loss)
+        return fail(EP_ERR_INVALID_ARG, "grad_topk_w, or counts, coef and grad_loss, must be given");
+    if (!aligned(grad_topk_w, 4) || !aligned(counts, 4) || !aligned(coef, 4) || !aligned(grad_loss, 4))
+        return fail(EP_ERR_INVALID_ARG, "grad_topk_w, counts, coef and grad_loss must be 4-byte aligned");
+    if ((num_tokens > 0 && grad_logits == nullptr) || !aligned(grad_logits, r->logits_f32 ? 4 : 2))
+        return fail(EP_ERR_INVALID_ARG, "grad_logits must be non-NULL and aligned to its element size");
+    ep::RouteBackwardArgs a;
+    a.logits = logits;
+    a.idx = topk_idx;
+    a.grad_w = grad_topk_w;
+    a.counts = counts;
+    a.coef = coef;
+    a.grad_loss = grad_loss;
+    a.seq_off = seq_off;
+    a.grad = grad_logits;
+    a.T = num_tokens;
+    a.E = r->num_experts;
+    a.k = r->num_topk;
+    a.S = num_seqs;
+    a.score = r->score;
+    a.renormalize = r->renormalize;
+    a.idx_bits = r->idx_bits;
+    a.f32 = r->logits_f32;
+    a.scale = r->scale;
+    hipError_t e = ep::launch_route_backward(a, (hipStream_t)stream);
+    if (e != hipSuccess) return hip_fail(e, "router backward launch");
     return EP_OK;
 }
 

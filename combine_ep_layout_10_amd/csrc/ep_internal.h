@@ -195,6 +195,52 @@ constexpr int kMaxNormTokens = (1 << 22) - 1;
 // the device's CU count.
 constexpr int kNormParts = 512;
 
+// The router (ep_route.hip): choice, balance loss, gradient.
+struct RouteArgs {
+    const void* logits;   // binary32 or bf16 [T, E]
+    const float* bias;    // [E] or NULL
+    const uint8_t* mask;  // [T] or NULL
+    void* idx;
+    float* w;
+    int T, E, k, G, keep, best, score, renormalize, idx_bits, f32;
+    float scale;
+};
+
+struct BalanceArgs {
+    const void* logits;
+    const void* idx;
+    const int32_t* seq_off;  // or NULL: one sequence
+    float* loss;
+    int32_t* counts;
+    float* coef;
+    // partial results of the pieces (tile b of sequence q at place b + q) and of the sequences
+    float* sums;       // [places, E]
+    int32_t* pairs;    // [places, E]
+    int32_t* tokens;   // [places]
+    double* unit;      // [S]: coef before the division by the sequences used
+    double* term;      // [S]
+    int T, E, k, S, score, idx_bits, f32;
+};
+
+struct RouteBackwardArgs {
+    const void* logits;
+    const void* idx;
+    const float* grad_w;  // [T, k] or NULL
+    const int32_t* counts;  // [S, E] or NULL
+    const float* coef;
+    const float* grad_loss;
+    const int32_t* seq_off;
+    void* grad;
+    int T, E, k, S, score, renormalize, idx_bits, f32;
+    float scale;
+};
+
+constexpr int kMaxRouteGroups = 64;         // one a lane
+constexpr int kMaxRouteTokens = 1 << 25;    // a wave each: 2^31 threads
+constexpr int kMaxRouteSequences = 1 << 20;
+constexpr int kBalanceTile = 64;   // tokens of a piece
+constexpr int kBalanceWaves = 16;  // of a piece
+
 // Padding rows per zero-fill piece (a piece of one expert's padding): in the
 // dispatch kernel, and in the single-launch layout + dispatch, where every
 // block also redoes the small layout and so should be few. In the dispatch
@@ -230,6 +276,9 @@ hipError_t launch_grouped_gemm_bf16_stream(const StreamArgs& a, int64_t pairs, h
 hipError_t launch_grouped_gemm_mxfp4(const StreamArgs& a, int64_t pairs, hipStream_t stream);
 hipError_t launch_rms_norm(const NormArgs& a, hipStream_t stream);
 hipError_t launch_rms_norm_backward(const NormBackwardArgs& a, hipStream_t stream);
+hipError_t launch_route(const RouteArgs& a, hipStream_t stream);
+hipError_t launch_balance_loss(const BalanceArgs& a, hipStream_t stream);
+hipError_t launch_route_backward(const RouteBackwardArgs& a, hipStream_t stream);
 // Kernel arguments of the single-launch layout + dispatch, packed into the
 // fields that kernel reads: the handle's arrays as 32-bit offsets from the
 // workspace base, small sizes as 16-bit fields. A launch costs the host

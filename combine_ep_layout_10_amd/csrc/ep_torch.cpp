@@ -334,6 +334,101 @@ std::tuple<at::Tensor, at::Tensor> rms_norm_backward(
     return {gx, gw};
 }
 
+// ---------------------------------------------------------------- router
+
+// The router's sizes with the types that this call's tensors have.
+ep_router router_of(int64_t addr, const at::Tensor& logits) {
+    ep_router r = *reinterpret_cast<const ep_router*>(addr);
+    if (logits.dim() != 2 || logits.size(1) != r.num_experts)
+        throw std::invalid_argument("logits must be [T, " + std::to_string(r.num_experts) + "]");
+    if (logits.scalar_type() != at::kFloat && logits.scalar_type() != at::kBFloat16)
+        throw std::invalid_argument(std::string("logits has dtype ") + std::string(c10::toString(logits.scalar_type())) +
+                                    ", expected Float or BFloat16");
+    r.logits_f32 = logits.scalar_type() == at::kFloat;
+    return r;
+}
+
+at::ScalarType idx_type(const ep_router& r) { return r.idx_bits == 64 ? at::kLong : at::kInt; }
+
+std::tuple<at::Tensor, at::Tensor> route(int64_t router, const at::Tensor& logits, const c10::optional<at::Tensor>& bias,
+                                         const c10::optional<at::Tensor>& token_mask,
+                                         const c10::optional<at::Tensor>& topk_idx,
+                                         const c10::optional<at::Tensor>& topk_w, int64_t stream, int64_t dev) {
+    const ep_router r = router_of(router, logits);
+    const int64_t T = logits.size(0), k = r.num_topk;
+    opt_shape(bias, {r.num_experts}, "bias");
+    opt_shape(token_mask, {T}, "token_mask");
+    const void* pl = ptr(logits, "logits", logits.scalar_type(), dev);
+    const float* pb = (const float*)opt_ptr(bias, "bias", at::kFloat, dev);
+    const uint8_t* pm = (const uint8_t*)opt_ptr(token_mask, "token_mask", at::kBool, dev);
+    at::Tensor i = output(topk_idx, {T, k}, idx_type(r), logits, "topk_idx");
+    at::Tensor w = output(topk_w, {T, k}, at::kFloat, logits, "topk_w");
+    ok(ep_route(&r, width(T), pl, pb, pm, ptr(i, "topk_idx", idx_type(r), dev),
+                (float*)ptr(w, "topk_w", at::kFloat, dev), stream_of(stream)),
+       "ep_route");
+    return {i, w};
+}
+
+// Sequences of a batch: seq_off [S + 1], or one of all tokens.
+int32_t sequences(const c10::optional<at::Tensor>& seq_off) {
+    if (!seq_off.has_value()) return 1;
+    if (seq_off->dim() != 1 || seq_off->size(0) < 2) throw std::invalid_argument("seq_off must be [sequences + 1]");
+    return width(seq_off->size(0) - 1);
+}
+
+std::tuple<at::Tensor, at::Tensor, at::Tensor> balance_loss(
+    int64_t router, const at::Tensor& logits, const at::Tensor& topk_idx, const c10::optional<at::Tensor>& seq_off,
+    const c10::optional<at::Tensor>& loss, const c10::optional<at::Tensor>& counts,
+    const c10::optional<at::Tensor>& coef, const c10::optional<at::Tensor>& workspace, int64_t stream, int64_t dev) {
+    const ep_router r = router_of(router, logits);
+    const int64_t T = logits.size(0), S = sequences(seq_off);
+    shape(topk_idx, {T, r.num_topk}, "topk_idx");
+    const void* pl = ptr(logits, "logits", logits.scalar_type(), dev);
+    const void* pi = ptr(topk_idx, "topk_idx", idx_type(r), dev);
+    const int32_t* ps = (const int32_t*)opt_ptr(seq_off, "seq_off", at::kInt, dev);
+    at::Tensor l = output(loss, {}, at::kFloat, logits, "loss");
+    at::Tensor c = output(counts, {S, r.num_experts}, at::kInt, logits, "counts");
+    at::Tensor f = output(coef, {S}, at::kFloat, logits, "coef");
+    at::Tensor ws;
+    if (workspace.has_value()) {
+        ws = *workspace;
+    } else {
+        const size_t need = ep_balance_loss_workspace_bytes(&r, width(T), (int32_t)S);
+        if (need == 0) ok(EP_ERR_INVALID_ARG, "ep_balance_loss_workspace_bytes");
+        ws = at::empty({(int64_t)need}, logits.options().dtype(at::kByte));
+    }
+    ok(ep_balance_loss(&r, width(T), pl, pi, ps, (int32_t)S, (float*)ptr(l, "loss", at::kFloat, dev),
+                       (int32_t*)ptr(c, "counts", at::kInt, dev), (float*)ptr(f, "coef", at::kFloat, dev),
+                       ptr(ws, "workspace", at::kByte, dev), (size_t)ws.numel(), stream_of(stream)),
+       "ep_balance_loss");
+    return {l, c, f};
+}
+
+at::Tensor route_backward(int64_t router, const at::Tensor& logits, const at::Tensor& topk_idx,
+                          const c10::optional<at::Tensor>& grad_topk_w, const c10::optional<at::Tensor>& counts,
+                          const c10::optional<at::Tensor>& coef, const c10::optional<at::Tensor>& grad_loss,
+                          const c10::optional<at::Tensor>& seq_off, const c10::optional<at::Tensor>& grad_logits,
+                          int64_t stream, int64_t dev) {
+    const ep_router r = router_of(router, logits);
+    const int64_t T = logits.size(0), E = r.num_experts, S = sequences(seq_off);
+    shape(topk_idx, {T, r.num_topk}, "topk_idx");
+    opt_shape(grad_topk_w, {T, r.num_topk}, "grad_topk_w");
+    opt_shape(counts, {S, E}, "counts");
+    opt_shape(coef, {S}, "coef");
+    opt_shape(grad_loss, {}, "grad_loss");
+    const void* pl = ptr(logits, "logits", logits.scalar_type(), dev);
+    const void* pi = ptr(topk_idx, "topk_idx", idx_type(r), dev);
+    at::Tensor g = output(grad_logits, {T, E}, logits.scalar_type(), logits, "grad_logits");
+    ok(ep_route_backward(&r, width(T), pl, pi, (const float*)opt_ptr(grad_topk_w, "grad_topk_w", at::kFloat, dev),
+                         (const int32_t*)opt_ptr(counts, "counts", at::kInt, dev),
+                         (const float*)opt_ptr(coef, "coef", at::kFloat, dev),
+                         (const float*)opt_ptr(grad_loss, "grad_loss", at::kFloat, dev),
+                         (const int32_t*)opt_ptr(seq_off, "seq_off", at::kInt, dev), (int32_t)S,
+                         ptr(g, "grad_logits", logits.scalar_type(), dev), stream_of(stream)),
+       "ep_route_backward");
+    return g;
+}
+
 }  // namespace
 
 PYBIND11_MODULE(TORCH_EXTENSION_NAME, m) {
@@ -350,4 +445,7 @@ PYBIND11_MODULE(TORCH_EXTENSION_NAME, m) {
     m.def("grouped_gemm_mxfp4", &grouped_gemm_mxfp4);
     m.def("rms_norm", &rms_norm);
     m.def("rms_norm_backward", &rms_norm_backward);
+    m.def("route", &route);
+    m.def("balance_loss", &balance_loss);
+    m.def("route_backward", &route_backward);
 }

@@ -57,6 +57,8 @@ BF16 = F.EP_BF16
 FP8_QUANTIZE = F.EP_FP8_QUANTIZE
 FP8_PREQUANT = F.EP_FP8_PREQUANT
 FLAG_NO_ZERO_PAD = F.EP_FLAG_NO_ZERO_PAD
+SCORE_SOFTMAX = F.EP_SCORE_SOFTMAX
+SCORE_SIGMOID = F.EP_SCORE_SIGMOID
 
 
 @dataclasses.dataclass(frozen=True)
@@ -437,6 +439,85 @@ def rms_norm_backward(total: torch.Tensor, weight: torch.Tensor, rstd: torch.Ten
     cur = _current_device()
     return _B.rms_norm_backward(total, weight, rstd, grad_y, grad_total, grad_x, grad_weight, workspace,
                                 _raw_stream(cur), cur)
+
+
+# ---------------------------------------------------------------- router
+
+@dataclasses.dataclass(frozen=True)
+class Router:
+    """Sizes and rule of a router. Logits may be float32 or bfloat16 in any call."""
+    num_experts: int
+    num_topk: int
+    score: int = SCORE_SOFTMAX
+    num_groups: int = 1
+    topk_groups: int = 1
+    group_best: int = 1
+    renormalize: bool = False
+    scale: float = 1.0
+    idx_bits: int = 64
+
+    def c(self) -> F.ep_router:
+        """The C struct, built once per Router (cached on the instance)."""
+        c = self.__dict__.get("_c_struct")
+        if c is None:
+            c = F.ep_router(self.num_experts, self.num_topk, self.score, self.num_groups, self.topk_groups,
+                            self.group_best, int(self.renormalize), self.idx_bits, 1, self.scale)
+            object.__setattr__(self, "_c_struct", c)
+            object.__setattr__(self, "_c_addr", ctypes.addressof(c))
+        return c
+
+    def c_addr(self) -> int:
+        """Address of the cached C struct (the compiled binding reads it)."""
+        a = self.__dict__.get("_c_addr")
+        if a is None:
+            self.c()
+            a = self.__dict__["_c_addr"]
+        return a
+
+
+def route(router: Router, logits: torch.Tensor, bias: Optional[torch.Tensor] = None,
+          token_mask: Optional[torch.Tensor] = None, topk_idx: Optional[torch.Tensor] = None,
+          topk_w: Optional[torch.Tensor] = None):
+    """Chooses each token's experts from its logits [T, E]. Returns (topk_idx,
+    topk_w), [T, k], highest key first, which layout and dispatch_forward take.
+    bias [E] float32 steers the choice alone; token_mask [T] bool: tokens that
+    are False (padding) get -1 and 0. An expert with a logit or bias of
+    -infinity is never chosen; -1 and 0 where none is left."""
+    cur = _current_device()
+    return _B.route(router.c_addr(), logits, bias, token_mask, topk_idx, topk_w, _raw_stream(cur), cur)
+
+
+def balance_loss_workspace(router: Router, num_tokens: int, num_seqs: int = 1, device="cuda") -> torch.Tensor:
+    """Workspace of balance_loss, for callers that keep one."""
+    n = F.ep_balance_loss_workspace_bytes(router.c(), num_tokens, num_seqs)
+    if n == 0:
+        raise F.EPError(F.EP_ERR_INVALID_ARG, "ep_balance_loss_workspace_bytes", F.last_error_message())
+    return torch.empty(n, dtype=torch.uint8, device=device)
+
+
+def balance_loss(router: Router, logits: torch.Tensor, topk_idx: torch.Tensor, seq_off: Optional[torch.Tensor] = None,
+                 loss: Optional[torch.Tensor] = None, counts: Optional[torch.Tensor] = None,
+                 coef: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None):
+    """The balance loss of a batch, the mean over its sequences (seq_off int32
+    [S + 1]; without it the batch is one). Returns (loss, counts, coef): a
+    scalar; the pairs of each sequence and expert, int32 [S, E]; and the factor
+    of each sequence [S], which route_backward takes with the counts."""
+    cur = _current_device()
+    return _B.balance_loss(router.c_addr(), logits, topk_idx, seq_off, loss, counts, coef, workspace, _raw_stream(cur),
+                           cur)
+
+
+def route_backward(router: Router, logits: torch.Tensor, topk_idx: torch.Tensor,
+                   grad_topk_w: Optional[torch.Tensor] = None, counts: Optional[torch.Tensor] = None,
+                   coef: Optional[torch.Tensor] = None, grad_loss: Optional[torch.Tensor] = None,
+                   seq_off: Optional[torch.Tensor] = None, grad_logits: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Gradient of route's weights (grad_topk_w [T, k]) and of balance_loss
+    (grad_loss, a scalar tensor, with the loss's counts, coef and seq_off) with
+    respect to the logits: [T, E] in the logits' type. Either may be left out."""
+    cur = _current_device()
+    return _B.route_backward(router.c_addr(), logits, topk_idx, grad_topk_w, counts, coef, grad_loss, seq_off,
+                             grad_logits, _raw_stream(cur), cur)
+
 
 # ---------------------------------------------------------------- bound calls
 

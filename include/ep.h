@@ -451,6 +451,108 @@ ep_status ep_rms_norm_backward(int32_t num_tokens, int32_t hidden, const void* t
                                const float* rstd, const void* grad_y, const void* grad_total, void* grad_x,
                                float* grad_weight, void* workspace, size_t workspace_bytes, void* stream);
 
+/* ---- The router: what stands between the norm and the layout. ---- */
+
+/* Scores of a token's experts from its logits l. */
+typedef enum { EP_SCORE_SOFTMAX = 0, EP_SCORE_SIGMOID = 1 } ep_score;
+
+/* Sizes and rule of a router. Limits: 1 <= num_experts <= 1024,
+ * 1 <= num_topk <= 32, num_groups divides num_experts and is at most 64,
+ * 1 <= topk_groups <= num_groups, group_best 1 or 2 and at most the
+ * num_experts / num_groups experts of a group, num_topk at most the
+ * topk_groups * num_experts / num_groups experts that stay, scale finite. */
+typedef struct {
+    int32_t num_experts;  /* E */
+    int32_t num_topk;     /* k */
+    int32_t score;        /* ep_score */
+    int32_t num_groups;   /* G: experts in G contiguous groups; 1 = no groups */
+    int32_t topk_groups;  /* groups whose experts a token may choose */
+    int32_t group_best;   /* a group goes by the sum of its 1 or 2 highest keys */
+    int32_t renormalize;  /* 1: a token's weights are divided by their sum */
+    int32_t idx_bits;     /* 64 or 32: type of topk_idx */
+    int32_t logits_f32;   /* 1: logits (and their gradient) binary32, 0: bf16 */
+    float scale;          /* factor of the weights */
+} ep_router;
+
+/* Chooses each token's experts: the topk_idx and topk_w that ep_layout and
+ * ep_combine take. For every token, with l its logits and e < E,
+ *   s[e] = exp(l[e] - max l) / sum_i exp(l[i] - max l)   (EP_SCORE_SOFTMAX)
+ *        = 1 / (1 + exp(-l[e]))                           (EP_SCORE_SIGMOID);
+ *   key[e] = s[e] + bias[e], in binary64; the logit itself when there is no bias
+ *        and group_best is 1, where scores order as logits do;
+ * the topk_groups groups with the largest sums of their group_best highest keys
+ * stay (num_groups > 1), and of their experts the k with the highest keys are
+ * chosen, highest first; among equals the lowest index goes first. Then
+ *   topk_w[j] = scale * s[i_j]  or, with renormalize,
+ *               scale * s[i_j] / (sum_m s[i_m] + 1e-20),
+ * in binary32: the bias steers the choice alone.
+ * An expert whose logit or bias is -infinity is never chosen. Where that
+ * leaves fewer than k (a group none), the remaining topk_idx are -1 and their
+ * weights 0: ep_layout skips such pairs. A key that is NaN counts as the lowest
+ * finite number; NaN and +infinity reach the weights by the formulas.
+ *   logits      device [num_tokens, E], binary32 or bf16.
+ *   bias        device binary32 [E], or NULL.
+ *   token_mask  device bytes [num_tokens], or NULL: a token whose byte is 0
+ *               (padding of a batch) gets topk_idx -1 and weights 0, and its
+ *               logits are not read.
+ *   topk_idx    device [num_tokens, k], int64 or int32 per idx_bits.
+ *   topk_w      device binary32 [num_tokens, k].
+ * num_tokens is at most 2^25. One launch. */
+ep_status ep_route(const ep_router* r, int32_t num_tokens, const void* logits, const float* bias,
+                   const uint8_t* token_mask, void* topk_idx, float* topk_w, void* stream);
+
+/* Bytes of workspace ep_balance_loss needs; 0 when the arguments are invalid
+ * (see ep_last_error_message). */
+size_t ep_balance_loss_workspace_bytes(const ep_router* r, int32_t num_tokens, int32_t num_seqs);
+
+/* The balance loss of a batch, for every sequence of it, with the counts. A token
+ * is routed when one of its topk_idx lies in [0, E); others (padding) enter
+ * nothing. With p the shares of a token's scores (softmax: s; sigmoid:
+ * s / sum_i s[i]), for every sequence q and expert e
+ *   counts[q, e] = pairs of q's tokens with topk_idx = e,
+ *   N_q          = routed tokens of q, Q = sequences with N_q > 0,
+ *   coef[q]      = E / (k N_q^2 Q), 0 where N_q is 0;
+ *   loss         = sum_q coef[q] * sum_e counts[q, e] * sum_t p[t, e]
+ * over q's routed tokens t: 1 where scores and counts are even.
+ *   topk_idx    device [num_tokens, k] per idx_bits; ids outside [0, E) are no pairs.
+ *   seq_off     device int32 [num_seqs + 1], ascending: sequence q has tokens
+ *               [seq_off[q], seq_off[q + 1]), as far as they lie in [0, num_tokens);
+ *               tokens before the first and past the last enter nothing. NULL: one
+ *               sequence of all tokens, num_seqs 1.
+ *   loss        device binary32 [1].
+ *   counts      device int32 [num_seqs, E].
+ *   coef        device binary32 [num_seqs].
+ *   workspace   device, >= ep_balance_loss_workspace_bytes, 256-byte aligned; not
+ *               to be shared by calls that may overlap.
+ * Sums over tokens are taken in an order that depends on the sizes and seq_off
+ * alone. num_tokens is at most 2^25, num_seqs 2^20. Two launches, three for several
+ * sequences. */
+ep_status ep_balance_loss(const ep_router* r, int32_t num_tokens, const void* logits, const void* topk_idx,
+                          const int32_t* seq_off, int32_t num_seqs, float* loss, int32_t* counts, float* coef,
+                          void* workspace, size_t workspace_bytes, void* stream);
+
+/* Gradient of ep_route's weights and of ep_balance_loss with respect to the
+ * logits (the choice and the counts are constants). With n[e] how often e stands
+ * in a token's topk_idx, g[e] the sum of its grad_topk_w there, and
+ * D = sum_e n[e] s[e] + 1e-20,
+ *   u[e] = scale * g[e]  or, with renormalize,
+ *          scale * (g[e] - n[e] * (sum_i g[i] s[i]) / D) / D;
+ *   b[e] = grad_loss * coef[q] * counts[q, e], q the token's sequence;
+ * softmax: grad_logits = s[e] * (u[e] + b[e] - sum_i s[i] (u[i] + b[i]));
+ * sigmoid: grad_logits = s[e] (1 - s[e]) * (u[e] + (b[e] - sum_i p[i] b[i]) / sum_i s[i]).
+ * A token that is not routed gets zeros. Ids outside [0, E) add nothing.
+ *   grad_topk_w  device binary32 [num_tokens, k], or NULL (the loss's gradient alone).
+ *   counts, coef, grad_loss  ep_balance_loss's, and the loss's gradient (device
+ *                binary32 [1]); all three or none of them (the weights' gradient alone).
+ *   seq_off, num_seqs  as ep_balance_loss's (NULL and 1 without counts).
+ *   grad_logits  device [num_tokens, E], binary32 or bf16 as logits; may be the
+ *                logits' own buffer.
+ * num_tokens is at most 2^25. One launch. */
+ep_status ep_route_backward(const ep_router* r, int32_t num_tokens, const void* logits, const void* topk_idx,
+                            const float* grad_topk_w, const int32_t* counts, const float* coef,
+                            const float* grad_loss, const int32_t* seq_off, int32_t num_seqs, void* grad_logits,
+                            void* stream);
+
 /* Copies cnt and pad (host arrays of E, either may be NULL) and the row
  * total R (host, may be NULL) to the host. Synchronises the stream: this is
  * the README's CPU synchronisation of a non-cached dispatch. */

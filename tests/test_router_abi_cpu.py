@@ -1,0 +1,109 @@
+"""Argument checks of the router's calls on the CPU: every call below fails a check
+before anything reaches the GPU, so no pointer is dereferenced."""
+import ctypes
+
+import pytest
+
+from combine_ep_layout_10_amd import _ffi as F
+
+FAKE = ctypes.c_void_p(1 << 20)
+BAD, UNSUP, WS = F.EP_ERR_INVALID_ARG, F.EP_ERR_UNSUPPORTED, F.EP_ERR_WORKSPACE
+
+
+def off(n):
+    return ctypes.c_void_p((1 << 20) + n)
+
+
+def router(**kw):
+    d = dict(num_experts=64, num_topk=8, score=0, num_groups=1, topk_groups=1, group_best=1, renormalize=0, idx_bits=64,
+             logits_f32=1, scale=1.0)
+    d.update(kw)
+    return F.ep_router(*[d[n] for n, _ in F.ep_router._fields_])
+
+
+def calls(r, T):
+    l, p = F.lib(), None if r is None else ctypes.byref(r)
+    return {
+        "route": l.ep_route(p, T, FAKE, None, None, FAKE, FAKE, None),
+        "balance": l.ep_balance_loss(p, T, FAKE, FAKE, None, 1, FAKE, FAKE, FAKE, FAKE, 1 << 40, None),
+        "backward": l.ep_route_backward(p, T, FAKE, FAKE, FAKE, None, None, None, None, 1, FAKE, None),
+    }
+
+
+@pytest.mark.parametrize("kw", [
+    dict(num_experts=0), dict(num_experts=1025), dict(num_topk=0), dict(num_topk=33), dict(num_topk=9, num_experts=8),
+    dict(score=2), dict(score=-1), dict(num_groups=0), dict(num_groups=3), dict(num_groups=128, num_experts=1024),
+    dict(topk_groups=0), dict(topk_groups=2), dict(group_best=0), dict(group_best=3),
+    dict(num_groups=64, topk_groups=64, group_best=2), dict(num_groups=16, topk_groups=1), dict(renormalize=2),
+    dict(idx_bits=16), dict(logits_f32=2), dict(scale=float("inf")), dict(scale=float("nan"))])
+def test_router_sizes(kw):
+    for name, st in calls(router(**kw), 4).items():
+        assert st == BAD, name
+    assert F.lib().ep_balance_loss_workspace_bytes(ctypes.byref(router(**kw)), 4, 1) == 0
+
+
+def test_tokens():
+    assert all(st == BAD for st in calls(None, 4).values())
+    assert all(st == BAD for st in calls(router(), -1).values())
+    assert all(st == UNSUP for st in calls(router(), (1 << 25) + 1).values())
+    assert "num_tokens" in F.last_error_message()
+
+
+def test_route_pointers():
+    l, r = F.lib(), ctypes.byref(router())
+    assert l.ep_route(r, 4, None, None, None, FAKE, FAKE, None) == BAD
+    assert l.ep_route(r, 4, off(2), None, None, FAKE, FAKE, None) == BAD
+    assert "logits" in F.last_error_message()
+    assert l.ep_route(r, 4, FAKE, off(1), None, FAKE, FAKE, None) == BAD
+    assert "bias" in F.last_error_message()
+    assert l.ep_route(r, 4, FAKE, None, None, off(4), FAKE, None) == BAD
+    assert "topk_idx" in F.last_error_message()
+    assert l.ep_route(r, 4, FAKE, None, None, FAKE, None, None) == BAD
+    assert "topk_w" in F.last_error_message()
+    half = ctypes.byref(router(logits_f32=0, idx_bits=32))
+    assert l.ep_route(half, 4, off(1), None, None, FAKE, FAKE, None) == BAD
+    assert l.ep_route(half, 0, None, None, None, None, None, None) == F.EP_OK  # nothing to launch
+
+
+def test_balance_pointers():
+    l, r = F.lib(), ctypes.byref(router())
+    ok = [r, 4, FAKE, FAKE, FAKE, 3, FAKE, FAKE, FAKE, FAKE, 1 << 40, None]
+
+    def call(**kw):
+        a = list(ok)
+        for i, v in kw.items():
+            a[int(i[1:])] = v
+        return l.ep_balance_loss(*a)
+
+    for i in (2, 3, 6, 7, 8, 9):
+        assert call(**{"a%d" % i: None}) == BAD, i
+        assert call(**{"a%d" % i: off(1)}) == BAD, i
+    assert call(a4=None) == BAD and "seq_off" in F.last_error_message()
+    assert call(a4=off(2)) == BAD
+    assert call(a5=0) == BAD and call(a5=-1) == BAD
+    assert call(a5=(1 << 20) + 1) == UNSUP
+    assert call(a9=off(128)) == BAD
+    need = l.ep_balance_loss_workspace_bytes(r, 4, 3)
+    assert need > 0 and need % 256 == 0
+    assert call(a10=need - 1) == WS
+    assert l.ep_balance_loss_workspace_bytes(r, 4, 0) == 0
+    assert l.ep_balance_loss_workspace_bytes(r, 1 << 25, 1 << 20) > 4 * 64 * ((1 << 19) + (1 << 20)) * 2
+
+
+def test_backward_pointers():
+    l, r = F.lib(), ctypes.byref(router())
+    ok = [r, 4, FAKE, FAKE, FAKE, FAKE, FAKE, FAKE, FAKE, 3, FAKE, None]
+
+    def call(**kw):
+        a = list(ok)
+        for i, v in kw.items():
+            a[int(i[1:])] = v
+        return l.ep_route_backward(*a)
+
+    for i in (2, 3, 5, 6, 7, 8, 10):
+        assert call(**{"a%d" % i: None}) == BAD, i
+    for i in (2, 3, 4, 5, 6, 7, 8, 10):
+        assert call(**{"a%d" % i: off(1)}) == BAD, i
+    assert call(a5=None, a6=None, a7=None) == BAD and "seq_off" in F.last_error_message()
+    assert call(a4=None, a5=None, a6=None, a7=None, a8=None, a9=1) == BAD
+    assert "grad_topk_w" in F.last_error_message()
