@@ -114,6 +114,10 @@ _SIGNATURES = {
                                                         ctypes.c_int32, ctypes.c_int32, _P, _P]),
     "ep_grouped_gemm_mxfp4": (ctypes.c_int, [ctypes.POINTER(ep_handle), _P, _P, _P, ctypes.c_int32, ctypes.c_int32,
                                              _P, _P]),
+    "ep_quantize_mxfp4": (ctypes.c_int, [ctypes.POINTER(ep_handle), ctypes.c_int64, ctypes.c_int32, ctypes.c_int32, _P,
+                                         _P, _P, _P, _P]),
+    "ep_grouped_gemm_mxfp4_rows": (ctypes.c_int, [ctypes.POINTER(ep_handle), _P, _P, _P, _P, ctypes.c_int32,
+                                                  ctypes.c_int32, _P, _P]),
     "ep_rms_norm": (ctypes.c_int, [ctypes.c_int32, ctypes.c_int32, ctypes.c_int32, _P, _P, _P, ctypes.c_float, _P, _P,
                                    _P, _P, _P]),
     "ep_rms_norm_workspace_bytes": (ctypes.c_size_t, [ctypes.c_int32, ctypes.c_int32]),
@@ -248,6 +252,20 @@ def ep_grouped_gemm_mxfp4(h: ep_handle, a: int, b: int, b_scales: int, n: int, k
     st = (_lib or lib()).ep_grouped_gemm_mxfp4(ctypes.byref(h), a, b, b_scales, n, k, out, stream)
     if st != EP_OK:
         _check(st, "ep_grouped_gemm_mxfp4")
+
+
+def ep_quantize_mxfp4(h, rows: int, k: int, x_f32: int, x: int, codes: int, scales: int, values, stream: int) -> None:
+    st = (_lib or lib()).ep_quantize_mxfp4(None if h is None else ctypes.byref(h), rows, k, x_f32, x, codes, scales,
+                                           values, stream)
+    if st != EP_OK:
+        _check(st, "ep_quantize_mxfp4")
+
+
+def ep_grouped_gemm_mxfp4_rows(h: ep_handle, a: int, a_scales: int, b: int, b_scales: int, n: int, k: int, out: int,
+                               stream: int) -> None:
+    st = (_lib or lib()).ep_grouped_gemm_mxfp4_rows(ctypes.byref(h), a, a_scales, b, b_scales, n, k, out, stream)
+    if st != EP_OK:
+        _check(st, "ep_grouped_gemm_mxfp4_rows")
 
 
 def ep_rms_norm(num_tokens: int, hidden: int, dtype: int, x: int, residual, weight: int, eps: float, total, y: int,

@@ -17,7 +17,8 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libep.so")
 SOURCES = ["ep_api.hip", "ep_layout.hip", "ep_dispatch.hip", "ep_combine.hip", "ep_fused.hip", "ep_gemm.hip",
-           "ep_gemm_bf16.hip", "ep_gemm_stream.hip", "ep_norm.hip", "ep_route.hip"]
+           "ep_gemm_bf16.hip", "ep_gemm_stream.hip", "ep_norm.hip", "ep_route.hip",
+           "ep_mxfp4.hip", "ep_gemm_fp4.hip"]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"
 

@@ -767,6 +767,72 @@ ep_status ep_grouped_gemm_mxfp4(const ep_handle* h, const void* a, const void* b
     return EP_OK;
 }
 
+ep_status ep_quantize_mxfp4(const ep_handle* h, int64_t rows, int32_t k, int32_t x_f32, const void* x, void* codes,
+                            void* scales, void* values, void* stream) {
+    if (h != nullptr) {
+        ep_status s = check_handle(h);
+        if (s != EP_OK) return s;
+        if (h->row_src == nullptr) return fail(EP_ERR_INVALID_ARG, "handle has NULL arrays (not built by ep_layout?)");
+        if (rows != rows_bound(h->cfg))
+            return fail(EP_ERR_INVALID_ARG, "rows %lld differ from the layout's bound %lld", (long long)rows,
+                        (long long)rows_bound(h->cfg));
+    }
+    if (rows < 0) return fail(EP_ERR_INVALID_ARG, "rows %lld must not be negative", (long long)rows);
+    if (k < 32 || k % 32 != 0) return fail(EP_ERR_INVALID_ARG, "k %d must be a positive multiple of 32", k);
+    if (k > kMaxProductWidth) return fail(EP_ERR_UNSUPPORTED, "k %d may be at most %d", k, kMaxProductWidth);
+    if (rows > (1ll << 42) / k) return fail(EP_ERR_UNSUPPORTED, "rows * k may be at most 2^42");
+    if (x_f32 != 0 && x_f32 != 1) return fail(EP_ERR_INVALID_ARG, "x_f32 %d must be 0 or 1", x_f32);
+    // without a row (or a pair) nothing is read or written
+    const bool work = h != nullptr ? h->num_tokens > 0 : rows > 0;
+    if ((work && x == nullptr) || !aligned(x, 16))
+        return fail(EP_ERR_INVALID_ARG, "x must be non-NULL and 16-byte aligned");
+    if ((work && codes == nullptr) || !aligned(codes, 16))
+        return fail(EP_ERR_INVALID_ARG, "codes must be non-NULL and 16-byte aligned");
+    if (work && scales == nullptr) return fail(EP_ERR_INVALID_ARG, "scales must be non-NULL");
+    if (!aligned(values, 16)) return fail(EP_ERR_INVALID_ARG, "values must be 16-byte aligned");
+    if (!work) return EP_OK;
+    ep::QuantArgs a;
+    memset(&a, 0, sizeof a);
+    if (h != nullptr) {
+        a.rows = rows_args(h);
+        a.row_src = h->row_src;
+    }
+    a.x = x;
+    a.codes = (uint8_t*)codes;
+    a.scales = (uint8_t*)scales;
+    a.values = (uint16_t*)values;
+    hipError_t e = ep::launch_quantize_mxfp4(a, rows, k, h != nullptr, x_f32 != 0, (hipStream_t)stream);
+    if (e != hipSuccess) return hip_fail(e, "MXFP4 quantisation launch");
+    return EP_OK;
+}
+
+ep_status ep_grouped_gemm_mxfp4_rows(const ep_handle* h, const void* a, const void* a_scales, const void* b,
+                                     const void* b_scales, int32_t n, int32_t k, void* out, void* stream) {
+    ep_status s = check_product(h, n, k, 32);
+    if (s != EP_OK) return s;
+    const int64_t pairs = (int64_t)h->num_tokens * h->cfg.num_topk;
+    if (pairs > kMaxProductPairs)
+        return fail(EP_ERR_UNSUPPORTED, "%lld token-expert pairs exceed %lld", (long long)pairs,
+                    (long long)kMaxProductPairs);
+    if (pairs > 0 &&
+        (a == nullptr || a_scales == nullptr || b == nullptr || b_scales == nullptr || out == nullptr))
+        return fail(EP_ERR_INVALID_ARG, "a, a_scales, b, b_scales and out must be non-NULL");
+    if (!aligned(a, 16) || !aligned(b, 16) || !aligned(out, 16))
+        return fail(EP_ERR_INVALID_ARG, "a, b and out must be 16-byte aligned");
+    ep::Fp4Args g;
+    g.rows = rows_args(h);
+    g.x = (const uint8_t*)a;
+    g.x_scales = (const uint8_t*)a_scales;
+    g.b = (const uint8_t*)b;
+    g.b_scales = (const uint8_t*)b_scales;
+    g.out = (uint16_t*)out;
+    g.N = n;
+    g.K = k;
+    hipError_t e = ep::launch_grouped_gemm_mxfp4_rows(g, pairs, (hipStream_t)stream);
+    if (e != hipSuccess) return product_fail(e, "MXFP4 rows grouped GEMM launch");
+    return EP_OK;
+}
+
 ep_status ep_rms_norm(int32_t num_tokens, int32_t hidden, int32_t dtype, const void* x, const void* residual,
                       const void* weight, float eps, void* total, void* y, float* y_scales, float* rstd,
                       void* stream) {

@@ -1,0 +1,256 @@
+// Products grouped by expert with both operands in MXFP4, on the matrix unit's own
+// 4-bit form. For rows r of expert e:
+//   out[r, c] = bf16( sum_k a[r, k] * b[e, c, k] ),
+// a and b code times power of two; products are exact, sums are the matrix unit's in
+// binary32, and the only other rounding is the output's.
+//
+// The weights go from memory straight into registers; a block of 8 waves takes up to
+// TB rows of one expert by 128 MC / S output columns. A wave's piece is 16 MC columns
+// of the weights as the MFMA's first operand. The reduction runs in units of 512: lane
+// (g, r16) reads codes 128 g .. + 127 of its column (four 16-byte loads) with their
+// four scales (one word), and MFMA t takes the t-th 32 of each group, so its scale is byte t.
+// The rows (second operand) are shared by the block through LDS in slices of NC
+// units, two slices deep; 16-byte chunk c of a unit of row r is stored at c ^
+// row_slot(r), which meets each bank once in every read. S splits the reduction over
+// the waves of a block, so that a small problem still reaches every CU: wave group ks
+// takes the ks-th part of every slice, and the S sums are added in order at the end.
+#include <type_traits>
+
+#include "ep_fp4_dev.h"
+#include "ep_rows_dev.h"
+
+namespace ep {
+
+namespace {
+
+constexpr int kWaves = 8;
+constexpr int kUnit = 512;  // of the reduction: 256 bytes of codes and 16 of scales a row
+
+__device__ __forceinline__ int row_slot(int r) { return (row_swizzle16(r) << 2) | (r & 3); }
+
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t resource(const void* p, int size) {
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), 0, size, kBufferFlags);
+}
+
+// Slices: units of a slice, and what a slice of rows takes in LDS (scales padded by
+// a word a row, so that 16 rows' words lie in different banks).
+template <int TB, int S>
+struct Slice {
+    static constexpr int NC = TB == 16 && S == 8 ? 16 : TB == 32 && S == 4 ? 8 : 128 / TB;
+    static constexpr int B = NC / S;              // units of a wave group
+    static constexpr int kCodes = TB * NC * 256;  // bytes
+    static constexpr int kPitch = NC * 16 + 4;    // scales of a row
+    static constexpr int kBytes = kCodes + TB * kPitch;
+};
+
+// Rows m0 .. m0 + rows - 1 of the expert (rows <= 16 NT) by the block's columns.
+template <int TB, int MC, int S, int NT>
+__device__ __forceinline__ void run_tile(const Fp4Args& a, const ExpertRows& er, int e, int m0, int rows, int n0,
+                                         uint8_t* s_x) {
+    using L = Slice<TB, S>;
+    constexpr int NC = L::NC, B = L::B, P = B > 1 ? 2 : 1;
+    constexpr int kRows = NT * 16, XL = (kRows * NC * 16 + 64 * kWaves - 1) / (64 * kWaves);
+    constexpr int SL = (kRows * NC * 4 + 64 * kWaves - 1) / (64 * kWaves);
+    const int tid = threadIdx.x, lane = tid & 63, r16 = lane & 15, g = lane >> 4;
+    const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int ks = w / (kWaves / S), cw = w % (kWaves / S);
+    const int half = a.K / 2, groups = a.K / 32;  // bytes of a row's codes and scales
+    const int slices = (a.K + NC * kUnit - 1) / (NC * kUnit);
+    const int c0 = n0 + 16 * MC * cw;
+    const int cols = max(0, min(16 * MC, a.N - c0));
+    const int64_t first_col = (int64_t)e * a.N + min(c0, a.N - 1), first_row = (int64_t)er.first + m0;
+    const __amdgpu_buffer_rsrc_t rw = resource(a.b + first_col * half, cols * half);
+    const __amdgpu_buffer_rsrc_t rx = resource(a.x + first_row * half, rows * half);
+    const uint8_t* const w_scales = a.b_scales + first_col * groups;
+    const uint8_t* const x_scales = a.x_scales + first_row * groups;
+
+    u32x4_t code[P][MC][4];
+    uint32_t scale[P][MC];
+    // unit u of the reduction; columns past N, and the reduction past K, are zero
+    const auto load = [&](int u, int p) {
+#pragma unroll
+        for (int c = 0; c < MC; ++c) {
+#pragma unroll
+            for (int t = 0; t < 4; ++t) {
+                const int byte = u * 256 + g * 64 + t * 16;
+                code[p][c][t] = __builtin_amdgcn_raw_buffer_load_b128(
+                    rw, byte < half ? (16 * c + r16) * half + byte : kOutOfRange, 0, 0);
+            }
+            scale[p][c] = load_scales4(w_scales + (int64_t)min(16 * c + r16, max(cols - 1, 0)) * groups,
+                                       u * 16 + g * 4, groups);
+        }
+    };
+    u32x4_t xr[XL];
+    uint32_t xs[SL];
+    const auto load_rows = [&](int kc) {
+#pragma unroll
+        for (int j = 0; j < XL; ++j) {
+            const int q = j * 64 * kWaves + tid, row = q / (NC * 16), byte = (kc * NC * 16 + q % (NC * 16)) * 16;
+            xr[j] = __builtin_amdgcn_raw_buffer_load_b128(rx, row < rows && byte < half ? row * half + byte : kOutOfRange,
+                                                          0, 0);
+        }
+#pragma unroll
+        for (int j = 0; j < SL; ++j) {
+            const int q = j * 64 * kWaves + tid, row = q / (NC * 4);
+            xs[j] = row < rows ? load_scales4(x_scales + (int64_t)row * groups, (kc * NC * 4 + q % (NC * 4)) * 4, groups)
+                               : 0u;
+        }
+    };
+    const auto store_rows = [&](int stage) {
+        uint8_t* const at = s_x + stage * L::kBytes;
+#pragma unroll
+        for (int j = 0; j < XL; ++j) {
+            const int q = j * 64 * kWaves + tid, row = q / (NC * 16), c = q % (NC * 16);
+            if (row < kRows) *(u32x4_t*)(at + row * (NC * 256) + ((c ^ row_slot(row & 15)) << 4)) = xr[j];
+        }
+#pragma unroll
+        for (int j = 0; j < SL; ++j) {
+            const int q = j * 64 * kWaves + tid, row = q / (NC * 4), c = q % (NC * 4);
+            if (row < kRows) *(uint32_t*)(at + L::kCodes + row * L::kPitch + c * 4) = xs[j];
+        }
+    };
+
+    load_rows(0);
+#pragma unroll
+    for (int p = 0; p < P; ++p) load(ks * B + p, p);
+    f32x4_t acc[NT][MC];
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int c = 0; c < MC; ++c) acc[n][c] = (f32x4_t){0.0f, 0.0f, 0.0f, 0.0f};
+    store_rows(0);
+    wait_lgkmcnt0();
+    block_barrier();
+
+    for (int kc = 0; kc < slices; ++kc) {
+        // the next slice of rows travels while this one is used; its place in LDS
+        // was last read a barrier ago
+        if (kc + 1 < slices) load_rows(kc + 1);
+        const uint8_t* const x = s_x + (kc & 1) * L::kBytes;
+#pragma unroll
+        for (int b = 0; b < B; ++b) {
+            const int p = b % P, u = ks * B + b;
+            uint32_t row_scale[NT];
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+                row_scale[n] = *(const uint32_t*)(x + L::kCodes + (16 * n + r16) * L::kPitch + u * 16 + g * 4);
+            const auto part = [&](auto tt) {
+                constexpr int t = decltype(tt)::value;
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+                    const u32x4_t v = *(const u32x4_t*)(x + (16 * n + r16) * (NC * 256) +
+                                                        ((16 * u + ((4 * g + t) ^ row_slot(r16))) << 4));
+#pragma unroll
+                    for (int c = 0; c < MC; ++c)
+                        acc[n][c] = mfma_fp4<t>(code[p][c][t], v, acc[n][c], scale[p][c], row_scale[n]);
+                }
+            };
+            part(std::integral_constant<int, 0>());
+            part(std::integral_constant<int, 1>());
+            part(std::integral_constant<int, 2>());
+            part(std::integral_constant<int, 3>());
+            // the unit P further on in this wave's order: b + P of this slice, or of the next
+            load((b + P < B ? kc : kc + 1) * NC + ks * B + (b + P) % B, p);
+        }
+        if (kc + 1 < slices) store_rows((kc + 1) & 1);
+        wait_lgkmcnt0();
+        block_barrier();
+    }
+
+    if (S > 1) {  // the groups' sums, in order
+        f32x4_t* sum = (f32x4_t*)s_x;
+        if (ks > 0) {
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int c = 0; c < MC; ++c) sum[((w * NT + n) * MC + c) * 64 + lane] = acc[n][c];
+        }
+        wait_lgkmcnt0();
+        block_barrier();
+        if (ks > 0) return;
+#pragma unroll
+        for (int s = 1; s < S; ++s)
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int c = 0; c < MC; ++c)
+                    acc[n][c] += sum[(((s * (kWaves / S) + cw) * NT + n) * MC + c) * 64 + lane];
+    }
+    // lane: row r16 of each piece, columns 4 g .. 4 g + 3
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int c = 0; c < MC; ++c) {
+            const int row = 16 * n + r16, col = c0 + 16 * c + 4 * g;
+            if (row < rows && col < a.N)
+                *(uint2*)(a.out + (first_row + row) * a.N + col) =
+                    make_uint2(pack_bf16x2(acc[n][c][0], acc[n][c][1]), pack_bf16x2(acc[n][c][2], acc[n][c][3]));
+        }
+}
+
+template <int TB, int MC, int S>
+__global__ __launch_bounds__(64 * kWaves) void k_grouped_gemm_fp4_stream(Fp4Args a) {
+    constexpr int kCols = 16 * MC * kWaves / S;
+    __shared__ __attribute__((aligned(16))) uint8_t s_x[2 * Slice<TB, S>::kBytes];
+    const int nt_n = (a.N + kCols - 1) / kCols;
+    int e, local;
+    if (!find_expert(a.rows, TB, nt_n, &e, &local)) return;
+    e = __builtin_amdgcn_readfirstlane(e);
+    const ExpertRows er = expert_rows(a.rows, e);
+    // row tiles of one column tile are neighbours: they read the same weights.
+    // An expert's rows are cut into tiles of equal size, rounded up to 16.
+    const int nt_m = (er.live + TB - 1) / TB, m = local % nt_m;
+    const int each = ((er.live + nt_m - 1) / nt_m + 15) & ~15;
+    const int m0 = __builtin_amdgcn_readfirstlane(m * each);
+    const int rows = __builtin_amdgcn_readfirstlane(min(each, er.live - m0));
+    const int n0 = __builtin_amdgcn_readfirstlane(local / nt_m * kCols);
+    if (a.rows.zero_pad && m == nt_m - 1) clear_padding<kCols>(a.out, a.N, er, n0);
+    switch ((rows + 15) / 16) {
+        case 1: return run_tile<TB, MC, S, 1>(a, er, e, m0, rows, n0, s_x);
+        case 2: if (TB >= 32) return run_tile<TB, MC, S, TB >= 32 ? 2 : 1>(a, er, e, m0, rows, n0, s_x); break;
+        case 3: if (TB >= 64) return run_tile<TB, MC, S, TB >= 64 ? 3 : 1>(a, er, e, m0, rows, n0, s_x); break;
+        default: if (TB >= 64) return run_tile<TB, MC, S, TB >= 64 ? 4 : 1>(a, er, e, m0, rows, n0, s_x); break;
+    }
+}
+
+template <int TB, int MC, int S>
+hipError_t launch(const Fp4Args& a, int64_t pairs, hipStream_t stream) {
+    constexpr int kCols = 16 * MC * kWaves / S;
+    const int64_t blocks = max_row_tiles(a.rows, TB, pairs) * ((a.N + kCols - 1) / kCols);
+    if (blocks > 0x7FFFFF) return hipErrorInvalidConfiguration;
+    if (launch_debug())
+        launch_debug_print("k_grouped_gemm_fp4_stream", dim3((unsigned)blocks), dim3(64 * kWaves),
+                           "rows %d split %d n %d k %d", TB, S, a.N, a.K);
+    hipLaunchKernelGGL((k_grouped_gemm_fp4_stream<TB, MC, S>), dim3((unsigned)blocks), dim3(64 * kWaves), 0, stream, a);
+    return hipGetLastError();
+}
+
+// Parts of the reduction: it is split while that leaves about one block a CU (256 of
+// 8 waves), and only where every part keeps a unit. Never by the device's real CU
+// count: the order of the sums must not depend on it.
+int parts(const Fp4Args& a, int64_t pairs) {
+    const int64_t waves = (pairs < a.rows.E ? pairs : a.rows.E) * ((a.N + 15) / 16);
+    int split = waves >= 1536 ? 1 : waves >= 768 ? 2 : waves >= 384 ? 4 : 8;
+    while (split > 1 && a.K < kUnit * split) split /= 2;
+    return split;
+}
+
+}  // namespace
+
+hipError_t launch_grouped_gemm_mxfp4_rows(const Fp4Args& a, int64_t pairs, hipStream_t stream) {
+    if (pairs == 0) return hipSuccess;
+    const int64_t mean = (pairs + a.rows.E - 1) / a.rows.E;
+    if (mean > 20) return launch<64, 2, 1>(a, pairs, stream);
+    const int split = parts(a, pairs);
+    if (mean > 6) {
+        if (split == 1) return launch<32, 2, 1>(a, pairs, stream);
+        if (split == 2) return launch<32, 1, 2>(a, pairs, stream);
+        return launch<32, 1, 4>(a, pairs, stream);
+    }
+    if (split == 1) return launch<16, 1, 1>(a, pairs, stream);
+    if (split == 2) return launch<16, 1, 2>(a, pairs, stream);
+    if (split == 4) return launch<16, 1, 4>(a, pairs, stream);
+    return launch<16, 1, 8>(a, pairs, stream);
+}
+
+}  // namespace ep

@@ -161,6 +161,30 @@ struct StreamArgs {
     int N, K;
 };
 
+// Products with both operands in MXFP4 (ep_gemm_fp4.hip).
+struct Fp4Args {
+    RowsArgs rows;
+    const uint8_t* x;         // codes [rows, K / 2]
+    const uint8_t* x_scales;  // [rows, K / 32]
+    const uint8_t* b;         // codes [E, N, K / 2]
+    const uint8_t* b_scales;  // [E, N, K / 32]
+    uint16_t* out;            // bf16 [rows, N]
+    int N, K;
+};
+
+// Quantisation to MXFP4 (ep_mxfp4.hip).
+struct QuantArgs {
+    RowsArgs rows;           // of the layout, when only its live rows are quantised
+    const int32_t* row_src;
+    const void* x;
+    uint8_t* codes;
+    uint8_t* scales;
+    uint16_t* values;  // or NULL
+    int64_t vectors;     // of 8 values: of a row (live rows), or of all rows
+    int64_t row_pieces;  // pieces that these are cut into
+    int64_t pieces;
+};
+
 // RMS norm (ep_norm.hip) and its backward.
 struct NormArgs {
     const uint16_t* x;
@@ -274,6 +298,8 @@ hipError_t launch_grouped_gemm_fp8(const GemmArgs& a, int64_t rows_bound, hipStr
 hipError_t launch_grouped_gemm_bf16(int dir, const GroupedArgs& a, int64_t pairs, hipStream_t stream);
 hipError_t launch_grouped_gemm_bf16_stream(const StreamArgs& a, int64_t pairs, hipStream_t stream);
 hipError_t launch_grouped_gemm_mxfp4(const StreamArgs& a, int64_t pairs, hipStream_t stream);
+hipError_t launch_grouped_gemm_mxfp4_rows(const Fp4Args& a, int64_t pairs, hipStream_t stream);
+hipError_t launch_quantize_mxfp4(QuantArgs a, int64_t rows, int32_t k, bool live_rows, bool f32, hipStream_t stream);
 hipError_t launch_rms_norm(const NormArgs& a, hipStream_t stream);
 hipError_t launch_rms_norm_backward(const NormBackwardArgs& a, hipStream_t stream);
 hipError_t launch_route(const RouteArgs& a, hipStream_t stream);

@@ -13,6 +13,7 @@
 #include <stdexcept>
 #include <string>
 #include <tuple>
+#include <vector>
 
 #include "../../include/ep.h"
 
@@ -274,6 +275,60 @@ at::Tensor grouped_gemm_mxfp4(int64_t handle, const at::Tensor& a, const at::Ten
     return o;
 }
 
+// x [..., k] of any leading sizes, or the receive rows of a handle (0: none).
+std::tuple<at::Tensor, at::Tensor> quantize_mxfp4(int64_t handle, const at::Tensor& x,
+                                                  const c10::optional<at::Tensor>& codes,
+                                                  const c10::optional<at::Tensor>& scales,
+                                                  const c10::optional<at::Tensor>& values, int64_t stream, int64_t dev) {
+    const ep_handle* h = handle != 0 ? handle_of(handle) : nullptr;
+    const at::ScalarType xt = x.scalar_type();
+    if (xt != at::kFloat && xt != at::kBFloat16)
+        throw std::invalid_argument(std::string("x has dtype ") + std::string(c10::toString(xt)) +
+                                    ", expected Float or BFloat16");
+    if (x.dim() < 1) throw std::invalid_argument("x must be [..., k]");
+    const int64_t k = x.size(-1);
+    if (k < 32 || k % 32 != 0) throw std::invalid_argument("x's last size " + std::to_string(k) + " must be a positive multiple of 32");
+    if (h != nullptr) shape(x, {rows_bound(&h->cfg), k}, "x");
+    const void* px = ptr(x, "x", xt, dev);
+    std::vector<int64_t> cs = x.sizes().vec(), ss = cs;
+    cs.back() = k / 2;
+    ss.back() = k / 32;
+    const auto buffer = [&](const c10::optional<at::Tensor>& t, const std::vector<int64_t>& want, const char* name) {
+        if (!t.has_value()) return at::empty(want, x.options().dtype(at::kByte));
+        if (t->sizes() != at::IntArrayRef(want))
+            throw std::invalid_argument(std::string(name) + " has shape " + c10::str(t->sizes()) + ", expected " +
+                                        c10::str(at::IntArrayRef(want)));
+        return *t;
+    };
+    at::Tensor c = buffer(codes, cs, "codes"), s = buffer(scales, ss, "scales");
+    if (values.has_value() && values->sizes() != x.sizes())
+        throw std::invalid_argument("values has shape " + c10::str(values->sizes()) + ", expected " + c10::str(x.sizes()));
+    ok(ep_quantize_mxfp4(h, x.numel() / k, width(k), xt == at::kFloat ? 1 : 0, px, ptr(c, "codes", at::kByte, dev),
+                         ptr(s, "scales", at::kByte, dev), opt_ptr(values, "values", at::kBFloat16, dev),
+                         stream_of(stream)),
+       "ep_quantize_mxfp4");
+    return {c, s};
+}
+
+at::Tensor grouped_gemm_mxfp4_rows(int64_t handle, const at::Tensor& a, const at::Tensor& a_scales, const at::Tensor& b,
+                                   const at::Tensor& b_scales, const c10::optional<at::Tensor>& out, int64_t stream,
+                                   int64_t dev) {
+    const ep_handle* h = handle_of(handle);
+    const int64_t R = rows_bound(&h->cfg), E = h->cfg.num_experts;
+    experts_first(b, E, "[E, n, k / 2]");
+    const int64_t n = b.size(1), k = 2 * b.size(2);
+    shape(a, {R, k / 2}, "a");
+    shape(a_scales, {R, k / 32}, "a_scales");
+    shape(b_scales, {E, n, k / 32}, "b_scales");
+    const void *pa = ptr(a, "a", at::kByte, dev), *ps = ptr(a_scales, "a_scales", at::kByte, dev);
+    const void *pb = ptr(b, "b", at::kByte, dev), *pt = ptr(b_scales, "b_scales", at::kByte, dev);
+    at::Tensor o = output(out, {R, n}, at::kBFloat16, a, "out");
+    ok(ep_grouped_gemm_mxfp4_rows(h, pa, ps, pb, pt, width(n), width(k), ptr(o, "out", at::kBFloat16, dev),
+                                  stream_of(stream)),
+       "ep_grouped_gemm_mxfp4_rows");
+    return o;
+}
+
 std::tuple<at::Tensor, c10::optional<at::Tensor>, at::Tensor, at::Tensor> rms_norm(
     const at::Tensor& x, const at::Tensor& weight, double eps, const c10::optional<at::Tensor>& residual, int64_t dtype,
     const c10::optional<at::Tensor>& total, const c10::optional<at::Tensor>& y,
@@ -443,6 +498,8 @@ PYBIND11_MODULE(TORCH_EXTENSION_NAME, m) {
     m.def("grouped_gemm_bf16_grad_input", &grouped_gemm_bf16_grad_input);
     m.def("grouped_gemm_bf16_grad_weight", &grouped_gemm_bf16_grad_weight);
     m.def("grouped_gemm_mxfp4", &grouped_gemm_mxfp4);
+    m.def("quantize_mxfp4", &quantize_mxfp4);
+    m.def("grouped_gemm_mxfp4_rows", &grouped_gemm_mxfp4_rows);
     m.def("rms_norm", &rms_norm);
     m.def("rms_norm_backward", &rms_norm_backward);
     m.def("route", &route);

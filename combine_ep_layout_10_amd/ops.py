@@ -406,6 +406,25 @@ def grouped_gemm_mxfp4(h: Handle, a: torch.Tensor, b: torch.Tensor, b_scales: to
     return _B.grouped_gemm_mxfp4(ctypes.addressof(h.c), a, b, b_scales, out, _raw_stream(cur), cur)
 
 
+def quantize_mxfp4(x: torch.Tensor, h: Optional[Handle] = None, codes: Optional[torch.Tensor] = None,
+                   scales: Optional[torch.Tensor] = None, values: Optional[torch.Tensor] = None):
+    """Quantises x [..., k] (bfloat16 or float32, k a multiple of 32) to MXFP4.
+    Returns (codes, scales), uint8 [..., k / 2] and [..., k / 32], the operands
+    of grouped_gemm_mxfp4 and grouped_gemm_mxfp4_rows. With a handle x holds its
+    receive rows, and only rows that hold a pair are read and written. values
+    (bfloat16, x's shape; may be x itself) receives what the codes stand for."""
+    cur = _current_device()
+    return _B.quantize_mxfp4(0 if h is None else ctypes.addressof(h.c), x, codes, scales, values, _raw_stream(cur), cur)
+
+
+def grouped_gemm_mxfp4_rows(h: Handle, a: torch.Tensor, a_scales: torch.Tensor, b: torch.Tensor, b_scales: torch.Tensor,
+                            out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """grouped_gemm_mxfp4 with the rows in MXFP4 as well: a uint8 [rows bound, k / 2]
+    and a_scales uint8 [rows bound, k / 32], as quantize_mxfp4 writes them."""
+    cur = _current_device()
+    return _B.grouped_gemm_mxfp4_rows(ctypes.addressof(h.c), a, a_scales, b, b_scales, out, _raw_stream(cur), cur)
+
+
 # ---------------------------------------------------------------- RMS norm
 
 def rms_norm(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6, residual: Optional[torch.Tensor] = None,

@@ -398,6 +398,42 @@ ep_status ep_grouped_gemm_bf16_grad_weight(const ep_handle* h, const void* grad_
 ep_status ep_grouped_gemm_mxfp4(const ep_handle* h, const void* a, const void* b, const void* b_scales, int32_t n,
                                 int32_t k, void* out, void* stream);
 
+/* Quantises rows to MXFP4 (OCP Microscaling Formats), the operands of
+ * ep_grouped_gemm_mxfp4 and ep_grouped_gemm_mxfp4_rows. For each 32 consecutive
+ * values of a row, with m = max|x|,
+ *   X = max(floor(log2 m) - 2, -127), scale = X + 127 (0 for 32 zeros),
+ *   code = E2M1(x / 2^X), rounded to nearest even, at most 6 in magnitude, the
+ *          sign kept;
+ * a NaN or an infinity among them: scale 255 (NaN) and zero codes.
+ *   h       NULL: all rows. Otherwise x has the receive layout, rows is
+ *           ep_recv_rows_bound(&h->cfg), and only rows that hold a pair are read
+ *           and written.
+ *   k       a multiple of 32, at most 2^20 (EP_ERR_UNSUPPORTED above); rows * k
+ *           at most 2^42.
+ *   x       device [rows, k], bf16, or binary32 when x_f32 is 1.
+ *   codes   device bytes [rows, k / 2]: value j in byte j / 2, even j in the low
+ *           nibble.
+ *   scales  device bytes [rows, k / 32], any alignment.
+ *   values  device bf16 [rows, k]: what the codes stand for, exactly (NaN where the
+ *           scale is), or NULL. The operand of the BF16 products in the backward
+ *           pass of training with 4-bit operands. May be x's own buffer when x is bf16. */
+ep_status ep_quantize_mxfp4(const ep_handle* h, int64_t rows, int32_t k, int32_t x_f32, const void* x, void* codes,
+                            void* scales, void* values, void* stream);
+
+/* ep_grouped_gemm_mxfp4 with the rows in MXFP4 as well, on the matrix unit's 4-bit
+ * form:
+ *   out[r, c] = bf16( sum_j av[r, j] * bv[e, c, j] ),
+ * av and bv the values that codes and scales stand for.
+ *   a         device bytes [rows bound, k / 2], codes as ep_quantize_mxfp4 writes
+ *             them; k is a multiple of 32.
+ *   a_scales  device bytes [rows bound, k / 32], any alignment. 255 is NaN, as in b_scales.
+ *   b, b_scales, out  as ep_grouped_gemm_mxfp4's, and likewise n.
+ * Products are exact, and summed in binary32 by the MFMA (a sum's terms more than
+ * 23 binary places below its largest are cut off), rounded once. Tiles: 128 columns by R = 16 for
+ * P <= 6 E, 256 columns by 32 for P <= 20 E, otherwise 256 columns by 64. */
+ep_status ep_grouped_gemm_mxfp4_rows(const ep_handle* h, const void* a, const void* a_scales, const void* b,
+                                     const void* b_scales, int32_t n, int32_t k, void* out, void* stream);
+
 /* RMS norm with the residual's addition: the norm before the router and the
  * dispatch, whose FP8 output is an EP_FP8_PREQUANT dispatch's input. For every
  * token t < num_tokens and channel c < hidden:
