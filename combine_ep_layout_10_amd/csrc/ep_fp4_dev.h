@@ -24,6 +24,14 @@ __device__ __forceinline__ f32x4_t mfma_fp4(u32x4_t a, u32x4_t b, f32x4_t c, uin
     return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(x, y, c, kFp4, kFp4, T, (int)sa, T, (int)sb);
 }
 
+// Likewise 32 rows of A and of B by 64: lane (g, r), g < 2.
+template <int T>
+__device__ __forceinline__ f32x16_t mfma_fp4_32(u32x4_t a, u32x4_t b, f32x16_t c, uint32_t sa, uint32_t sb) {
+    const i32x8_t x = {(int)a[0], (int)a[1], (int)a[2], (int)a[3], 0, 0, 0, 0};
+    const i32x8_t y = {(int)b[0], (int)b[1], (int)b[2], (int)b[3], 0, 0, 0, 0};
+    return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(x, y, c, kFp4, kFp4, T, (int)sa, T, (int)sb);
+}
+
 // Four of a row's `groups` scales from `first` on, as a word; zeros past the last.
 __device__ __forceinline__ uint32_t load_scales4(const uint8_t* row, int first, int groups) {
     uint32_t w = 0;

@@ -57,7 +57,6 @@ namespace ep {
 namespace {
 
 constexpr int kTile = 256;     // rows of a tile
-constexpr int kGroupRows = 4;  // row tiles that share column tiles in the block order
 
 struct Tile {
     int e;          // expert
@@ -66,20 +65,6 @@ struct Tile {
     int last_rows;  // whether it is the expert's last row tile
     ExpertRows er;
 };
-
-// Tile of logical block `local` among an expert's nt_m x nt_n: groups of
-// kGroupRows row tiles, within a group column by column, so that blocks that run
-// together on an XCD share few operand tiles; a last, shorter row tile comes in a
-// group of its own or with few others, and does not put the long ones out of step.
-// 65,536 rows x 4096 x 7168 on 32 experts: groups of 4, 8, 16 fetch 9.4, 12.0, 14.9
-// GB into L2 (in 3.24, 3.24, 3.28 ms then).
-__device__ __forceinline__ void order_tiles(int local, int nt_m, int nt_n, int* m, int* n) {
-    const int g = local / (kGroupRows * nt_n);
-    const int in_group = min(kGroupRows, nt_m - g * kGroupRows);
-    const int rem = local - g * kGroupRows * nt_n;
-    *n = rem / in_group;
-    *m = g * kGroupRows + rem % in_group;
-}
 
 // This block's tile of kTile rows by COLS columns; false when it has none.
 template <int DIR, int COLS>

@@ -213,6 +213,259 @@ __global__ __launch_bounds__(64 * kWaves) void k_grouped_gemm_fp4_stream(Fp4Args
     }
 }
 
+// ---------------------------------------------------------------- whole tiles: 8 waves, 256 x 256
+
+// Wave (wm, wn) computes the 32-row pieces 2 i + wm of the tile by columns 64 wn ..
+// + 63. The reduction runs in steps of 256: both operands' slices (rows of 128
+// bytes, whole cache lines) move from memory to LDS by DMA, two steps deep; lane (g,
+// r32) of the MFMA reads chunks 4 g + t (16 bytes, 32 codes) of its row for t = 0 .. 3,
+// whose scales are the four bytes of one word. Chunk c of row r is stored at
+// c ^ (r / 2 mod 8), so that a read meets each bank once. Scales move in slabs of two
+// steps, 16 bytes a row, two slabs deep.
+//
+// Schedule: the waves form two groups (wm) half a step apart: while one group's MFMAs
+// run, the other reads its operands from LDS, then a barrier exchanges the roles.
+// Group 0 reads step kb in interval 2 kb, group 1 in the next. The rows' slice is kept
+// in two halves, one for each group's pieces, since a half is free one interval after
+// its own group has read it:
+//   interval 2 kb      sends B of step kb + 1 (all waves),
+//   interval 2 kb + 1  group 0 sends group 1's half of A of step kb + 1, group 1 sends
+//                      group 0's half of A of step kb + 2; every second one the next slab.
+// What is sent has two intervals to land, and 128 KiB hold what would else take 160.
+constexpr int kTile = 256;
+constexpr int kStepBytes = 128;                  // of a row: 256 codes
+constexpr int kHalfA = 128 * kStepBytes;         // bytes of a group's half of a slice of A
+constexpr int kSliceB = kTile * kStepBytes;
+constexpr int kSlabRows = 2 * kTile;             // A's, then B's
+constexpr int kTileLds = 4 * kHalfA + 2 * kSliceB + 2 * kSlabRows * 16;
+constexpr int kStoreLds = 4096;
+
+struct TileLds {
+    uint32_t base;
+    __device__ __forceinline__ uint32_t a(int kb, int half) const { return base + (2 * (kb & 1) + half) * kHalfA; }
+    __device__ __forceinline__ uint32_t b(int kb) const { return base + 4 * kHalfA + (kb & 1) * kSliceB; }
+    __device__ __forceinline__ uint32_t slab(int j) const { return base + 4 * kHalfA + 2 * kSliceB + (j & 1) * kSlabRows * 16; }
+};
+
+// What a wave sends. MI: 32-row pieces of a wave.
+template <int MI>
+struct Sender {
+    const uint8_t *a, *b, *s;        // of the tile, reduction step 0; s: this wave's scales
+    int half, groups;                // bytes of a row's codes and scales
+    int rows, cols, s_rows;          // that exist
+    int steps;
+    uint32_t off_a[MI], off_b[4], off_s;
+    int w;
+    TileLds lds;
+
+    __device__ __forceinline__ void init(const Fp4Args& g, int64_t first_row, int64_t first_col, int n_rows, int n_cols) {
+        const int lane = lane_id(), pos = lane & 7;
+        rows = n_rows;
+        cols = n_cols;
+        a = g.x + first_row * half;
+        b = g.b + first_col * half;
+        // group 0 sends group 1's pieces, and the reverse
+#pragma unroll
+        for (int j = 0; j < MI; ++j) {
+            const int q = (w & 3) * MI + j, in = (q & 3) * 8 + (lane >> 3);  // 8 rows a load
+            off_a[j] = __umul24(32 * (2 * (q >> 2) + (w < 4 ? 1 : 0)) + in, half) + 16 * (pos ^ ((in >> 1) & 7));
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int r = (4 * w + j) * 8 + (lane >> 3);
+            off_b[j] = __umul24(r, half) + 16 * (pos ^ ((r >> 1) & 7));
+        }
+        // scales: waves 0 to 3 those of 64 rows of A each, waves 4 to 7 of B
+        const int r0 = 64 * (w & 3);
+        const bool of_b = w >= 4;
+        s = (of_b ? g.b_scales + first_col * groups : g.x_scales + first_row * groups) + (int64_t)r0 * groups;
+        s_rows = max(0, min(64, (of_b ? cols : rows) - r0));
+        off_s = __umul24(lane, groups);
+    }
+    __device__ __forceinline__ void send_a(int kb, int j) const {
+        dma16(a + (int64_t)kb * kStepBytes, kb < steps ? rows * half - kb * kStepBytes : 0, off_a[j],
+              lds.a(kb, w < 4 ? 1 : 0) + ((w & 3) * MI + j) * 1024);
+    }
+    __device__ __forceinline__ void send_b(int kb, int j) const {
+        dma16(b + (int64_t)kb * kStepBytes, kb < steps ? cols * half - kb * kStepBytes : 0, off_b[j],
+              lds.b(kb) + (4 * w + j) * 1024);
+    }
+    // slab j: steps 2 j and 2 j + 1
+    __device__ __forceinline__ void send_slab(int j) const {
+        dma16(s + (int64_t)j * 16, 2 * j < steps ? max(0, s_rows * groups - j * 16) : 0, off_s, lds.slab(j) + w * 1024);
+    }
+};
+
+__device__ __forceinline__ u32x4_t read_codes(uint32_t at) { return read_lds_words(at); }
+typedef uint32_t __attribute__((address_space(3), may_alias)) lds_u32_t;
+__device__ __forceinline__ uint32_t read_word(uint32_t at) { return *(const lds_u32_t*)at; }
+
+// The loop of one group of waves over all steps.
+template <bool SECOND, int MI>
+__device__ __forceinline__ void multiply(const Sender<MI>& send, f32x16_t (&acc)[MI][2], int wn, int words) {
+    const int lane = lane_id(), r32 = lane & 31, g = lane >> 5;
+    const uint32_t row = r32 * kStepBytes + (((4 * g) ^ ((r32 >> 1) & 7)) << 4);
+    const TileLds lds = send.lds;
+    for (int kb = 0; kb < send.steps; ++kb) {
+        const uint32_t at_a = lds.a(kb, SECOND ? 1 : 0) + row, at_b = lds.b(kb) + wn * 64 * kStepBytes + row;
+        const uint32_t at_s = lds.slab(kb >> 1) + r32 * 16 + (kb & 1) * 8 + g * 4;
+        u32x4_t fa[4][MI], fb[4][2];
+        uint32_t sa[MI], sb[2];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) sb[j] = read_word(at_s + (kTile + 64 * wn + 32 * j) * 16);
+#pragma unroll
+        for (int i = 0; i < MI; ++i) sa[i] = read_word(at_s + (64 * i + (SECOND ? 32 : 0)) * 16);
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+#pragma unroll
+            for (int j = 0; j < 2; ++j) fb[t][j] = read_codes((at_b ^ (t << 4)) + 32 * kStepBytes * j);
+#pragma unroll
+            for (int i = 0; i < MI; ++i) fa[t][i] = read_codes((at_a ^ (t << 4)) + 32 * kStepBytes * i);
+        }
+        const bool slab = !(kb & 1);  // interval 2 kb + 1 sends the next slab
+        if (SECOND) {  // interval 2 kb + 1
+#pragma unroll
+            for (int j = 0; j < MI; ++j) send.send_a(kb + 2, j);
+            if (slab) send.send_slab((kb >> 1) + 1);
+            // B of step kb + 1 has landed, and all before it
+            if (slab) wait_vmcnt<MI + 1>();
+            else wait_vmcnt<MI>();
+        } else {  // interval 2 kb
+#pragma unroll
+            for (int j = 0; j < 4; ++j) send.send_b(kb + 1, j);
+            wait_vmcnt<4>();  // group 1's half of A of step kb has landed
+        }
+        wait_lgkmcnt0();
+        block_barrier();
+        if (2 * kb + g >= words) {  // past the reduction: 2^-127 by 2^-127
+#pragma unroll
+            for (int j = 0; j < 2; ++j) sb[j] = 0u;
+#pragma unroll
+            for (int i = 0; i < MI; ++i) sa[i] = 0u;
+        }
+        __builtin_amdgcn_s_setprio(1);
+        // operands swapped: each 32 x 32 piece comes out transposed, lane (g, r32) holding
+        // row r32 and columns 8 q + 4 g .. + 3 for q < 4
+        const auto part = [&](auto tt) {
+            constexpr int t = decltype(tt)::value;
+#pragma unroll
+            for (int i = 0; i < MI; ++i) {
+                if (SECOND) {  // interval 2 kb + 2
+                    if (i == 0) send.send_b(kb + 2, t);
+                } else {  // interval 2 kb + 1
+                    if (i == MI - 1 && t < MI) send.send_a(kb + 1, t);
+                    if (i == MI - 1 && t == 3 && slab) send.send_slab((kb >> 1) + 1);
+                }
+#pragma unroll
+                for (int j = 0; j < 2; ++j) acc[i][j] = mfma_fp4_32<t>(fb[t][j], fa[t][i], acc[i][j], sb[j], sa[i]);
+                __builtin_amdgcn_sched_barrier(0);
+            }
+        };
+        part(std::integral_constant<int, 0>());
+        part(std::integral_constant<int, 1>());
+        part(std::integral_constant<int, 2>());
+        part(std::integral_constant<int, 3>());
+        __builtin_amdgcn_s_setprio(0);
+        if (!SECOND) {
+            if (slab) wait_vmcnt<MI + 1>();
+            else wait_vmcnt<MI>();
+        }
+        block_barrier();
+    }
+}
+
+// Rows of the tile: MI 32-row pieces for each group.
+template <int MI>
+__device__ __forceinline__ void run_whole(const Fp4Args& a, const ExpertRows& er, int e, int m0, int rows, int n0,
+                                          bool last, uint32_t lds) {
+    const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), wm = w >> 2, wn = w & 3;
+    const int64_t first_row = (int64_t)er.first + m0;
+    Sender<MI> send;
+    send.half = a.K / 2;
+    send.groups = a.K / 32;
+    send.steps = (a.K + 255) / 256;
+    send.w = w;
+    send.lds.base = lds;
+    send.init(a, first_row, (int64_t)e * a.N + n0, rows, min(kTile, a.N - n0));
+    f32x16_t acc[MI][2];
+#pragma unroll
+    for (int i = 0; i < MI; ++i)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) acc[i][j] = (f32x16_t)0.0f;
+    // ahead of interval 0: slab 0, B and group 0's half of A of step 0 (by group 1), then group
+    // 1's half (by group 0) and group 0's half of step 1 (by group 1)
+    send.send_slab(0);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) send.send_b(0, j);
+#pragma unroll
+    for (int j = 0; j < MI; ++j) send.send_a(0, j);
+    if (wm == 1) {
+#pragma unroll
+        for (int j = 0; j < MI; ++j) send.send_a(1, j);
+    }
+    wait_vmcnt<MI>();
+    block_barrier();
+    const int words = a.K / 128;
+    if (wm == 0) {
+        multiply<false, MI>(send, acc, wn, words);
+        block_barrier();
+    } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) send.send_b(1, j);
+        block_barrier();  // half a step later
+        multiply<true, MI>(send, acc, wn, words);
+    }
+    wait_vmcnt<0>();
+    block_barrier();  // no wave reads or fills the ring any more
+
+    // stores: each 32 rows are turned through the wave's own LDS, so that neighbouring
+    // lanes store neighbouring columns; 16-byte chunks XORed with half the row
+    const int lane = lane_id(), r32 = lane & 31, g = lane >> 5;
+    const uint32_t at = lds + w * kStoreLds;
+#pragma unroll
+    for (int i = 0; i < MI; ++i) {
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const u32x2_t v = {pack_bf16x2(acc[i][j][4 * q], acc[i][j][4 * q + 1]),
+                                   pack_bf16x2(acc[i][j][4 * q + 2], acc[i][j][4 * q + 3])};
+                write_lds(at + r32 * 128 + (((4 * j + q) ^ ((r32 >> 1) & 7)) << 4) + g * 8, v);
+            }
+        const int row = 32 * (2 * i + wm), col = n0 + 64 * wn + 8 * (lane & 7);
+#pragma unroll
+        for (int s = 0; s < 4; ++s) {
+            const int r = 8 * s + (lane >> 3);
+            const u32x4_t v = read_lds_words(at + r * 128 + (((lane & 7) ^ ((r >> 1) & 7)) << 4));
+            if (row + r < rows && col < a.N) *(u32x4_t*)(a.out + (first_row + row + r) * a.N + col) = v;
+        }
+    }
+    if (a.rows.zero_pad && last) clear_padding<kTile>(a.out, a.N, er, n0);
+}
+
+__global__ __launch_bounds__(512) void k_grouped_gemm_fp4(Fp4Args a) {
+    __shared__ __attribute__((aligned(1024))) uint8_t s_ring[kTileLds];
+    const int nt_n = (a.N + kTile - 1) / kTile;
+    int e, local, m, n;
+    if (!find_expert(a.rows, kTile, nt_n, &e, &local)) return;
+    e = __builtin_amdgcn_readfirstlane(e);
+    const ExpertRows er = expert_rows(a.rows, e);
+    const int nt_m = (er.live + kTile - 1) / kTile;
+    order_tiles(local, nt_m, nt_n, &m, &n);
+    const int each = ((er.live + nt_m - 1) / nt_m + 63) & ~63;  // rows of a tile; never leaves the last one empty
+    const int m0 = __builtin_amdgcn_readfirstlane(m * each), n0 = __builtin_amdgcn_readfirstlane(n * kTile);
+    const int rows = __builtin_amdgcn_readfirstlane(min(each, er.live - m0));
+    const bool last = m == nt_m - 1;
+    const uint32_t lds = lds_offset(s_ring);
+    asm volatile("" ::"v"(s_ring) : "memory");  // the ring is written by the DMA alone
+    switch ((rows + 63) / 64) {
+        case 1: return run_whole<1>(a, er, e, m0, rows, n0, last, lds);
+        case 2: return run_whole<2>(a, er, e, m0, rows, n0, last, lds);
+        case 3: return run_whole<3>(a, er, e, m0, rows, n0, last, lds);
+        default: return run_whole<4>(a, er, e, m0, rows, n0, last, lds);
+    }
+}
+
 template <int TB, int MC, int S>
 hipError_t launch(const Fp4Args& a, int64_t pairs, hipStream_t stream) {
     constexpr int kCols = 16 * MC * kWaves / S;
@@ -240,7 +493,19 @@ int parts(const Fp4Args& a, int64_t pairs) {
 hipError_t launch_grouped_gemm_mxfp4_rows(const Fp4Args& a, int64_t pairs, hipStream_t stream) {
     if (pairs == 0) return hipSuccess;
     const int64_t mean = (pairs + a.rows.E - 1) / a.rows.E;
-    if (mean > 20) return launch<64, 2, 1>(a, pairs, stream);
+    if (mean > 20) {
+        // Whole tiles take their scales by DMA, which needs rows of whole words
+        const bool words = a.K % 128 == 0 && ((uintptr_t)a.x_scales | (uintptr_t)a.b_scales) % 4 == 0;
+        if (words && mean > 64) {
+            const int64_t blocks = max_row_tiles(a.rows, kTile, pairs) * ((a.N + kTile - 1) / kTile);
+            if (blocks > 0x7FFFFF) return hipErrorInvalidConfiguration;
+            if (launch_debug())
+                launch_debug_print("k_grouped_gemm_fp4", dim3((unsigned)blocks), dim3(512), "n %d k %d", a.N, a.K);
+            hipLaunchKernelGGL(k_grouped_gemm_fp4, dim3((unsigned)blocks), dim3(512), 0, stream, a);
+            return hipGetLastError();
+        }
+        return launch<64, 2, 1>(a, pairs, stream);
+    }
     const int split = parts(a, pairs);
     if (mean > 6) {
         if (split == 1) return launch<32, 2, 1>(a, pairs, stream);

@@ -86,3 +86,26 @@ def test_reference_on_known_values():
     assert ref.quantize(np.full((1, 32), 8.0))[1][0, 0] == 128
     assert ref.quantize(np.zeros((1, 32)))[1][0, 0] == 0
     assert np.array_equal(ref.decode(codes, scales), values)
+
+
+def test_dma_loads_bring_their_wait_states(tmp_path):
+    """The LDS DMA loads are inline assembly, into which the compiler's hazard pass
+    does not look: they bring the five wait states behind a scalar's write themselves."""
+    import os
+    import re
+    import subprocess
+
+    from combine_ep_layout_10_amd import build as B
+    if not os.path.exists(B.HIPCC):
+        pytest.skip("hipcc not installed")
+    out = tmp_path / "fp4.s"
+    flags = [f for f in B.FLAGS if f not in ("-shared", "-fPIC")]
+    subprocess.run([B.HIPCC] + flags + ["--cuda-device-only", "-S", "-o", str(out),
+                                        os.path.join(B.CSRC, "ep_gemm_fp4.hip")], check=True, capture_output=True)
+    lines = [l.split(";")[0].strip() for l in out.read_text().splitlines()]
+    lines = [l for l in lines if l and not l.startswith(".")]
+    loads = [i for i, l in enumerate(lines) if l.startswith("buffer_load_dwordx4") and l.endswith(" lds")]
+    assert len(loads) > 50
+    for i in loads:
+        m = re.fullmatch(r"s_nop (\d+)", lines[i - 1])
+        assert m and int(m.group(1)) >= 4, lines[i - 3:i + 1]
