@@ -344,11 +344,11 @@ ep_status check_sequences(const int32_t* seq_off, int32_t num_seqs) {
 
 // Workspace of a balance loss: the pieces' partial results, the sequences' terms.
 struct BalanceMap {
-    size_t sums, pairs, tokens, unit, term, total;
+    size_t sums, pairs, tokens, term, routed, done, total;
 };
 
 BalanceMap balance_map(int E, int32_t num_tokens, int32_t num_seqs) {
-    const size_t places = (size_t)(num_tokens + ep::kBalanceTile - 1) / ep::kBalanceTile + num_seqs;
+    const size_t tile = ep::balance_tile(num_tokens), places = (num_tokens + tile - 1) / tile + num_seqs;
     BalanceMap m;
     size_t o = 0;
     auto take = [&](size_t bytes) {
@@ -359,8 +359,9 @@ BalanceMap balance_map(int E, int32_t num_tokens, int32_t num_seqs) {
     m.sums = take(4 * places * E);
     m.pairs = take(4 * places * E);
     m.tokens = take(4 * places);
-    m.unit = take(8 * (size_t)num_seqs);
-    m.term = take(8 * (size_t)num_seqs);
+    m.term = take(8 * (size_t)num_seqs * ((E + 63) / 64));
+    m.routed = take(8 * (size_t)num_seqs);
+    m.done = take(4);
     m.total = o;
     return m;
 }
@@ -980,8 +981,9 @@ ep_status ep_balance_loss(const ep_router* r, int32_t num_tokens, const void* lo
     a.sums = (float*)(ws + m.sums);
     a.pairs = (int32_t*)(ws + m.pairs);
     a.tokens = (int32_t*)(ws + m.tokens);
-    a.unit = (double*)(ws + m.unit);
     a.term = (double*)(ws + m.term);
+    a.routed = (double*)(ws + m.routed);
+    a.done = (int32_t*)(ws + m.done);
     a.T = num_tokens;
     a.E = r->num_experts;
     a.k = r->num_topk;
@@ -989,6 +991,8 @@ ep_status ep_balance_loss(const ep_router* r, int32_t num_tokens, const void* lo
     a.score = r->score;
     a.idx_bits = r->idx_bits;
     a.f32 = r->logits_f32;
+    a.tile = ep::balance_tile(num_tokens);
+    a.chunks = (r->num_experts + 63) / 64;
     hipError_t e = ep::launch_balance_loss(a, (hipStream_t)stream);
     if (e != hipSuccess) return hip_fail(e, "balance loss launch");
     return EP_OK;

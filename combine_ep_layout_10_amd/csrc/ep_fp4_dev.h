@@ -7,29 +7,20 @@
 namespace ep {
 
 typedef int i32x8_t __attribute__((ext_vector_type(8)));
-typedef float f32x16_t __attribute__((ext_vector_type(16)));
 
 constexpr int kFp4 = 4;  // the matrix instructions' number for E2M1
 
 // D = A B + C with both operands' scales applied by the matrix unit: 16 rows of A
 // and of B by 128 of the reduction. Lane (g, r) holds 32 consecutive codes of row r,
-// and their scale in byte T of its scale word; which 32 of the reduction group g
+// and their scale in byte TA (B: TB) of its scale word; which 32 of the reduction group g
 // holds is free as long as both operands agree. Checked on MI355X: products of codes and
 // scales are exact, and what is more than 23 binary places below a sum's largest
 // term is cut off (the tolerance of binary32); scale 255 makes NaN, also of zero codes.
-template <int T>
+template <int TA, int TB>
 __device__ __forceinline__ f32x4_t mfma_fp4(u32x4_t a, u32x4_t b, f32x4_t c, uint32_t sa, uint32_t sb) {
     const i32x8_t x = {(int)a[0], (int)a[1], (int)a[2], (int)a[3], 0, 0, 0, 0};
     const i32x8_t y = {(int)b[0], (int)b[1], (int)b[2], (int)b[3], 0, 0, 0, 0};
-    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(x, y, c, kFp4, kFp4, T, (int)sa, T, (int)sb);
-}
-
-// Likewise 32 rows of A and of B by 64: lane (g, r), g < 2.
-template <int T>
-__device__ __forceinline__ f32x16_t mfma_fp4_32(u32x4_t a, u32x4_t b, f32x16_t c, uint32_t sa, uint32_t sb) {
-    const i32x8_t x = {(int)a[0], (int)a[1], (int)a[2], (int)a[3], 0, 0, 0, 0};
-    const i32x8_t y = {(int)b[0], (int)b[1], (int)b[2], (int)b[3], 0, 0, 0, 0};
-    return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(x, y, c, kFp4, kFp4, T, (int)sa, T, (int)sb);
+    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(x, y, c, kFp4, kFp4, TA, (int)sa, TB, (int)sb);
 }
 
 // Four of a row's `groups` scales from `first` on, as a word; zeros past the last.

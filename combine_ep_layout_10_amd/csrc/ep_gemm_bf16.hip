@@ -57,6 +57,7 @@ namespace ep {
 namespace {
 
 constexpr int kTile = 256;     // rows of a tile
+constexpr int kGroupRows = 4;  // row tiles that share column tiles in the block order
 
 struct Tile {
     int e;          // expert
@@ -75,7 +76,7 @@ __device__ __forceinline__ bool find_tile(const GroupedArgs& a, Tile* t) {
         const int nt_m = (a.M + kTile - 1) / kTile;
         const int L = logical_block((int)gridDim.x);
         t->e = __builtin_amdgcn_readfirstlane(L / (nt_m * nt_n));
-        order_tiles(L % (nt_m * nt_n), nt_m, nt_n, &m, &n);
+        order_tiles<kGroupRows>(L % (nt_m * nt_n), nt_m, nt_n, &m, &n);
         t->er = expert_rows(a.rows, t->e);
         t->m0 = m * kTile;
         t->rows = min(kTile, a.M - t->m0);
@@ -85,7 +86,7 @@ __device__ __forceinline__ bool find_tile(const GroupedArgs& a, Tile* t) {
         if (!find_expert(a.rows, kTile, nt_n, &t->e, &local)) return false;
         t->er = expert_rows(a.rows, t->e);
         const int live = t->er.live, nt_m = (live + kTile - 1) / kTile;
-        order_tiles(local, nt_m, nt_n, &m, &n);
+        order_tiles<kGroupRows>(local, nt_m, nt_n, &m, &n);
         const int each = ((live + nt_m - 1) / nt_m + 31) & ~31;  // rows of a tile; never leaves the last one empty
         t->m0 = m * each;
         t->rows = min(each, live - t->m0);

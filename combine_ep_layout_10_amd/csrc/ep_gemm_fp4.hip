@@ -142,7 +142,7 @@ __device__ __forceinline__ void run_tile(const Fp4Args& a, const ExpertRows& er,
                                                         ((16 * u + ((4 * g + t) ^ row_slot(r16))) << 4));
 #pragma unroll
                     for (int c = 0; c < MC; ++c)
-                        acc[n][c] = mfma_fp4<t>(code[p][c][t], v, acc[n][c], scale[p][c], row_scale[n]);
+                        acc[n][c] = mfma_fp4<t, t>(code[p][c][t], v, acc[n][c], scale[p][c], row_scale[n]);
                 }
             };
             part(std::integral_constant<int, 0>());
@@ -216,12 +216,12 @@ __global__ __launch_bounds__(64 * kWaves) void k_grouped_gemm_fp4_stream(Fp4Args
 // ---------------------------------------------------------------- whole tiles: 8 waves, 256 x 256
 
 // Wave (wm, wn) computes the 32-row pieces 2 i + wm of the tile by columns 64 wn ..
-// + 63. The reduction runs in steps of 256: both operands' slices (rows of 128
-// bytes, whole cache lines) move from memory to LDS by DMA, two steps deep; lane (g,
-// r32) of the MFMA reads chunks 4 g + t (16 bytes, 32 codes) of its row for t = 0 .. 3,
-// whose scales are the four bytes of one word. Chunk c of row r is stored at
-// c ^ (r / 2 mod 8), so that a read meets each bank once. Scales move in slabs of two
-// steps, 16 bytes a row, two slabs deep.
+// + 63, with v_mfma_scale_f32_16x16x128. The reduction runs in steps of 256: both
+// operands' slices (rows of 128 bytes, whole cache lines) move from memory to LDS by
+// DMA, two steps deep. Lane (g, r16) of the MFMA reads chunks f(g) and f(g) + 1 (16
+// bytes, 32 codes) of its row, f = 0, 6, 2, 4, whose scales are two neighbouring bytes.
+// Chunk c of row r is stored at c ^ (r / 2 mod 8): with these f a read meets each bank
+// once. Scales move in slabs of four steps, 32 bytes a row, two slabs deep.
 //
 // Schedule: the waves form two groups (wm) half a step apart: while one group's MFMAs
 // run, the other reads its operands from LDS, then a barrier exchanges the roles.
@@ -229,22 +229,24 @@ __global__ __launch_bounds__(64 * kWaves) void k_grouped_gemm_fp4_stream(Fp4Args
 // in two halves, one for each group's pieces, since a half is free one interval after
 // its own group has read it:
 //   interval 2 kb      sends B of step kb + 1 (all waves),
-//   interval 2 kb + 1  group 0 sends group 1's half of A of step kb + 1, group 1 sends
-//                      group 0's half of A of step kb + 2; every second one the next slab.
+//   interval 2 kb + 1  group 1 sends its own half of A of step kb + 1, group 0 its own half
+//                      of A of step kb + 2; every fourth one the next slab.
 // What is sent has two intervals to land, and 128 KiB hold what would else take 160.
 constexpr int kTile = 256;
 constexpr int kStepBytes = 128;                  // of a row: 256 codes
 constexpr int kHalfA = 128 * kStepBytes;         // bytes of a group's half of a slice of A
 constexpr int kSliceB = kTile * kStepBytes;
 constexpr int kSlabRows = 2 * kTile;             // A's, then B's
-constexpr int kTileLds = 4 * kHalfA + 2 * kSliceB + 2 * kSlabRows * 16;
+constexpr int kSlabSteps = 4, kSlabRow = 8 * kSlabSteps;  // steps of a slab of scales, its bytes a row
+constexpr int kSlab = kSlabRows * kSlabRow;
+constexpr int kTileLds = 4 * kHalfA + 2 * kSliceB + 2 * kSlab;  // all of the CU's 160 KiB
 constexpr int kStoreLds = 4096;
 
 struct TileLds {
     uint32_t base;
     __device__ __forceinline__ uint32_t a(int kb, int half) const { return base + (2 * (kb & 1) + half) * kHalfA; }
     __device__ __forceinline__ uint32_t b(int kb) const { return base + 4 * kHalfA + (kb & 1) * kSliceB; }
-    __device__ __forceinline__ uint32_t slab(int j) const { return base + 4 * kHalfA + 2 * kSliceB + (j & 1) * kSlabRows * 16; }
+    __device__ __forceinline__ uint32_t slab(int j) const { return base + 4 * kHalfA + 2 * kSliceB + (j & 1) * kSlab; }
 };
 
 // What a wave sends. MI: 32-row pieces of a wave.
@@ -264,11 +266,11 @@ struct Sender {
         cols = n_cols;
         a = g.x + first_row * half;
         b = g.b + first_col * half;
-        // group 0 sends group 1's pieces, and the reverse
+        // a group sends its own pieces
 #pragma unroll
         for (int j = 0; j < MI; ++j) {
             const int q = (w & 3) * MI + j, in = (q & 3) * 8 + (lane >> 3);  // 8 rows a load
-            off_a[j] = __umul24(32 * (2 * (q >> 2) + (w < 4 ? 1 : 0)) + in, half) + 16 * (pos ^ ((in >> 1) & 7));
+            off_a[j] = __umul24(32 * (2 * (q >> 2) + (w >> 2)) + in, half) + 16 * (pos ^ ((in >> 1) & 7));
         }
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
@@ -280,94 +282,114 @@ struct Sender {
         const bool of_b = w >= 4;
         s = (of_b ? g.b_scales + first_col * groups : g.x_scales + first_row * groups) + (int64_t)r0 * groups;
         s_rows = max(0, min(64, (of_b ? cols : rows) - r0));
-        off_s = __umul24(lane, groups);
+        off_s = __umul24(lane >> 1, groups) + 16 * (lane & 1);
     }
     __device__ __forceinline__ void send_a(int kb, int j) const {
         dma16(a + (int64_t)kb * kStepBytes, kb < steps ? rows * half - kb * kStepBytes : 0, off_a[j],
-              lds.a(kb, w < 4 ? 1 : 0) + ((w & 3) * MI + j) * 1024);
+              lds.a(kb, w >> 2) + ((w & 3) * MI + j) * 1024);
     }
     __device__ __forceinline__ void send_b(int kb, int j) const {
         dma16(b + (int64_t)kb * kStepBytes, kb < steps ? cols * half - kb * kStepBytes : 0, off_b[j],
               lds.b(kb) + (4 * w + j) * 1024);
     }
-    // slab j: steps 2 j and 2 j + 1
+    // slab j: steps 4 j .. 4 j + 3; a load takes 32 rows
     __device__ __forceinline__ void send_slab(int j) const {
-        dma16(s + (int64_t)j * 16, 2 * j < steps ? max(0, s_rows * groups - j * 16) : 0, off_s, lds.slab(j) + w * 1024);
+        const int size = kSlabSteps * j < steps ? max(0, s_rows * groups - j * kSlabRow) : 0;
+#pragma unroll
+        for (int d = 0; d < 2; ++d)
+            dma16(s + (int64_t)j * kSlabRow, size, off_s + 32 * d * groups, lds.slab(j) + (2 * w + d) * 1024);
     }
 };
 
 __device__ __forceinline__ u32x4_t read_codes(uint32_t at) { return read_lds_words(at); }
-typedef uint32_t __attribute__((address_space(3), may_alias)) lds_u32_t;
-__device__ __forceinline__ uint32_t read_word(uint32_t at) { return *(const lds_u32_t*)at; }
+// The pairs of scales of rows 0 and 16 on from `at`, in a word.
+typedef uint16_t __attribute__((address_space(3), may_alias)) lds_u16_t;
+__device__ __forceinline__ uint32_t read_scales(uint32_t at) {
+    typedef uint16_t u16x2_t __attribute__((ext_vector_type(2)));
+    const u16x2_t v = {*(const lds_u16_t*)at, *(const lds_u16_t*)(at + 16 * kSlabRow)};
+    return __builtin_bit_cast(uint32_t, v);
+}
 
 // The loop of one group of waves over all steps.
 template <bool SECOND, int MI>
-__device__ __forceinline__ void multiply(const Sender<MI>& send, f32x16_t (&acc)[MI][2], int wn, int words) {
-    const int lane = lane_id(), r32 = lane & 31, g = lane >> 5;
-    const uint32_t row = r32 * kStepBytes + (((4 * g) ^ ((r32 >> 1) & 7)) << 4);
+__device__ __forceinline__ void multiply(const Sender<MI>& send, f32x4_t (&acc)[2 * MI][4], int wn, int groups) {
+    const int lane = lane_id(), r16 = lane & 15, g = lane >> 4;
+    const int first = g == 0 ? 0 : g == 1 ? 6 : g == 2 ? 2 : 4;  // chunk of half 0
+    const uint32_t row = r16 * kStepBytes + ((first ^ ((r16 >> 1) & 7)) << 4);
     const TileLds lds = send.lds;
     for (int kb = 0; kb < send.steps; ++kb) {
         const uint32_t at_a = lds.a(kb, SECOND ? 1 : 0) + row, at_b = lds.b(kb) + wn * 64 * kStepBytes + row;
-        const uint32_t at_s = lds.slab(kb >> 1) + r32 * 16 + (kb & 1) * 8 + g * 4;
-        u32x4_t fa[4][MI], fb[4][2];
-        uint32_t sa[MI], sb[2];
+        const uint32_t at_s = lds.slab(kb / kSlabSteps) + r16 * kSlabRow + kb % kSlabSteps * 8 + first;
+        u32x4_t fa[2][2 * MI], fb[2][4];
+        uint32_t sa[MI], sb[2];  // two pieces' pairs of scales a word
 #pragma unroll
-        for (int j = 0; j < 2; ++j) sb[j] = read_word(at_s + (kTile + 64 * wn + 32 * j) * 16);
+        for (int j = 0; j < 2; ++j) sb[j] = read_scales(at_s + (kTile + 64 * wn + 32 * j) * kSlabRow);
 #pragma unroll
-        for (int i = 0; i < MI; ++i) sa[i] = read_word(at_s + (64 * i + (SECOND ? 32 : 0)) * 16);
+        for (int i = 0; i < MI; ++i) sa[i] = read_scales(at_s + (64 * i + (SECOND ? 32 : 0)) * kSlabRow);
 #pragma unroll
-        for (int t = 0; t < 4; ++t) {
+        for (int h = 0; h < 2; ++h) {
 #pragma unroll
-            for (int j = 0; j < 2; ++j) fb[t][j] = read_codes((at_b ^ (t << 4)) + 32 * kStepBytes * j);
+            for (int j = 0; j < 4; ++j) fb[h][j] = read_codes((at_b ^ (h << 4)) + 16 * kStepBytes * j);
 #pragma unroll
-            for (int i = 0; i < MI; ++i) fa[t][i] = read_codes((at_a ^ (t << 4)) + 32 * kStepBytes * i);
+            for (int i = 0; i < 2 * MI; ++i) fa[h][i] = read_codes((at_a ^ (h << 4)) + 16 * kStepBytes * i);
         }
-        const bool slab = !(kb & 1);  // interval 2 kb + 1 sends the next slab
+        const bool slab = kb % kSlabSteps == 0;  // interval 2 kb + 1 sends the next slab
         if (SECOND) {  // interval 2 kb + 1
 #pragma unroll
-            for (int j = 0; j < MI; ++j) send.send_a(kb + 2, j);
-            if (slab) send.send_slab((kb >> 1) + 1);
+            for (int j = 0; j < MI; ++j) send.send_a(kb + 1, j);
+            if (slab) send.send_slab(kb / kSlabSteps + 1);
             // B of step kb + 1 has landed, and all before it
-            if (slab) wait_vmcnt<MI + 1>();
+            if (slab) wait_vmcnt<MI + 2>();
             else wait_vmcnt<MI>();
         } else {  // interval 2 kb
 #pragma unroll
             for (int j = 0; j < 4; ++j) send.send_b(kb + 1, j);
-            wait_vmcnt<4>();  // group 1's half of A of step kb has landed
         }
         wait_lgkmcnt0();
         block_barrier();
-        if (2 * kb + g >= words) {  // past the reduction: 2^-127 by 2^-127
+        if (8 * kb + first >= groups) {  // past the reduction: 2^-127 by 2^-127
 #pragma unroll
             for (int j = 0; j < 2; ++j) sb[j] = 0u;
 #pragma unroll
             for (int i = 0; i < MI; ++i) sa[i] = 0u;
         }
         __builtin_amdgcn_s_setprio(1);
-        // operands swapped: each 32 x 32 piece comes out transposed, lane (g, r32) holding
-        // row r32 and columns 8 q + 4 g .. + 3 for q < 4
-        const auto part = [&](auto tt) {
-            constexpr int t = decltype(tt)::value;
+        // operands swapped: each 16 x 16 piece comes out transposed, lane (g, r16) holding
+        // row r16 and columns 4 g .. 4 g + 3
+        const auto part = [&](auto hh) {
+            constexpr int h = decltype(hh)::value;
 #pragma unroll
             for (int i = 0; i < MI; ++i) {
                 if (SECOND) {  // interval 2 kb + 2
-                    if (i == 0) send.send_b(kb + 2, t);
+#pragma unroll
+                    for (int d = 0; d < 4; ++d)
+                        if (d * 2 * MI / 4 == h * MI + i) send.send_b(kb + 2, d);
                 } else {  // interval 2 kb + 1
-                    if (i == MI - 1 && t < MI) send.send_a(kb + 1, t);
-                    if (i == MI - 1 && t == 3 && slab) send.send_slab((kb >> 1) + 1);
+#pragma unroll
+                    for (int d = 0; d < MI; ++d)
+                        if (d * 2 == h * MI + i) send.send_a(kb + 2, d);
+                    if (i == MI - 1 && h == 1 && slab) send.send_slab(kb / kSlabSteps + 1);
                 }
 #pragma unroll
-                for (int j = 0; j < 2; ++j) acc[i][j] = mfma_fp4_32<t>(fb[t][j], fa[t][i], acc[i][j], sb[j], sa[i]);
+                for (int j = 0; j < 2; ++j) {
+                    acc[2 * i][2 * j] = mfma_fp4<h, h>(fb[h][2 * j], fa[h][2 * i], acc[2 * i][2 * j], sb[j], sa[i]);
+                    acc[2 * i][2 * j + 1] = mfma_fp4<2 + h, h>(fb[h][2 * j + 1], fa[h][2 * i], acc[2 * i][2 * j + 1], sb[j], sa[i]);
+                }
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    acc[2 * i + 1][2 * j] = mfma_fp4<h, 2 + h>(fb[h][2 * j], fa[h][2 * i + 1], acc[2 * i + 1][2 * j], sb[j], sa[i]);
+                    acc[2 * i + 1][2 * j + 1] = mfma_fp4<2 + h, 2 + h>(fb[h][2 * j + 1], fa[h][2 * i + 1], acc[2 * i + 1][2 * j + 1], sb[j], sa[i]);
+                }
                 __builtin_amdgcn_sched_barrier(0);
             }
         };
         part(std::integral_constant<int, 0>());
         part(std::integral_constant<int, 1>());
-        part(std::integral_constant<int, 2>());
-        part(std::integral_constant<int, 3>());
         __builtin_amdgcn_s_setprio(0);
-        if (!SECOND) {
-            if (slab) wait_vmcnt<MI + 1>();
+        if (SECOND) {  // this group's half of A of step kb + 1 has landed
+            wait_vmcnt<4>();
+        } else {  // B of step kb + 1 has landed, and all before it
+            if (slab) wait_vmcnt<MI + 2>();
             else wait_vmcnt<MI>();
         }
         block_barrier();
@@ -387,56 +409,53 @@ __device__ __forceinline__ void run_whole(const Fp4Args& a, const ExpertRows& er
     send.w = w;
     send.lds.base = lds;
     send.init(a, first_row, (int64_t)e * a.N + n0, rows, min(kTile, a.N - n0));
-    f32x16_t acc[MI][2];
+    f32x4_t acc[2 * MI][4];
 #pragma unroll
-    for (int i = 0; i < MI; ++i)
+    for (int i = 0; i < 2 * MI; ++i)
 #pragma unroll
-        for (int j = 0; j < 2; ++j) acc[i][j] = (f32x16_t)0.0f;
-    // ahead of interval 0: slab 0, B and group 0's half of A of step 0 (by group 1), then group
-    // 1's half (by group 0) and group 0's half of step 1 (by group 1)
+        for (int j = 0; j < 4; ++j) acc[i][j] = (f32x4_t){0.0f, 0.0f, 0.0f, 0.0f};
+    // ahead of interval 0: slab 0, B and A of step 0, group 0's half of A of step 1
     send.send_slab(0);
 #pragma unroll
     for (int j = 0; j < 4; ++j) send.send_b(0, j);
 #pragma unroll
     for (int j = 0; j < MI; ++j) send.send_a(0, j);
-    if (wm == 1) {
+    if (wm == 0) {
 #pragma unroll
         for (int j = 0; j < MI; ++j) send.send_a(1, j);
     }
-    wait_vmcnt<MI>();
+    wait_vmcnt<MI>();  // group 1's half may still be on its way
     block_barrier();
-    const int words = a.K / 128;
+    const int groups = a.K / 32;
     if (wm == 0) {
-        multiply<false, MI>(send, acc, wn, words);
+        multiply<false, MI>(send, acc, wn, groups);
         block_barrier();
     } else {
 #pragma unroll
         for (int j = 0; j < 4; ++j) send.send_b(1, j);
+        wait_vmcnt<4>();
         block_barrier();  // half a step later
-        multiply<true, MI>(send, acc, wn, words);
+        multiply<true, MI>(send, acc, wn, groups);
     }
     wait_vmcnt<0>();
     block_barrier();  // no wave reads or fills the ring any more
 
-    // stores: each 32 rows are turned through the wave's own LDS, so that neighbouring
+    // stores: each 16 rows are turned through the wave's own LDS, so that neighbouring
     // lanes store neighbouring columns; 16-byte chunks XORed with half the row
-    const int lane = lane_id(), r32 = lane & 31, g = lane >> 5;
+    const int lane = lane_id(), r16 = lane & 15, g = lane >> 4;
     const uint32_t at = lds + w * kStoreLds;
 #pragma unroll
-    for (int i = 0; i < MI; ++i) {
+    for (int i = 0; i < 2 * MI; ++i) {
 #pragma unroll
-        for (int j = 0; j < 2; ++j)
+        for (int j = 0; j < 4; ++j) {
+            const u32x2_t v = {pack_bf16x2(acc[i][j][0], acc[i][j][1]), pack_bf16x2(acc[i][j][2], acc[i][j][3])};
+            write_lds(at + r16 * 128 + (((2 * j + (g >> 1)) ^ (r16 >> 1)) << 4) + (g & 1) * 8, v);
+        }
+        const int row = 32 * (i & ~1) + 32 * wm + 16 * (i & 1), col = n0 + 64 * wn + 8 * (lane & 7);
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                const u32x2_t v = {pack_bf16x2(acc[i][j][4 * q], acc[i][j][4 * q + 1]),
-                                   pack_bf16x2(acc[i][j][4 * q + 2], acc[i][j][4 * q + 3])};
-                write_lds(at + r32 * 128 + (((4 * j + q) ^ ((r32 >> 1) & 7)) << 4) + g * 8, v);
-            }
-        const int row = 32 * (2 * i + wm), col = n0 + 64 * wn + 8 * (lane & 7);
-#pragma unroll
-        for (int s = 0; s < 4; ++s) {
+        for (int s = 0; s < 2; ++s) {
             const int r = 8 * s + (lane >> 3);
-            const u32x4_t v = read_lds_words(at + r * 128 + (((lane & 7) ^ ((r >> 1) & 7)) << 4));
+            const u32x4_t v = read_lds_words(at + r * 128 + (((lane & 7) ^ (r >> 1)) << 4));
             if (row + r < rows && col < a.N) *(u32x4_t*)(a.out + (first_row + row + r) * a.N + col) = v;
         }
     }
@@ -451,7 +470,7 @@ __global__ __launch_bounds__(512) void k_grouped_gemm_fp4(Fp4Args a) {
     e = __builtin_amdgcn_readfirstlane(e);
     const ExpertRows er = expert_rows(a.rows, e);
     const int nt_m = (er.live + kTile - 1) / kTile;
-    order_tiles(local, nt_m, nt_n, &m, &n);
+    order_tiles<2>(local, nt_m, nt_n, &m, &n);
     const int each = ((er.live + nt_m - 1) / nt_m + 63) & ~63;  // rows of a tile; never leaves the last one empty
     const int m0 = __builtin_amdgcn_readfirstlane(m * each), n0 = __builtin_amdgcn_readfirstlane(n * kTile);
     const int rows = __builtin_amdgcn_readfirstlane(min(each, er.live - m0));

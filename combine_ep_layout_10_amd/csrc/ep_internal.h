@@ -227,6 +227,7 @@ struct RouteArgs {
     void* idx;
     float* w;
     int T, E, k, G, keep, best, score, renormalize, idx_bits, f32;
+    int group_lanes;  // lanes of a group where that is a power of two of whole lanes, else 0 (the launcher's)
     float scale;
 };
 
@@ -241,9 +242,12 @@ struct BalanceArgs {
     float* sums;       // [places, E]
     int32_t* pairs;    // [places, E]
     int32_t* tokens;   // [places]
-    double* unit;      // [S]: coef before the division by the sequences used
-    double* term;      // [S]
+    double* term;      // [S, chunks]
+    double* routed;    // [S]
+    int32_t* done;     // blocks of the second kernel that are done
     int T, E, k, S, score, idx_bits, f32;
+    int tile;          // tokens of a piece
+    int chunks;        // 64 experts each
 };
 
 struct RouteBackwardArgs {
@@ -261,9 +265,15 @@ struct RouteBackwardArgs {
 
 constexpr int kMaxRouteGroups = 64;         // one a lane
 constexpr int kMaxRouteTokens = 1 << 25;    // a wave each: 2^31 threads
-constexpr int kMaxRouteSequences = 1 << 20;
-constexpr int kBalanceTile = 64;   // tokens of a piece
-constexpr int kBalanceWaves = 16;  // of a piece
+constexpr int kMaxRouteSequences = 1 << 17;  // a block of 1,024 threads for 64 experts of each: 2^31 threads
+constexpr int kBalanceWaves = 8;             // of a piece
+
+// Tokens of a piece: a turn of its waves, and more where that would make over 512
+// pieces, which a block of the second kernel reads in turn. By the sizes alone.
+inline int balance_tile(int tokens) {
+    const int turn = 4 * kBalanceWaves, pieces = 512;
+    return ((tokens + pieces - 1) / pieces + turn - 1) / turn * turn + (tokens == 0 ? turn : 0);
+}
 
 // Padding rows per zero-fill piece (a piece of one expert's padding): in the
 // dispatch kernel, and in the single-launch layout + dispatch, where every
@@ -302,7 +312,7 @@ hipError_t launch_grouped_gemm_mxfp4_rows(const Fp4Args& a, int64_t pairs, hipSt
 hipError_t launch_quantize_mxfp4(QuantArgs a, int64_t rows, int32_t k, bool live_rows, bool f32, hipStream_t stream);
 hipError_t launch_rms_norm(const NormArgs& a, hipStream_t stream);
 hipError_t launch_rms_norm_backward(const NormBackwardArgs& a, hipStream_t stream);
-hipError_t launch_route(const RouteArgs& a, hipStream_t stream);
+hipError_t launch_route(RouteArgs a, hipStream_t stream);
 hipError_t launch_balance_loss(const BalanceArgs& a, hipStream_t stream);
 hipError_t launch_route_backward(const RouteBackwardArgs& a, hipStream_t stream);
 // Kernel arguments of the single-launch layout + dispatch, packed into the

@@ -107,14 +107,45 @@ __device__ __forceinline__ float wave_max_logit(const float l[V]) {
     return unordered(wave_max(ordered(m == m ? m : -__builtin_inff())));
 }
 
+// e^x for x <= 0, within four units 2^-24: 2^t of the rounded product t = x log2(e) (the
+// instruction's error is one unit of the last place), times the rest of the product.
+// Below 2^-160 it is 0, NaN stays.
+__device__ __forceinline__ float exp_negative(float x) {
+    const float t = x * 1.44269504f;
+    const float rest = __builtin_fmaf(x, 1.44269504f, -t) + x * 1.92596303e-8f;  // log2(e) to 48 bits
+    const float y = __builtin_amdgcn_exp2f(t) * __builtin_fmaf(rest, 0.693147181f, 1.0f);
+    return t < -160.0f ? 0.0f : y;
+}
+
+// 1 / (1 + e^-l), and its slope s (1 - s) without the difference. The reciprocal is
+// within one unit of the last place.
+__device__ __forceinline__ float sigmoid(float l, float* slope) {
+    const float e = exp_negative(-fabsf(l)), y = __builtin_amdgcn_rcpf(1.0f + e);
+    *slope = e * y * y;
+    return l >= 0.0f ? y : e * y;
+}
+
 // exp(l - max l) and their sum over the wave. A row of -infinity alone has none.
 template <int V>
-__device__ __forceinline__ float softmax_terms(const float l[V], float x[V]) {
-    const float m = wave_max_logit<V>(l);
+__device__ __forceinline__ float softmax_terms(const float l[V], float m, float x[V]) {
     float sum = 0.0f;
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-        x[v] = l[v] == -__builtin_inff() ? 0.0f : expf(l[v] - m);
+        x[v] = l[v] == -__builtin_inff() ? 0.0f : exp_negative(l[v] - m);
+        sum += x[v];
+    }
+    return wave_sum(sum);
+}
+
+// A token's scores and their sum: softmax's terms (divided by the sum they are the
+// scores), or sigmoids with their slopes.
+template <int V>
+__device__ __forceinline__ float score_terms(int score, const float l[V], float x[V], float slope[V]) {
+    if (score == EP_SCORE_SOFTMAX) return softmax_terms<V>(l, wave_max_logit<V>(l), x);
+    float sum = 0.0f;
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+        x[v] = sigmoid(l[v], &slope[v]);
         sum += x[v];
     }
     return wave_sum(sum);
@@ -123,11 +154,12 @@ __device__ __forceinline__ float softmax_terms(const float l[V], float x[V]) {
 // ---------------------------------------------------------------- choice
 
 // The highest of the wave's keys with its lowest index, which is cleared; false
-// when none is left. FULL: keys of 64 bits (hi, lo), otherwise hi alone.
+// when none is left. FULL: keys of 64 bits (hi, lo), otherwise hi alone. Which experts
+// have it is known in scalar registers, so most of a round is scalar work beside the
+// vector unit: three maxima, four steps over a row of 16, and two operations an expert.
 struct Taken {
     uint32_t hi, lo;
-    int lane;      // that holds it, the same in every lane
-    int v;         // in that lane: which of its experts
+    int lane, v;  // where, the same in every lane
 };
 
 template <int V, bool FULL>
@@ -137,28 +169,90 @@ __device__ __forceinline__ bool take_highest(uint32_t hi[V], const uint32_t lo[V
     for (int v = 1; v < V; ++v) m = max(m, hi[v]);
     t->hi = wave_max(m);
     if (t->hi == 0) return false;
+    uint64_t have[V], any = 0;
+    int count = 0;
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+        have[v] = ballot64(hi[v] == t->hi);
+        any |= have[v];
+        count += __builtin_popcountll(have[v]);
+    }
     t->lo = 0;
     if (FULL) {
         uint32_t n = 0;
 #pragma unroll
         for (int v = 0; v < V; ++v) n = hi[v] == t->hi ? max(n, lo[v]) : n;
-        t->lo = wave_max(n);
-    }
-    t->v = V;
+        if (count > 1) {  // the lower halves decide
+            t->lo = wave_max(n);
+            any = 0;
 #pragma unroll
-    for (int v = V - 1; v >= 0; --v)
-        if (hi[v] == t->hi && (!FULL || lo[v] == t->lo)) t->v = v;
-    t->lane = __builtin_ctzll(ballot64(t->v < V));
+            for (int v = 0; v < V; ++v) {
+                have[v] &= ballot64(lo[v] == t->lo);
+                any |= have[v];
+            }
+        } else {
+            t->lo = lane_value(n, __builtin_ctzll(any));
+        }
+    }
+    t->lane = __builtin_ctzll(any);
+    t->v = 0;
+#pragma unroll
+    for (int v = V - 1; v > 0; --v) t->v = (have[v] >> t->lane) & 1 ? v : t->v;
+    t->v = have[0] >> t->lane & 1 ? 0 : t->v;
     const bool mine = lane_id() == t->lane;
 #pragma unroll
     for (int v = 0; v < V; ++v) hi[v] = mine && v == t->v ? 0u : hi[v];
     return true;
 }
 
+// A group's key from its highest (first > 0) and second highest; 0: none.
+__device__ __forceinline__ uint64_t group_key(uint64_t first, uint64_t second, int best) {
+    if (best < 2 || second == 0) return first;
+    const double sum = unordered(first) + unordered(second);
+    return ordered(sum < kLowest64 ? kLowest64 : sum);
+}
+
+// The two highest of two pairs, each in order.
+__device__ __forceinline__ void merge_pairs(uint64_t* first, uint64_t* second, uint64_t a, uint64_t b) {
+    const bool more = a > *first;
+    const uint64_t low = more ? *first : a, high = more ? b : *second;
+    *first = more ? a : *first;
+    *second = low > high ? low : high;
+}
+
+template <int CTRL>
+__device__ __forceinline__ uint64_t dpp64(uint64_t v) {
+    return (uint64_t)dpp<CTRL>((uint32_t)(v >> 32)) << 32 | dpp<CTRL>((uint32_t)v);
+}
+
 // Clears the keys of the experts outside the best groups.
 template <int V, bool FULL>
 __device__ __forceinline__ void keep_groups(const RouteArgs& a, int lane, uint32_t hi[V], const uint32_t lo[V]) {
     const int size = a.E / a.G;
+    if (a.group_lanes > 0) {
+        // A group is a power of two of whole lanes: pairs are merged over them, and every
+        // lane ranks its own group (8192 tokens, 256 experts in 8 groups: 15 us of 31
+        // in place of the way below).
+        const int lanes = a.group_lanes;
+        uint64_t first = 0, second = 0;
+#pragma unroll
+        for (int v = 0; v < V; ++v) merge_pairs(&first, &second, (uint64_t)hi[v] << 32 | (FULL ? lo[v] : 0u), 0);
+        if (lanes > 1) merge_pairs(&first, &second, dpp64<0xB1>(first), dpp64<0xB1>(second));
+        if (lanes > 2) merge_pairs(&first, &second, dpp64<0x4E>(first), dpp64<0x4E>(second));
+        if (lanes > 4) merge_pairs(&first, &second, dpp64<0x141>(first), dpp64<0x141>(second));
+        if (lanes > 8) merge_pairs(&first, &second, dpp64<0x140>(first), dpp64<0x140>(second));
+        if (lanes > 16) merge_pairs(&first, &second, __shfl_xor(first, 16, kWave), __shfl_xor(second, 16, kWave));
+        if (lanes > 32) merge_pairs(&first, &second, __shfl_xor(first, 32, kWave), __shfl_xor(second, 32, kWave));
+        const uint64_t key = group_key(first, second, FULL ? a.best : 1);
+        int before = 0;  // groups that come first
+        for (int at = 0; at < a.G * lanes; at += lanes) {
+            const uint64_t other = (uint64_t)lane_value((uint32_t)(key >> 32), at) << 32 | lane_value((uint32_t)key, at);
+            before += other > key || (other == key && at + lanes <= lane) ? 1 : 0;
+        }
+#pragma unroll
+        for (int v = 0; v < V; ++v) hi[v] = before < a.keep ? hi[v] : 0u;
+        return;
+    }
     uint32_t group_hi[1] = {0u}, group_lo[1] = {0u};  // lane g: group g's
     for (int g = 0; g < a.G; ++g) {
         uint32_t h[V];
@@ -167,13 +261,11 @@ __device__ __forceinline__ void keep_groups(const RouteArgs& a, int lane, uint32
             const int e = lane * V + v;
             h[v] = e >= g * size && e < (g + 1) * size ? hi[v] : 0u;
         }
-        Taken first, second;
+        Taken first, second = {0u, 0u, 0, 0};
         if (!take_highest<V, FULL>(h, lo, &first)) continue;
-        uint64_t key = (uint64_t)first.hi << 32 | first.lo;
-        if (FULL && a.best == 2 && take_highest<V, FULL>(h, lo, &second)) {
-            const double sum = unordered(key) + unordered((uint64_t)second.hi << 32 | second.lo);
-            key = ordered(sum < kLowest64 ? kLowest64 : sum);
-        }
+        if (FULL && a.best == 2 && !take_highest<V, FULL>(h, lo, &second)) second.hi = second.lo = 0u;
+        const uint64_t key = group_key((uint64_t)first.hi << 32 | first.lo, (uint64_t)second.hi << 32 | second.lo,
+                                       FULL ? a.best : 1);
         if (lane == g) {
             group_hi[0] = (uint32_t)(key >> 32);
             group_lo[0] = (uint32_t)key;
@@ -236,7 +328,7 @@ __global__ __launch_bounds__(64 * kRouteWaves) void k_route(RouteArgs a) {
             if (a.score == EP_SCORE_SOFTMAX) {
                 float x[V];
                 max_l = wave_max_logit<V>(l);
-                sum = softmax_terms<V>(l, x);
+                sum = softmax_terms<V>(l, max_l, x);
             }
 #pragma unroll
             for (int v = 0; v < V; ++v) {
@@ -248,17 +340,19 @@ __global__ __launch_bounds__(64 * kRouteWaves) void k_route(RouteArgs a) {
         for (int j = 0; j < a.k; ++j) {
             Taken p;
             if (!take_highest<V, FULL>(hi, lo, &p)) break;
-            float x = s[0];
-#pragma unroll
-            for (int v = 1; v < V; ++v) x = v == p.v ? s[v] : x;
-            const int e = (int)lane_value((uint32_t)(lane * V + p.v), p.lane);
-            x = lane_value(x, p.lane);
-            if (lane == j) {
-                chosen = e;
-                w = x;
-            }
+            chosen = lane == j ? p.lane * V + p.v : chosen;
         }
-        if (!FULL && chosen >= 0) w = a.score == EP_SCORE_SOFTMAX ? expf(w - max_l) / sum : 1.0f / (1.0f + expf(-w));
+        // the chosen experts' scores (or logits) from the lanes that hold them
+        const int at = chosen >= 0 ? chosen : 0;
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            const float x = __shfl(s[v], at / V, kWave);
+            w = chosen >= 0 && v == at % V ? x : w;
+        }
+        if (!FULL && chosen >= 0) {
+            float slope;
+            w = a.score == EP_SCORE_SOFTMAX ? exp_negative(w - max_l) / sum : sigmoid(w, &slope);
+        }
         if (a.renormalize) {
             const float total = wave_sum(w) + 1e-20f;
             w /= total;
@@ -295,16 +389,20 @@ __device__ __forceinline__ int sequence_past(const int32_t* off, int S, int t) {
     return lo;
 }
 
-// Tile b (kBalanceTile tokens) by sequence q: a piece of its own at place b + q of
-// the partial sums. The pieces of a batch run from (0, 0) up in b or in q, never
-// both, so places are distinct.
+// Tile b (a.tile tokens) by sequence q: a piece of its own at place b + q of the
+// partial sums. The pieces of a batch run from (0, 0) up in b or in q, never both,
+// so places are distinct. A wave has kBalanceAhead tokens in flight; their shares are
+// added in binary32, and those sums in binary64.
+constexpr int kBalanceAhead = 4;
+
 template <int V>
 __global__ __launch_bounds__(64 * kBalanceWaves) void k_balance_pieces(BalanceArgs a) {
     __shared__ float s_sum[kBalanceWaves][64 * V];
     __shared__ int s_count[64 * V];
     __shared__ int s_tokens;
     const int tid = threadIdx.x, lane = lane_id(), wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int t0 = (int)blockIdx.x * kBalanceTile, t1 = min(t0 + kBalanceTile, a.T);
+    const int t0 = (int)blockIdx.x * a.tile, t1 = min(t0 + a.tile, a.T);
+    if (blockIdx.x == 0 && tid == 0) *a.done = 0;
     int q = a.seq_off != nullptr ? sequence_past(a.seq_off, a.S, t0) : 0;
     for (; q < a.S; ++q) {
         int from = t0, to = t1;
@@ -318,40 +416,46 @@ __global__ __launch_bounds__(64 * kBalanceWaves) void k_balance_pieces(BalanceAr
         for (int e = tid; e < 64 * V; e += 64 * kBalanceWaves) s_count[e] = 0;
         if (tid == 0) s_tokens = 0;
         __syncthreads();
-        float sum[V];
+        double sum[V];
 #pragma unroll
-        for (int v = 0; v < V; ++v) sum[v] = 0.0f;
+        for (int v = 0; v < V; ++v) sum[v] = 0.0;
         int tokens = 0;
-        for (int t = from + wave; t < to; t += kBalanceWaves) {
-            const int id = lane < a.k ? load_id(a.idx, a.idx_bits, (int64_t)t * a.k + lane, a.E) : -1;
-            if (ballot64(id >= 0) == 0) continue;
-            if (id >= 0) atomicAdd(&s_count[id], 1);
-            ++tokens;
-            float l[V], x[V];
-            load_logits<V>(a.logits, a.f32, t, a.E, lane, l);
-            float total;
-            if (a.score == EP_SCORE_SOFTMAX) {
-                total = softmax_terms<V>(l, x);
-            } else {
-                total = 0.0f;
+        for (int t = from + wave; t < to; t += kBalanceAhead * kBalanceWaves) {
+            int id[kBalanceAhead];
+            float l[kBalanceAhead][V];
 #pragma unroll
-                for (int v = 0; v < V; ++v) {
-                    x[v] = 1.0f / (1.0f + expf(-l[v]));
-                    total += x[v];
-                }
-                total = wave_sum(total);
+            for (int i = 0; i < kBalanceAhead; ++i) {
+                const int u = t + i * kBalanceWaves;
+                id[i] = -1;
+                if (u >= to) continue;
+                if (lane < a.k) id[i] = load_id(a.idx, a.idx_bits, (int64_t)u * a.k + lane, a.E);
+                load_logits<V>(a.logits, a.f32, u, a.E, lane, l[i]);
             }
-            const float inv = total == 0.0f ? 0.0f : 1.0f / total;
+            float part[V];
 #pragma unroll
-            for (int v = 0; v < V; ++v) sum[v] += x[v] * inv;
+            for (int v = 0; v < V; ++v) part[v] = 0.0f;
+#pragma unroll
+            for (int i = 0; i < kBalanceAhead; ++i) {
+                if (ballot64(id[i] >= 0) == 0) continue;
+                if (id[i] >= 0) atomicAdd(&s_count[id[i]], 1);
+                ++tokens;
+                float x[V], slope[V];
+                const float total = score_terms<V>(a.score, l[i], x, slope);
+                const float inv = total == 0.0f ? 0.0f : 1.0f / total;
+#pragma unroll
+                for (int v = 0; v < V; ++v) part[v] += x[v] * inv;
+            }
+#pragma unroll
+            for (int v = 0; v < V; ++v) sum[v] += (double)part[v];
         }
 #pragma unroll
-        for (int v = 0; v < V; ++v) s_sum[wave][lane * V + v] = sum[v];
+        for (int v = 0; v < V; ++v) s_sum[wave][lane * V + v] = (float)sum[v];
         if (lane == 0 && tokens > 0) atomicAdd(&s_tokens, tokens);
         __syncthreads();
         const int64_t place = (int64_t)blockIdx.x + q;
         for (int e = tid; e < a.E; e += 64 * kBalanceWaves) {
             float total = 0.0f;
+#pragma unroll
             for (int i = 0; i < kBalanceWaves; ++i) total += s_sum[i][e];
             a.sums[place * a.E + e] = total;
             a.pairs[place * a.E + e] = s_count[e];
@@ -371,56 +475,74 @@ __device__ __forceinline__ double block_sum(double v, double* tmp) {
     return s;
 }
 
-// One sequence a block: its counts, its routed tokens and its term of the loss. A
-// batch of one sequence has its loss at once.
-__global__ __launch_bounds__(1024) void k_balance_sequences(BalanceArgs a) {
+// 64 experts of one sequence a block: their counts, and their part of the sequence's
+// term. The block that comes last (a count that the first kernel cleared) adds the
+// parts in order, so that nothing depends on which one that is.
+__global__ __launch_bounds__(1024) void k_balance_loss(BalanceArgs a) {
+    __shared__ double s_sum[16][64];
+    __shared__ int s_pairs[16][64];
     __shared__ double s_tmp[16];
-    const int q = blockIdx.x, tid = threadIdx.x;
+    __shared__ int s_last;
+    const int tid = threadIdx.x, x = tid & 63, y = tid >> 6;
+    const int q = blockIdx.x / a.chunks, chunk = blockIdx.x % a.chunks, e = chunk * 64 + x;
     int from = 0, to = a.T;
     if (a.seq_off != nullptr) {
         from = max(0, a.seq_off[q]);
         to = min(a.T, a.seq_off[q + 1]);
     }
-    const int b0 = from / kBalanceTile, b1 = from < to ? (to - 1) / kBalanceTile + 1 : b0;
-    double term = 0.0;
-    if (tid < a.E) {
-        double sum = 0.0;
-        int count = 0;
-        for (int b = b0; b < b1; ++b) {
-            const int64_t at = ((int64_t)b + q) * a.E + tid;
+    const int b0 = from / a.tile, b1 = from < to ? (to - 1) / a.tile + 1 : b0;
+    double sum = 0.0;
+    int pairs = 0;
+    if (e < a.E) {
+#pragma unroll 8
+        for (int b = b0 + y; b < b1; b += 16) {
+            const int64_t at = ((int64_t)b + q) * a.E + e;
             sum += (double)a.sums[at];
-            count += a.pairs[at];
+            pairs += a.pairs[at];
         }
-        a.counts[(int64_t)q * a.E + tid] = count;
-        term = (double)count * sum;
     }
     double tokens = 0.0;
     for (int b = b0 + tid; b < b1; b += 1024) tokens += (double)a.tokens[b + q];
-    term = block_sum(term, s_tmp);
+    s_sum[y][x] = sum;
+    s_pairs[y][x] = pairs;
     tokens = block_sum(tokens, s_tmp);
-    if (tid != 0) return;
-    const double c = tokens > 0.0 ? (double)a.E / ((double)a.k * tokens * tokens) : 0.0;
-    if (a.S == 1) {
-        a.coef[0] = (float)c;
-        a.loss[0] = (float)(c * term);
-    } else {
-        a.unit[q] = c;
-        a.term[q] = c * term;
+    if (y == 0) {
+#pragma unroll
+        for (int i = 1; i < 16; ++i) {
+            sum += s_sum[i][x];
+            pairs += s_pairs[i][x];
+        }
+        if (e < a.E) a.counts[(int64_t)q * a.E + e] = pairs;
+        sum = wave_sum((double)pairs * sum);
+        if (x == 0) {
+            __hip_atomic_store(&a.term[blockIdx.x], sum, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+            if (chunk == 0)
+                __hip_atomic_store(&a.routed[q], tokens, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+            s_last = __hip_atomic_fetch_add(a.done, 1, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT) == (int)gridDim.x - 1;
+        }
     }
-}
-
-__global__ __launch_bounds__(1024) void k_balance_loss(BalanceArgs a) {
-    __shared__ double s_tmp[16];
+    __syncthreads();
+    if (!s_last) return;
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "agent");
+    const double k = (double)a.k, E = (double)a.E;
     double used = 0.0, loss = 0.0;
-    for (int q = threadIdx.x; q < a.S; q += 1024) {
-        used += a.unit[q] > 0.0 ? 1.0 : 0.0;
-        loss += a.term[q];
+    for (int s = tid; s < a.S; s += 1024) {
+        const double n = __hip_atomic_load(&a.routed[s], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        if (n == 0.0) continue;
+        double term = 0.0;
+        for (int c = 0; c < a.chunks; ++c)
+            term += __hip_atomic_load(&a.term[s * a.chunks + c], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        used += 1.0;
+        loss += E / (k * n * n) * term;
     }
     used = block_sum(used, s_tmp);
     loss = block_sum(loss, s_tmp);
     if (used < 1.0) used = 1.0;
-    for (int q = threadIdx.x; q < a.S; q += 1024) a.coef[q] = (float)(a.unit[q] / used);
-    if (threadIdx.x == 0) a.loss[0] = (float)(loss / used);
+    for (int s = tid; s < a.S; s += 1024) {
+        const double n = __hip_atomic_load(&a.routed[s], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        a.coef[s] = n == 0.0 ? 0.0f : (float)(E / (k * n * n * used));
+    }
+    if (tid == 0) a.loss[0] = (float)(loss / used);
 }
 
 // ---------------------------------------------------------------- gradient
@@ -436,46 +558,45 @@ __global__ __launch_bounds__(64 * kRouteWaves) void k_route_backward(RouteBackwa
     const int id = lane < a.k ? load_id(a.idx, a.idx_bits, (int64_t)t * a.k + lane, a.E) : -1;
     if (ballot64(id >= 0) != 0) {
         const float gw = a.grad_w != nullptr && lane < a.k ? a.grad_w[(int64_t)t * a.k + lane] : 0.0f;
-        float l[V], s[V], n[V], u[V], b[V];
+        float l[V], s[V], slope[V], u[V], b[V];
+        int n[V];
         load_logits<V>(a.logits, a.f32, t, a.E, lane, l);
         const bool softmax = a.score == EP_SCORE_SOFTMAX;
-        float total = 0.0f;
+        const float total = score_terms<V>(a.score, l, s, slope);
+        const float inv = total == 0.0f ? 0.0f : 1.0f / total;
         if (softmax) {
-            total = softmax_terms<V>(l, s);
-            const float inv = total == 0.0f ? 0.0f : 1.0f / total;
 #pragma unroll
             for (int v = 0; v < V; ++v) s[v] *= inv;
-        } else {
-#pragma unroll
-            for (int v = 0; v < V; ++v) {
-                s[v] = 1.0f / (1.0f + expf(-l[v]));
-                total += s[v];
-            }
-            total = wave_sum(total);
         }
 #pragma unroll
-        for (int v = 0; v < V; ++v) n[v] = u[v] = b[v] = 0.0f;
+        for (int v = 0; v < V; ++v) {
+            u[v] = b[v] = 0.0f;
+            n[v] = 0;
+        }
         if (a.grad_w != nullptr) {
             for (int j = 0; j < a.k; ++j) {
-                const int e = (int)lane_value((uint32_t)id, j) - lane * V;
+                const int e = (int)lane_value((uint32_t)id, j);
+                if (e < 0) continue;
                 const float g = lane_value(gw, j);
+                const bool mine = lane == e / V;
 #pragma unroll
                 for (int v = 0; v < V; ++v) {
-                    n[v] += e == v ? 1.0f : 0.0f;
-                    u[v] += e == v ? g : 0.0f;
+                    if (v != e % V) continue;  // a scalar branch
+                    u[v] += mine ? g : 0.0f;
+                    n[v] += mine ? 1 : 0;
                 }
             }
             if (a.renormalize) {
                 float d = 0.0f, q = 0.0f;
 #pragma unroll
                 for (int v = 0; v < V; ++v) {
-                    d += n[v] * s[v];
+                    d += (float)n[v] * s[v];
                     q += u[v] * s[v];
                 }
                 d = wave_sum(d) + 1e-20f;
                 q = wave_sum(q) / d;
 #pragma unroll
-                for (int v = 0; v < V; ++v) u[v] = n[v] > 0.0f ? a.scale * ((u[v] - n[v] * q) / d) : 0.0f;
+                for (int v = 0; v < V; ++v) u[v] = n[v] > 0 ? a.scale * ((u[v] - (float)n[v] * q) / d) : 0.0f;
             } else {
 #pragma unroll
                 for (int v = 0; v < V; ++v) u[v] *= a.scale;
@@ -506,7 +627,6 @@ __global__ __launch_bounds__(64 * kRouteWaves) void k_route_backward(RouteBackwa
 #pragma unroll
                     for (int v = 0; v < V; ++v) b[v] -= mean;
                 } else {
-                    const float inv = total == 0.0f ? 0.0f : 1.0f / total;
 #pragma unroll
                     for (int v = 0; v < V; ++v) b[v] = (b[v] - mean * inv) * inv;
                 }
@@ -524,15 +644,28 @@ __global__ __launch_bounds__(64 * kRouteWaves) void k_route_backward(RouteBackwa
             for (int v = 0; v < V; ++v) grad[v] = s[v] * (u[v] - mean);
         } else {
 #pragma unroll
-            for (int v = 0; v < V; ++v) {
-                // s (1 - s) without the difference
-                const float x = expf(-fabsf(l[v])), y = 1.0f / (1.0f + x);
-                grad[v] = x * y * y * (u[v] + b[v]);
-            }
+            for (int v = 0; v < V; ++v) grad[v] = slope[v] * (u[v] + b[v]);
         }
     }
     const int e = lane * V;
     const int64_t at = (int64_t)t * a.E + e;
+    if (a.E % V == 0) {
+        if (e >= a.E) return;
+        if (a.f32) {
+            typedef float vec __attribute__((ext_vector_type(V), aligned(4)));
+            vec x;
+#pragma unroll
+            for (int v = 0; v < V; ++v) x[v] = grad[v];
+            *(vec*)((float*)a.grad + at) = x;
+        } else {
+            typedef uint16_t vec __attribute__((ext_vector_type(V), aligned(2)));
+            vec x;
+#pragma unroll
+            for (int v = 0; v < V; ++v) x[v] = (uint16_t)pack_bf16x2(grad[v], 0.0f);
+            *(vec*)((uint16_t*)a.grad + at) = x;
+        }
+        return;
+    }
 #pragma unroll
     for (int v = 0; v < V; ++v) {
         if (e + v >= a.E) continue;
@@ -553,8 +686,12 @@ void for_experts(int E, F f) {
 
 }  // namespace
 
-hipError_t launch_route(const RouteArgs& a, hipStream_t stream) {
+hipError_t launch_route(RouteArgs a, hipStream_t stream) {
     if (a.T == 0) return hipSuccess;
+    int V = 1;  // experts of a lane
+    while (64 * V < a.E) V *= 2;
+    const int size = a.E / a.G, lanes = size / V;
+    a.group_lanes = size % V == 0 && (lanes & (lanes - 1)) == 0 ? lanes : 0;
     const dim3 grid((unsigned)((a.T + kRouteWaves - 1) / kRouteWaves)), block(64 * kRouteWaves);
     const bool full = a.bias != nullptr || (a.G > 1 && a.best > 1);
     if (launch_debug()) launch_debug_print("k_route", grid, block, "experts %d keys %d", a.E, full ? 64 : 32);
@@ -567,23 +704,16 @@ hipError_t launch_route(const RouteArgs& a, hipStream_t stream) {
 }
 
 hipError_t launch_balance_loss(const BalanceArgs& a, hipStream_t stream) {
-    const int tiles = (a.T + kBalanceTile - 1) / kBalanceTile;
+    const int tiles = a.T > 0 ? (a.T + a.tile - 1) / a.tile : 1;  // one clears the count
     const dim3 grid((unsigned)tiles), block(64 * kBalanceWaves);
     if (launch_debug()) launch_debug_print("k_balance_pieces", grid, block, "experts %d sequences %d", a.E, a.S);
-    if (tiles > 0) {
-        for_experts(a.E, [&](auto v) {
-            constexpr int V = decltype(v)::value;
-            hipLaunchKernelGGL(k_balance_pieces<V>, grid, block, 0, stream, a);
-        });
-        const hipError_t e = hipGetLastError();
-        if (e != hipSuccess) return e;
-    }
-    hipLaunchKernelGGL(k_balance_sequences, dim3((unsigned)a.S), dim3(1024), 0, stream, a);
-    if (a.S > 1) {
-        const hipError_t e = hipGetLastError();
-        if (e != hipSuccess) return e;
-        hipLaunchKernelGGL(k_balance_loss, dim3(1), dim3(1024), 0, stream, a);
-    }
+    for_experts(a.E, [&](auto v) {
+        constexpr int V = decltype(v)::value;
+        hipLaunchKernelGGL(k_balance_pieces<V>, grid, block, 0, stream, a);
+    });
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    hipLaunchKernelGGL(k_balance_loss, dim3((unsigned)(a.S * a.chunks)), dim3(1024), 0, stream, a);
     return hipGetLastError();
 }
 

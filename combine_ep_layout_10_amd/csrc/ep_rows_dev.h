@@ -88,20 +88,20 @@ __device__ __forceinline__ bool find_expert(const RowsArgs& a, int bm, int per, 
     return false;
 }
 
-constexpr int kGroupRows = 4;  // row tiles that share column tiles in the block order
-
 // Tile of logical block `local` among an expert's nt_m x nt_n: groups of
-// kGroupRows row tiles, within a group column by column, so that blocks that run
+// GROUP row tiles, within a group column by column, so that blocks that run
 // together on an XCD share few operand tiles; a last, shorter row tile comes in a
 // group of its own or with few others, and does not put the long ones out of step.
 // BF16, 65,536 rows x 4096 x 7168 on 32 experts: groups of 4, 8, 16 fetch 9.4, 12.0, 14.9
-// GB into L2 (in 3.24, 3.24, 3.28 ms then).
+// GB into L2 (in 3.24, 3.24, 3.28 ms then). MXFP4 rows and weights, the same sizes:
+// groups of 2, 3, 4, 8 take 0.993, 0.997, 1.014, 1.03 ms.
+template <int GROUP>
 __device__ __forceinline__ void order_tiles(int local, int nt_m, int nt_n, int* m, int* n) {
-    const int g = local / (kGroupRows * nt_n);
-    const int in_group = min(kGroupRows, nt_m - g * kGroupRows);
-    const int rem = local - g * kGroupRows * nt_n;
+    const int g = local / (GROUP * nt_n);
+    const int in_group = min(GROUP, nt_m - g * GROUP);
+    const int rem = local - g * GROUP * nt_n;
     *n = rem / in_group;
-    *m = g * kGroupRows + rem % in_group;
+    *m = g * GROUP + rem % in_group;
 }
 
 // Most row tiles of bm rows that `pairs` pairs can need: an expert with c rows

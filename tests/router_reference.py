@@ -125,10 +125,11 @@ def backward(logits, idx, grad_w, counts, coef, grad_loss, off, r):
 
 
 def spread(logits):
-    """Largest distance of a token's finite logits: what an exponent's argument may be off by, in units of 2^-24."""
+    """Largest distance of a token's finite logits: what an exponent's argument may be off by, in units of
+    2^-24. At most 400: exponentials below 2^-160 are zero on either side of any comparison."""
     l = logits.detach().double().cpu()
     l = l[torch.isfinite(l)]
-    return float(l.max() - l.min()) + float(l.abs().max()) if l.numel() else 0.0
+    return min(400.0, float(l.max() - l.min()) + float(l.abs().max())) if l.numel() else 0.0
 
 
 def close(got, want, tol, what):

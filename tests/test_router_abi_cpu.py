@@ -81,13 +81,13 @@ def test_balance_pointers():
     assert call(a4=None) == BAD and "seq_off" in F.last_error_message()
     assert call(a4=off(2)) == BAD
     assert call(a5=0) == BAD and call(a5=-1) == BAD
-    assert call(a5=(1 << 20) + 1) == UNSUP
+    assert call(a5=(1 << 17) + 1) == UNSUP
     assert call(a9=off(128)) == BAD
     need = l.ep_balance_loss_workspace_bytes(r, 4, 3)
     assert need > 0 and need % 256 == 0
     assert call(a10=need - 1) == WS
     assert l.ep_balance_loss_workspace_bytes(r, 4, 0) == 0
-    assert l.ep_balance_loss_workspace_bytes(r, 1 << 25, 1 << 20) > 4 * 64 * ((1 << 19) + (1 << 20)) * 2
+    assert l.ep_balance_loss_workspace_bytes(r, 1 << 25, 1 << 17) > 8 * 64 * (512 + (1 << 17))
 
 
 def test_backward_pointers():
