@@ -360,7 +360,7 @@ BalanceMap balance_map(int E, int32_t num_tokens, int32_t num_seqs) {
     m.pairs = take(4 * places * E);
     m.tokens = take(4 * places);
     m.term = take(8 * (size_t)num_seqs * ((E + 63) / 64));
-    m.routed = take(8 * (size_t)num_seqs);
+    m.routed = take(4 * (size_t)num_seqs);
     m.done = take(4);
     m.total = o;
     return m;
@@ -982,7 +982,7 @@ ep_status ep_balance_loss(const ep_router* r, int32_t num_tokens, const void* lo
     a.pairs = (int32_t*)(ws + m.pairs);
     a.tokens = (int32_t*)(ws + m.tokens);
     a.term = (double*)(ws + m.term);
-    a.routed = (double*)(ws + m.routed);
+    a.routed = (int32_t*)(ws + m.routed);
     a.done = (int32_t*)(ws + m.done);
     a.T = num_tokens;
     a.E = r->num_experts;

@@ -243,7 +243,7 @@ struct BalanceArgs {
     int32_t* pairs;    // [places, E]
     int32_t* tokens;   // [places]
     double* term;      // [S, chunks]
-    double* routed;    // [S]
+    int32_t* routed;   // [S]: tokens
     int32_t* done;     // blocks of the second kernel that are done
     int T, E, k, S, score, idx_bits, f32;
     int tile;          // tokens of a piece

@@ -49,10 +49,21 @@ __device__ __forceinline__ float wave_sum(float v) {
     return (lane_value(v, 0) + lane_value(v, 16)) + (lane_value(v, 32) + lane_value(v, 48));
 }
 
+template <int CTRL>
+__device__ __forceinline__ double dpp(double v) {
+    const uint64_t u = (uint64_t)__double_as_longlong(v);
+    return __longlong_as_double((long long)((uint64_t)dpp<CTRL>((uint32_t)(u >> 32)) << 32 | dpp<CTRL>((uint32_t)u)));
+}
+__device__ __forceinline__ double lane_value(double v, int lane) {
+    const uint64_t u = (uint64_t)__double_as_longlong(v);
+    return __longlong_as_double((long long)((uint64_t)lane_value((uint32_t)(u >> 32), lane) << 32 | lane_value((uint32_t)u, lane)));
+}
 __device__ __forceinline__ double wave_sum(double v) {
-#pragma unroll
-    for (int o = 32; o > 0; o >>= 1) v += __shfl_xor(v, o, kWave);
-    return v;
+    v += dpp<0xB1>(v);
+    v += dpp<0x4E>(v);
+    v += dpp<0x141>(v);
+    v += dpp<0x140>(v);
+    return (lane_value(v, 0) + lane_value(v, 16)) + (lane_value(v, 32) + lane_value(v, 48));
 }
 
 // Integers that order as the numbers do; -0 and +0 are equal.
@@ -158,7 +169,7 @@ __device__ __forceinline__ float score_terms(int score, const float l[V], float 
 // have it is known in scalar registers, so most of a round is scalar work beside the
 // vector unit: three maxima, four steps over a row of 16, and two operations an expert.
 struct Taken {
-    uint32_t hi, lo;
+    uint32_t hi;
     int lane, v;  // where, the same in every lane
 };
 
@@ -177,21 +188,16 @@ __device__ __forceinline__ bool take_highest(uint32_t hi[V], const uint32_t lo[V
         any |= have[v];
         count += __builtin_popcountll(have[v]);
     }
-    t->lo = 0;
-    if (FULL) {
+    if (FULL && count > 1) {  // the lower halves decide
         uint32_t n = 0;
 #pragma unroll
         for (int v = 0; v < V; ++v) n = hi[v] == t->hi ? max(n, lo[v]) : n;
-        if (count > 1) {  // the lower halves decide
-            t->lo = wave_max(n);
-            any = 0;
+        n = wave_max(n);
+        any = 0;
 #pragma unroll
-            for (int v = 0; v < V; ++v) {
-                have[v] &= ballot64(lo[v] == t->lo);
-                any |= have[v];
-            }
-        } else {
-            t->lo = lane_value(n, __builtin_ctzll(any));
+        for (int v = 0; v < V; ++v) {
+            have[v] &= ballot64(lo[v] == n);
+            any |= have[v];
         }
     }
     t->lane = __builtin_ctzll(any);
@@ -230,9 +236,8 @@ template <int V, bool FULL>
 __device__ __forceinline__ void keep_groups(const RouteArgs& a, int lane, uint32_t hi[V], const uint32_t lo[V]) {
     const int size = a.E / a.G;
     if (a.group_lanes > 0) {
-        // A group is a power of two of whole lanes: pairs are merged over them, and every
-        // lane ranks its own group (8192 tokens, 256 experts in 8 groups: 15 us of 31
-        // in place of the way below).
+        // A group is a power of two of whole lanes: pairs of its highest keys are merged
+        // over them, and every lane ranks its own group.
         const int lanes = a.group_lanes;
         uint64_t first = 0, second = 0;
 #pragma unroll
@@ -244,10 +249,15 @@ __device__ __forceinline__ void keep_groups(const RouteArgs& a, int lane, uint32
         if (lanes > 16) merge_pairs(&first, &second, __shfl_xor(first, 16, kWave), __shfl_xor(second, 16, kWave));
         if (lanes > 32) merge_pairs(&first, &second, __shfl_xor(first, 32, kWave), __shfl_xor(second, 32, kWave));
         const uint64_t key = group_key(first, second, FULL ? a.best : 1);
-        int before = 0;  // groups that come first
-        for (int at = 0; at < a.G * lanes; at += lanes) {
-            const uint64_t other = (uint64_t)lane_value((uint32_t)(key >> 32), at) << 32 | lane_value((uint32_t)key, at);
-            before += other > key || (other == key && at + lanes <= lane) ? 1 : 0;
+        // groups that come first: each lane of a group asks about one of them
+        int before = 0;
+        const int mine = lane & (lanes - 1), base = lane - mine;
+        const uint64_t own = lanes < 64 ? (1ull << lanes) - 1 : ~0ull;
+        for (int g0 = 0; g0 < a.G; g0 += lanes) {
+            const int g = g0 + mine, at = min(g, a.G - 1) * lanes;
+            const uint64_t other = __shfl(key, at, kWave);
+            const bool ahead = g < a.G && (other > key || (other == key && at < base));
+            before += __popcll((ballot64(ahead) >> base) & own);
         }
 #pragma unroll
         for (int v = 0; v < V; ++v) hi[v] = before < a.keep ? hi[v] : 0u;
@@ -261,11 +271,17 @@ __device__ __forceinline__ void keep_groups(const RouteArgs& a, int lane, uint32
             const int e = lane * V + v;
             h[v] = e >= g * size && e < (g + 1) * size ? hi[v] : 0u;
         }
-        Taken first, second = {0u, 0u, 0, 0};
-        if (!take_highest<V, FULL>(h, lo, &first)) continue;
-        if (FULL && a.best == 2 && !take_highest<V, FULL>(h, lo, &second)) second.hi = second.lo = 0u;
-        const uint64_t key = group_key((uint64_t)first.hi << 32 | first.lo, (uint64_t)second.hi << 32 | second.lo,
-                                       FULL ? a.best : 1);
+        const auto taken = [&]() -> uint64_t {
+            Taken t;
+            if (!take_highest<V, FULL>(h, lo, &t)) return 0;
+            uint32_t low = 0;
+#pragma unroll
+            for (int v = 0; v < V; ++v) low = FULL && v == t.v ? lane_value(lo[v], t.lane) : low;
+            return (uint64_t)t.hi << 32 | low;
+        };
+        const uint64_t first = taken();
+        if (first == 0) continue;
+        const uint64_t key = group_key(first, FULL && a.best == 2 ? taken() : 0, FULL ? a.best : 1);
         if (lane == g) {
             group_hi[0] = (uint32_t)(key >> 32);
             group_lo[0] = (uint32_t)key;
@@ -378,13 +394,17 @@ __device__ __forceinline__ int load_id(const void* idx, int idx_bits, int64_t at
     return i >= 0 && i < E ? i : -1;
 }
 
-// The first sequence whose end lies past token t (S: none).
+// The first sequence whose end lies past token t (S: none), the same in every lane: the
+// wave asks about 64 ends at a time, a 64th of the rest each.
 __device__ __forceinline__ int sequence_past(const int32_t* off, int S, int t) {
-    int lo = 0, hi = S;
-    while (lo < hi) {
-        const int mid = (lo + hi) >> 1;
-        if (off[mid + 1] > t) hi = mid;
-        else lo = mid + 1;
+    int lo = 0, n = S;
+    while (n > 0) {
+        const int step = (n + 63) / 64, at = lane_id() * step;
+        const bool behind = at < n && off[lo + min(at + step, n)] <= t;
+        const int c = __builtin_popcountll(ballot64(behind)) * step;
+        lo += min(c, n);
+        if (step == 1) break;
+        n = min(step, n - c);
     }
     return lo;
 }
@@ -465,23 +485,13 @@ __global__ __launch_bounds__(64 * kBalanceWaves) void k_balance_pieces(BalanceAr
     }
 }
 
-__device__ __forceinline__ double block_sum(double v, double* tmp) {
-    v = wave_sum(v);
-    __syncthreads();
-    if (lane_id() == 0) tmp[threadIdx.x >> 6] = v;
-    __syncthreads();
-    double s = 0.0;
-    for (int i = 0; i < (int)(blockDim.x >> 6); ++i) s += tmp[i];
-    return s;
-}
-
 // 64 experts of one sequence a block: their counts, and their part of the sequence's
 // term. The block that comes last (a count that the first kernel cleared) adds the
 // parts in order, so that nothing depends on which one that is.
 __global__ __launch_bounds__(1024) void k_balance_loss(BalanceArgs a) {
     __shared__ double s_sum[16][64];
     __shared__ int s_pairs[16][64];
-    __shared__ double s_tmp[16];
+    __shared__ int s_tokens[16];
     __shared__ int s_last;
     const int tid = threadIdx.x, x = tid & 63, y = tid >> 6;
     const int q = blockIdx.x / a.chunks, chunk = blockIdx.x % a.chunks, e = chunk * 64 + x;
@@ -492,63 +502,94 @@ __global__ __launch_bounds__(1024) void k_balance_loss(BalanceArgs a) {
     }
     const int b0 = from / a.tile, b1 = from < to ? (to - 1) / a.tile + 1 : b0;
     double sum = 0.0;
-    int pairs = 0;
-    if (e < a.E) {
+    int pairs = 0, tokens = 0;
+    const int column = min(e, a.E - 1);
 #pragma unroll 8
-        for (int b = b0 + y; b < b1; b += 16) {
-            const int64_t at = ((int64_t)b + q) * a.E + e;
-            sum += (double)a.sums[at];
-            pairs += a.pairs[at];
-        }
+    for (int b = b0 + y; b < b1; b += 16) {
+        const int64_t at = ((int64_t)b + q) * a.E + column;
+        sum += (double)a.sums[at];
+        pairs += a.pairs[at];
+        tokens += a.tokens[b + q];
     }
-    double tokens = 0.0;
-    for (int b = b0 + tid; b < b1; b += 1024) tokens += (double)a.tokens[b + q];
+    if (e >= a.E) {
+        sum = 0.0;
+        pairs = 0;
+    }
     s_sum[y][x] = sum;
     s_pairs[y][x] = pairs;
-    tokens = block_sum(tokens, s_tmp);
+    if (x == 0) s_tokens[y] = tokens;
+    __syncthreads();
     if (y == 0) {
 #pragma unroll
         for (int i = 1; i < 16; ++i) {
             sum += s_sum[i][x];
             pairs += s_pairs[i][x];
+            tokens += s_tokens[i];
         }
         if (e < a.E) a.counts[(int64_t)q * a.E + e] = pairs;
         sum = wave_sum((double)pairs * sum);
         if (x == 0) {
             __hip_atomic_store(&a.term[blockIdx.x], sum, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-            if (chunk == 0)
-                __hip_atomic_store(&a.routed[q], tokens, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+            if (chunk == 0) __hip_atomic_store(&a.routed[q], tokens, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
             s_last = __hip_atomic_fetch_add(a.done, 1, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT) == (int)gridDim.x - 1;
         }
     }
     __syncthreads();
     if (!s_last) return;
     __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "agent");
+    // sequences over the lanes of one wave, or of all waves where there are many
+    const int threads = a.S <= 64 ? 64 : 1024;
+    if (tid >= threads) return;
     const double k = (double)a.k, E = (double)a.E;
-    double used = 0.0, loss = 0.0;
-    for (int s = tid; s < a.S; s += 1024) {
-        const double n = __hip_atomic_load(&a.routed[s], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-        if (n == 0.0) continue;
+    double used = 0.0, loss = 0.0, unit = 0.0;  // unit: of this thread's only sequence, where it has one
+    for (int s = tid; s < a.S; s += threads) {
+        const int n = __hip_atomic_load(&a.routed[s], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
         double term = 0.0;
+#pragma unroll 4
         for (int c = 0; c < a.chunks; ++c)
             term += __hip_atomic_load(&a.term[s * a.chunks + c], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-        used += 1.0;
-        loss += E / (k * n * n) * term;
+        unit = n > 0 ? E / (k * (double)n * (double)n) : 0.0;
+        used += n > 0 ? 1.0 : 0.0;
+        loss += n > 0 ? unit * term : 0.0;
     }
-    used = block_sum(used, s_tmp);
-    loss = block_sum(loss, s_tmp);
+    used = wave_sum(used);
+    loss = wave_sum(loss);
+    if (threads > 64) {  // the waves' sums, in order
+        if (x == 0) {
+            s_sum[0][y] = used;
+            s_sum[1][y] = loss;
+        }
+        __syncthreads();
+        used = loss = 0.0;
+        for (int i = 0; i < 16; ++i) {
+            used += s_sum[0][i];
+            loss += s_sum[1][i];
+        }
+    }
     if (used < 1.0) used = 1.0;
-    for (int s = tid; s < a.S; s += 1024) {
-        const double n = __hip_atomic_load(&a.routed[s], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-        a.coef[s] = n == 0.0 ? 0.0f : (float)(E / (k * n * n * used));
-    }
     if (tid == 0) a.loss[0] = (float)(loss / used);
+    for (int s = tid; s < a.S; s += threads) {
+        if (a.S > threads) {
+            const int n = __hip_atomic_load(&a.routed[s], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+            unit = n > 0 ? E / (k * (double)n * (double)n) : 0.0;
+        }
+        a.coef[s] = (float)(unit / used);
+    }
 }
 
 // ---------------------------------------------------------------- gradient
 
+// Orders the LDS accesses of a wave's lanes for the compiler; the hardware keeps them
+// in order.
+__device__ __forceinline__ void wave_lds_fence() {
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+}
+
 template <int V>
 __global__ __launch_bounds__(64 * kRouteWaves) void k_route_backward(RouteBackwardArgs a) {
+    __shared__ int s_pairs[kRouteWaves][64 * V];
+    __shared__ float s_grads[kRouteWaves][64 * V];
     const int lane = lane_id();
     const int t = __builtin_amdgcn_readfirstlane(blockIdx.x * kRouteWaves + (threadIdx.x >> 6));
     if (t >= a.T) return;
@@ -574,17 +615,34 @@ __global__ __launch_bounds__(64 * kRouteWaves) void k_route_backward(RouteBackwa
             n[v] = 0;
         }
         if (a.grad_w != nullptr) {
-            for (int j = 0; j < a.k; ++j) {
-                const int e = (int)lane_value((uint32_t)id, j);
-                if (e < 0) continue;
-                const float g = lane_value(gw, j);
-                const bool mine = lane == e / V;
+            // scattered through the wave's own LDS, whose accesses stay in order; an expert
+            // that a token names twice has its gradients added in order instead
+            int* const pairs = s_pairs[threadIdx.x >> 6];
+            float* const grads = s_grads[threadIdx.x >> 6];
 #pragma unroll
-                for (int v = 0; v < V; ++v) {
-                    if (v != e % V) continue;  // a scalar branch
-                    u[v] += mine ? g : 0.0f;
-                    n[v] += mine ? 1 : 0;
+            for (int v = 0; v < V; ++v) {
+                pairs[lane * V + v] = 0;
+                grads[lane * V + v] = 0.0f;
+            }
+            wave_lds_fence();
+            if (id >= 0) atomicAdd(&pairs[id], 1);
+            if (id >= 0) grads[id] = gw;
+            wave_lds_fence();
+            const uint64_t twice = ballot64(id >= 0 && pairs[id] > 1);
+            if (twice != 0) {
+                for (int j = 0; j < a.k; ++j) {
+                    if (!((twice >> j) & 1)) continue;
+                    const int e = (int)lane_value((uint32_t)id, j);
+                    float sum = 0.0f;
+                    for (int i = 0; i < a.k; ++i) sum += (int)lane_value((uint32_t)id, i) == e ? lane_value(gw, i) : 0.0f;
+                    if (lane == j) grads[e] = sum;
                 }
+                wave_lds_fence();
+            }
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                n[v] = pairs[lane * V + v];
+                u[v] = grads[lane * V + v];
             }
             if (a.renormalize) {
                 float d = 0.0f, q = 0.0f;
@@ -606,7 +664,7 @@ __global__ __launch_bounds__(64 * kRouteWaves) void k_route_backward(RouteBackwa
             int q = 0;
             bool in = true;
             if (a.seq_off != nullptr) {
-                q = __builtin_amdgcn_readfirstlane(sequence_past(a.seq_off, a.S, t));
+                q = sequence_past(a.seq_off, a.S, t);
                 in = q < a.S && a.seq_off[q] <= t;
             }
             if (in) {
