@@ -26,7 +26,19 @@ namespace {
 constexpr int kWaves = 8;
 constexpr int kUnit = 512;  // of the reduction: 256 bytes of codes and 16 of scales a row
 
-__device__ __forceinline__ int row_slot(int r) { return (row_swizzle16(r) << 2) | (r & 3); }
+__device__ __forceinline__ int row_slot(int r) { return ((r & 3) << 2) | row_swizzle16(r); }
+
+// A unit's 16 scales of a row, as the lanes load them (lane group g: scales 4 g .. 4 g +
+// 3), to the form the MFMAs take: lane group g has scale 4 t + g in byte t.
+__device__ __forceinline__ uint32_t scales_by_mfma(uint32_t w, uint32_t select) {
+    // words 0 and 1, 2 and 3, in either half of the wave; then each in every lane group
+    const auto halves = __builtin_amdgcn_permlane32_swap(w, w, false, false);
+    const auto low = __builtin_amdgcn_permlane16_swap(halves[0], halves[0], false, false);
+    const auto high = __builtin_amdgcn_permlane16_swap(halves[1], halves[1], false, false);
+    // byte g of each
+    const uint32_t a = __builtin_amdgcn_perm(low[1], low[0], select), b = __builtin_amdgcn_perm(high[1], high[0], select);
+    return __builtin_amdgcn_perm(b, a, 0x05040100u);
+}
 
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t resource(const void* p, int size) {
     return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), 0, size, kBufferFlags);
@@ -64,6 +76,7 @@ __device__ __forceinline__ void run_tile(const Fp4Args& a, const ExpertRows& er,
     const uint8_t* const w_scales = a.b_scales + first_col * groups;
     const uint8_t* const x_scales = a.x_scales + first_row * groups;
 
+    const uint32_t select = (uint32_t)(0x0400 + 0x0101 * g);  // bytes g of two words, as v_perm_b32 names them
     u32x4_t code[P][MC][4];
     uint32_t scale[P][MC];
     // unit u of the reduction; columns past N, and the reduction past K, are zero
@@ -72,7 +85,7 @@ __device__ __forceinline__ void run_tile(const Fp4Args& a, const ExpertRows& er,
         for (int c = 0; c < MC; ++c) {
 #pragma unroll
             for (int t = 0; t < 4; ++t) {
-                const int byte = u * 256 + g * 64 + t * 16;
+                const int byte = u * 256 + t * 64 + g * 16;
                 code[p][c][t] = __builtin_amdgcn_raw_buffer_load_b128(
                     rw, byte < half ? (16 * c + r16) * half + byte : kOutOfRange, 0, 0);
             }
@@ -104,9 +117,13 @@ __device__ __forceinline__ void run_tile(const Fp4Args& a, const ExpertRows& er,
             if (row < kRows) *(u32x4_t*)(at + row * (NC * 256) + ((c ^ row_slot(row & 15)) << 4)) = xr[j];
         }
 #pragma unroll
-        for (int j = 0; j < SL; ++j) {
+        for (int j = 0; j < SL; ++j) {  // scale 4 t + g of a unit to byte t of word g
             const int q = j * 64 * kWaves + tid, row = q / (NC * 4), c = q % (NC * 4);
-            if (row < kRows) *(uint32_t*)(at + L::kCodes + row * L::kPitch + c * 4) = xs[j];
+            if (row < kRows) {
+                uint8_t* const to = at + L::kCodes + row * L::kPitch + c / 4 * 16 + c % 4;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) to[4 * i] = (uint8_t)(xs[j] >> (8 * i));
+            }
         }
     };
 
@@ -134,15 +151,18 @@ __device__ __forceinline__ void run_tile(const Fp4Args& a, const ExpertRows& er,
 #pragma unroll
             for (int n = 0; n < NT; ++n)
                 row_scale[n] = *(const uint32_t*)(x + L::kCodes + (16 * n + r16) * L::kPitch + u * 16 + g * 4);
+            uint32_t col_scale[MC];
+#pragma unroll
+            for (int c = 0; c < MC; ++c) col_scale[c] = scales_by_mfma(scale[p][c], select);
             const auto part = [&](auto tt) {
                 constexpr int t = decltype(tt)::value;
 #pragma unroll
                 for (int n = 0; n < NT; ++n) {
                     const u32x4_t v = *(const u32x4_t*)(x + (16 * n + r16) * (NC * 256) +
-                                                        ((16 * u + ((4 * g + t) ^ row_slot(r16))) << 4));
+                                                        ((16 * u + ((4 * t + g) ^ row_slot(r16))) << 4));
 #pragma unroll
                     for (int c = 0; c < MC; ++c)
-                        acc[n][c] = mfma_fp4<t, t>(code[p][c][t], v, acc[n][c], scale[p][c], row_scale[n]);
+                        acc[n][c] = mfma_fp4<t, t>(code[p][c][t], v, acc[n][c], col_scale[c], row_scale[n]);
                 }
             };
             part(std::integral_constant<int, 0>());
