@@ -48,8 +48,7 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t resource(const void* p, int si
 // a word a row, so that 16 rows' words lie in different banks).
 template <int TB, int S>
 struct Slice {
-    static constexpr int NC = TB == 16 && S == 8 ? 16 : TB == 32 && S == 4 ? 8 : 128 / TB;
-    static constexpr int B = NC / S;              // units of a wave group
+    static constexpr int B = 2, NC = B * S;       // units of a wave group, and of all
     static constexpr int kCodes = TB * NC * 256;  // bytes
     static constexpr int kPitch = NC * 16 + 4;    // scales of a row
     static constexpr int kBytes = kCodes + TB * kPitch;
@@ -60,7 +59,7 @@ template <int TB, int MC, int S, int NT>
 __device__ __forceinline__ void run_tile(const Fp4Args& a, const ExpertRows& er, int e, int m0, int rows, int n0,
                                          uint8_t* s_x) {
     using L = Slice<TB, S>;
-    constexpr int NC = L::NC, B = L::B, P = B > 1 ? 2 : 1;
+    constexpr int NC = L::NC, B = L::B, P = 2;  // P units ahead
     constexpr int kRows = NT * 16, XL = (kRows * NC * 16 + 64 * kWaves - 1) / (64 * kWaves);
     constexpr int SL = (kRows * NC * 4 + 64 * kWaves - 1) / (64 * kWaves);
     const int tid = threadIdx.x, lane = tid & 63, r16 = lane & 15, g = lane >> 4;
@@ -225,11 +224,12 @@ __global__ __launch_bounds__(64 * kWaves) void k_grouped_gemm_fp4_stream(Fp4Args
     const int rows = __builtin_amdgcn_readfirstlane(min(each, er.live - m0));
     const int n0 = __builtin_amdgcn_readfirstlane(local / nt_m * kCols);
     if (a.rows.zero_pad && m == nt_m - 1) clear_padding<kCols>(a.out, a.N, er, n0);
+    if (TB == 16) return run_tile<TB, MC, S, 1>(a, er, e, m0, rows, n0, s_x);
     switch ((rows + 15) / 16) {
         case 1: return run_tile<TB, MC, S, 1>(a, er, e, m0, rows, n0, s_x);
-        case 2: if (TB >= 32) return run_tile<TB, MC, S, TB >= 32 ? 2 : 1>(a, er, e, m0, rows, n0, s_x); break;
-        case 3: if (TB >= 64) return run_tile<TB, MC, S, TB >= 64 ? 3 : 1>(a, er, e, m0, rows, n0, s_x); break;
-        default: if (TB >= 64) return run_tile<TB, MC, S, TB >= 64 ? 4 : 1>(a, er, e, m0, rows, n0, s_x); break;
+        case 2: return run_tile<TB, MC, S, TB == 64 ? 2 : 1>(a, er, e, m0, rows, n0, s_x);
+        case 3: return run_tile<TB, MC, S, TB == 64 ? 3 : 1>(a, er, e, m0, rows, n0, s_x);
+        default: return run_tile<TB, MC, S, TB == 64 ? 4 : 1>(a, er, e, m0, rows, n0, s_x);
     }
 }
 
@@ -505,56 +505,69 @@ __global__ __launch_bounds__(512) void k_grouped_gemm_fp4(Fp4Args a) {
     }
 }
 
-template <int TB, int MC, int S>
+template <int TB, int S>
 hipError_t launch(const Fp4Args& a, int64_t pairs, hipStream_t stream) {
-    constexpr int kCols = 16 * MC * kWaves / S;
+    constexpr int kCols = 16 * kWaves / S;
     const int64_t blocks = max_row_tiles(a.rows, TB, pairs) * ((a.N + kCols - 1) / kCols);
     if (blocks > 0x7FFFFF) return hipErrorInvalidConfiguration;
     if (launch_debug())
         launch_debug_print("k_grouped_gemm_fp4_stream", dim3((unsigned)blocks), dim3(64 * kWaves),
                            "rows %d split %d n %d k %d", TB, S, a.N, a.K);
-    hipLaunchKernelGGL((k_grouped_gemm_fp4_stream<TB, MC, S>), dim3((unsigned)blocks), dim3(64 * kWaves), 0, stream, a);
+    hipLaunchKernelGGL((k_grouped_gemm_fp4_stream<TB, 1, S>), dim3((unsigned)blocks), dim3(64 * kWaves), 0, stream, a);
     return hipGetLastError();
 }
 
-// Parts of the reduction: it is split while that leaves about one block a CU (256 of
-// 8 waves), and only where every part keeps a unit. Never by the device's real CU
-// count: the order of the sums must not depend on it.
-int parts(const Fp4Args& a, int64_t pairs) {
-    const int64_t waves = (pairs < a.rows.E ? pairs : a.rows.E) * ((a.N + 15) / 16);
-    int split = waves >= 1536 ? 1 : waves >= 768 ? 2 : waves >= 384 ? 4 : 8;
-    while (split > 1 && a.K < kUnit * split) split /= 2;
-    return split;
+hipError_t launch_whole(const Fp4Args& a, int64_t pairs, hipStream_t stream) {
+    const int64_t blocks = max_row_tiles(a.rows, kTile, pairs) * ((a.N + kTile - 1) / kTile);
+    if (blocks > 0x7FFFFF) return hipErrorInvalidConfiguration;
+    if (launch_debug())
+        launch_debug_print("k_grouped_gemm_fp4", dim3((unsigned)blocks), dim3(512), "n %d k %d", a.N, a.K);
+    hipLaunchKernelGGL(k_grouped_gemm_fp4, dim3((unsigned)blocks), dim3(512), 0, stream, a);
+    return hipGetLastError();
 }
 
 }  // namespace
 
+// Which kernel, by the sizes and the alignment of the scales (never by the device's CU
+// count: the order of the sums must not depend on it). us:
+//   top-8 of 64 experts, 4096 x 7168, mean rows     4    8   10   16   24   32   64  128
+//     16 rows a tile                              187  194  204  253  320  379  641 1168
+//     whole tiles                                 191  193  193  194  197  199  214  247
+//   top-1 of 8 experts, 4096 x 7168 (128 whole tiles) 8   32   64  128
+//     64 rows                                        31   34   62   79
+//     whole tiles                                    41   42   47
+//   top-1 of 8 experts, 1536 x 2048 (48 whole tiles)  8   32   64  128  256
+//     16 rows, split 2                              7.0  9.4 16.4   27
+//     64 rows, split 2                                   7.5 12.2 14.4   27
+//     64 rows                                            9.8 11.4 11.6 17.5
+//     whole tiles                                  10.6 10.7 12.7 15.0 18.1
+// Whole tiles want the chip full; they take scales by DMA, whose rows have to be whole words.
 hipError_t launch_grouped_gemm_mxfp4_rows(const Fp4Args& a, int64_t pairs, hipStream_t stream) {
     if (pairs == 0) return hipSuccess;
-    const int64_t mean = (pairs + a.rows.E - 1) / a.rows.E;
-    if (mean > 20) {
-        // Whole tiles take their scales by DMA, which needs rows of whole words
-        const bool words = a.K % 128 == 0 && ((uintptr_t)a.x_scales | (uintptr_t)a.b_scales) % 4 == 0;
-        if (words && mean > 64) {
-            const int64_t blocks = max_row_tiles(a.rows, kTile, pairs) * ((a.N + kTile - 1) / kTile);
-            if (blocks > 0x7FFFFF) return hipErrorInvalidConfiguration;
-            if (launch_debug())
-                launch_debug_print("k_grouped_gemm_fp4", dim3((unsigned)blocks), dim3(512), "n %d k %d", a.N, a.K);
-            hipLaunchKernelGGL(k_grouped_gemm_fp4, dim3((unsigned)blocks), dim3(512), 0, stream, a);
-            return hipGetLastError();
+    const int64_t used = pairs < a.rows.E ? pairs : a.rows.E, mean = (pairs + used - 1) / used;
+    // Parts of the reduction of a tile: it is split while that leaves about one block a
+    // CU (256 of 8 waves), and only where every part keeps a unit. One token on 8, 4, 2, 1
+    // experts, 4096 x 7168: split 1, 2, 4, 8 take 27, 13.8, 9.7, 8.0 us, the next smaller one
+    // -, 19.8, 13.0, 9.1 us, the next larger -, 14.8, 14.6 us.
+    const auto parts = [&](int64_t row_tiles) {
+        const int64_t waves = row_tiles * used * ((a.N + 15) / 16);
+        int split = waves >= 1536 ? 1 : waves >= 768 ? 2 : waves >= 384 ? 4 : 8;
+        while (split > 1 && a.K < kUnit * split) split /= 2;
+        return split;
+    };
+    if (mean <= 6) {
+        switch (parts(1)) {
+            case 1: return launch<16, 1>(a, pairs, stream);
+            case 2: return launch<16, 2>(a, pairs, stream);
+            case 4: return launch<16, 4>(a, pairs, stream);
+            default: return launch<16, 8>(a, pairs, stream);
         }
-        return launch<64, 2, 1>(a, pairs, stream);
     }
-    const int split = parts(a, pairs);
-    if (mean > 6) {
-        if (split == 1) return launch<32, 2, 1>(a, pairs, stream);
-        if (split == 2) return launch<32, 1, 2>(a, pairs, stream);
-        return launch<32, 1, 4>(a, pairs, stream);
-    }
-    if (split == 1) return launch<16, 1, 1>(a, pairs, stream);
-    if (split == 2) return launch<16, 1, 2>(a, pairs, stream);
-    if (split == 4) return launch<16, 1, 4>(a, pairs, stream);
-    return launch<16, 1, 8>(a, pairs, stream);
+    const bool words = a.K % 128 == 0 && ((uintptr_t)a.x_scales | (uintptr_t)a.b_scales) % 4 == 0;
+    const int64_t tiles = (mean + kTile - 1) / kTile * used * ((a.N + kTile - 1) / kTile);
+    if (words && (tiles >= 192 || (mean > 48 && tiles >= 96) || mean > kTile)) return launch_whole(a, pairs, stream);
+    // an expert's rows scatter around their mean
+    return parts((mean + mean / 4 + 63) / 64) > 1 ? launch<64, 2>(a, pairs, stream) : launch<64, 1>(a, pairs, stream);
 }
 
 }  // namespace ep

@@ -74,6 +74,20 @@ def test_pairs(tokens):
     assert "pairs" in F.last_error_message()
 
 
+# tokens, top-k (1,024 experts), n, k, and the tiles of the header's rule: rows and columns of one
+@pytest.mark.parametrize("tokens,topk,n,k,rows,cols", [
+    (6 * 1024, 1, 5957 * 128 + 8, 64, 16, 128), (8 * 1024, 1, 7281 * 128 + 8, 32, 64, 128), (1 << 26, 16, 264, 128, 256, 256)])
+def test_tiles_of_a_launch(tokens, topk, n, k, rows, cols):
+    """The smallest width past the header's limit of 2^23 - 1 tiles."""
+    tiles = lambda w: (tokens * topk // rows + 1024) * -(-w // cols)
+    assert tiles(n) > (1 << 23) - 1 >= tiles(n - 8)
+    h = fake_handle(max_tokens=tokens, num_experts=1024, num_topk=topk)
+    h.num_tokens = tokens
+    f = F.lib().ep_grouped_gemm_mxfp4_rows
+    assert f(ctypes.byref(h), FAKE, FAKE, FAKE, FAKE, n, k, FAKE, None) == UNSUP
+    assert "tiles" in F.last_error_message()
+
+
 def test_reference_on_known_values():
     """The tests' own quantiser on values worked out by hand."""
     x = np.zeros((1, 32))

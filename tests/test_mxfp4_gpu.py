@@ -13,6 +13,8 @@ With scales far apart: one matrix instruction cuts each of its 128 products and 
 running sum off at 2^-23 of the largest of them, none of which exceeds
 S = sum |a b|, so ceil(K / 128) instructions (and the sum of up to 8 parts) are off by at most
 (129 ceil(K / 128) + 8) 2^-23 S; the bf16 output adds 2^-8 of its value."""
+import os
+
 import numpy as np
 import pytest
 import torch
@@ -206,12 +208,113 @@ def run_case(h, n, k, seed=0, **kw):
     return o, out
 
 
+EVERY = [0, 1, 2, 7, 8, 15, 16, 17, 31, 32, 33, 47, 48, 49, 63, 64, 65, 96, 127, 128, 129, 191, 192, 193, 255, 256, 257, 320, 511,
+         513]
+
+
 @pytest.mark.parametrize("A", [1, 16, 300])
 def test_every_count(A):
-    counts = [0, 1, 2, 7, 8, 15, 16, 17, 31, 32, 33, 47, 48, 49, 63, 64, 65, 96, 127, 128, 129, 191, 192, 193, 255, 256, 257,
-              320, 511, 513]
-    run_case(make_handle(routing(counts), len(counts), A), 264, 544)
-    run_case(make_handle(routing(counts), len(counts), A), 264, 640)
+    for k in (544, 640):
+        run_case(make_handle(routing(EVERY), len(EVERY), A), 264, k)
+
+
+def kernels(capfd, h, o, out):
+    """The kernels that a call launches, as the library says."""
+    os.environ["EP_BUFFER_DEBUG"] = "1"
+    try:
+        capfd.readouterr()
+        call(h, o, out)
+        return [l.split()[1] for l in capfd.readouterr().err.splitlines() if l.startswith("[ep]")]
+    finally:
+        os.environ.pop("EP_BUFFER_DEBUG", None)
+
+
+def run_whole(capfd, h, n, k, seed=0, **kw):
+    """A case that whole tiles take."""
+    o, out = run_case(h, n, k, seed, **kw)
+    assert kernels(capfd, h, o, out) == ["k_grouped_gemm_fp4"]
+    return o, out
+
+
+@pytest.mark.parametrize("A", [1, 16, 300])
+@pytest.mark.parametrize("k", [128, 640, 1024])
+def test_whole_tiles_every_count(capfd, A, k):
+    run_whole(capfd, make_handle(routing(EVERY), len(EVERY), A), 1032, k)
+
+
+@pytest.mark.parametrize("n,k", [(1032, 256), (1040, 384), (1024, 512), (1272, 896), (1280, 1152), (1032, 1408), (1536, 1664),
+                                 (1032, 2048), (1032, 3200), (2056, 7168)])
+def test_whole_tiles_sizes(capfd, n, k):
+    """Reductions that end anywhere in a step and in a slab of scales; widths off the tile."""
+    counts = [0, 5, 100, 64, 300, 1, 700, 2] * 3
+    run_whole(capfd, make_handle(routing(counts), len(counts), 1), n, k, seed=n + k)
+
+
+def test_whole_tiles_fixed_capacity_and_no_zero_pad(capfd):
+    counts = [0, 5, 130, 1, 39, 40, 700, 256] * 4
+    for C in (3, 40, 160, 600):
+        run_whole(capfd, make_handle(routing(counts), len(counts), 1, ops.MODE_FIXED, C), 1032, 640)
+    run_whole(capfd, make_handle(routing(counts), len(counts), 64, flags=ops.FLAG_NO_ZERO_PAD), 1032, 640)
+
+
+@pytest.mark.parametrize("k", [128, 384, 1152, 2048])
+def test_whole_tiles_nan_scales(capfd, k):
+    """A row's NaN scales stay out of the rows before and behind it, though its last slab's loads run on into the next row."""
+    counts = [70, 3, 260, 64] * 8
+    h = make_handle(routing(counts), len(counts), 1)
+    o = operands(h, 1032, k, seed=k)
+    for first, live, _ in o["rr"]:
+        o["s"][first + 1, 0] = 255
+        o["s"][first + 2, k // 32 - 1] = 255
+    o["t"][:, 1, 0] = 255
+    o["t"][:, 1029, k // 32 - 1] = 255
+    o["t"][:, 1031, k // 64] = 255
+    out = torch.full((h.cfg.recv_rows_bound(), 1032), 7.0, dtype=torch.bfloat16, device="cuda")
+    assert kernels(capfd, h, o, out) == ["k_grouped_gemm_fp4"]
+    for e, (f, n, _) in enumerate(o["rr"]):
+        x, w = decode_mxfp4(o["a"][f:f + n], o["s"][f:f + n]), decode_mxfp4(o["b"][e], o["t"][e])
+        rows, cols = (o["s"][f:f + n] == 255).any(1), (o["t"][e] == 255).any(1)
+        nan = rows[:, None] | cols[None, :]
+        assert torch.equal(torch.isnan(out[f:f + n]), nan), e
+        x[rows], w[cols] = 0, 0
+        assert torch.equal(out[f:f + n][~nan], (x @ w.t()).to(torch.bfloat16)[~nan]), e
+
+
+def test_whole_tiles_far_offsets(capfd):
+    """Codes past 2^32 bytes, under whole tiles."""
+    E, n, k = 160, 8192, 8192
+    rows = {0: 300, E - 2: 320, E - 1: 380}
+    h = make_handle(np.concatenate([np.full((c, 1), e, np.int64) for e, c in rows.items()]), E)
+    g = gen(2)
+    b = torch.zeros((E, n, k // 2), dtype=torch.uint8, device="cuda")
+    t = torch.zeros((E, n, k // 32), dtype=torch.uint8, device="cuda")
+    for e in rows:
+        b[e], t[e] = ops.quantize_mxfp4(torch.randn((n, k), generator=g, device="cuda"))
+    a, s = ops.quantize_mxfp4(torch.randn((1000, k), generator=g, device="cuda"))
+    o = dict(a=a, s=s, b=b, t=t)
+    out = torch.empty((1000, n), dtype=torch.bfloat16, device="cuda")
+    assert kernels(capfd, h, o, out) == ["k_grouped_gemm_fp4"]
+    for e, (first, live, _) in enumerate(ranges(h)):
+        if live:
+            x, w = decode_mxfp4(a[first:first + live], s[first:first + live]), decode_mxfp4(b[e], t[e])
+            want, acc = x @ w.t(), (129 * (k // 128) + 8) * 2.0 ** -23 * (x.abs() @ w.abs().t())
+            assert bool(((out[first:first + live].double() - want).abs() <= acc + 2.0 ** -8 * (want.abs() + acc)).all()), e
+
+
+@pytest.mark.parametrize("counts,n,k,want", [([1], 72, 4096, "rows 16 split 8"), ([2, 3], 4104, 4096, "rows 16 split 4"),
+                                             ([3] * 8, 1536, 2080, "rows 16 split 2"), ([5] * 16, 1600, 1024, "rows 16 split 1"),
+                                             ([40, 7], 520, 2080, "rows 64 split 2"), ([100, 9] * 4, 1600, 1440, "rows 64 split 1")])
+def test_streamed_splits(capfd, counts, n, k, want):
+    """Each tile height and split of the kernel that streams the weights."""
+    h = make_handle(routing(counts), len(counts), 1)
+    o, out = run_case(h, n, k)
+    os.environ["EP_BUFFER_DEBUG"] = "1"
+    try:
+        capfd.readouterr()
+        call(h, o, out)
+        assert want in capfd.readouterr().err
+    finally:
+        os.environ.pop("EP_BUFFER_DEBUG", None)
 
 
 @pytest.mark.parametrize("n,k", [(8, 32), (16, 64), (24, 96), (8, 1056), (1000, 32), (248, 160), (256, 256), (264, 224),
