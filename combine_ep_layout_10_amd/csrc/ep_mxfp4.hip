@@ -16,8 +16,13 @@ namespace ep {
 namespace {
 
 constexpr int kQuantWaves = 4;
-constexpr int kQuantAhead = 4;  // vectors of 8 that a lane has in flight
-constexpr int kQuantStretch = kWave * kQuantAhead;  // vectors of a wave's piece
+constexpr int64_t kQuantBlocks = 1 << 22;  // of a launch at most
+
+// Vectors of 8 that a lane has in flight: 65,536 rows of 7168 in bf16 with 1, 2, 3, 4, 8
+// take 243, 195, 203, 212, 217 us (1.19 GB: 6.1 TB/s); weights of 8 x 4096 x 4096 in binary32
+// with their values, with 1, 2, 4, 151, 153, 158 us (0.88 GB: 5.8 TB/s).
+template <bool F32>
+constexpr int kQuantAhead = F32 ? 1 : 2;
 
 template <int CTRL>
 __device__ __forceinline__ uint32_t max_with(uint32_t v) {
@@ -26,41 +31,45 @@ __device__ __forceinline__ uint32_t max_with(uint32_t v) {
 
 typedef __bf16 bf16x2_v __attribute__((ext_vector_type(2)));
 
-// Whether row `row` of the receive layout holds a pair.
-__device__ __forceinline__ bool row_is_live(const QuantArgs& a, int64_t row) {
-    if (a.rows.mode == EP_MODE_COMPACT) return row < a.rows.expert_off[a.rows.E] && a.row_src[row] >= 0;
-    return row % a.rows.C < a.rows.pad[row / a.rows.C];
+// A word that the whole wave reads, through the scalar cache.
+__device__ __forceinline__ int uniform(const int32_t* p, int64_t i) {
+    return *((const __attribute__((address_space(4))) int32_t*)(uintptr_t)p + i);
 }
 
-// F32: x binary32, otherwise bf16. ROWS: only rows that hold a pair (a row is cut into
-// pieces); otherwise the rows follow each other as one.
+// Whether row `row` of the receive layout holds a pair.
+__device__ __forceinline__ bool row_is_live(const QuantArgs& a, int row) {
+    if (a.rows.mode == EP_MODE_COMPACT) return row < uniform(a.rows.expert_off, a.rows.E) && uniform(a.row_src, row) >= 0;
+    return row % a.rows.C < uniform(a.rows.pad, row / a.rows.C);
+}
+
+// F32: x binary32, otherwise bf16. ROWS: only rows that hold a pair, each cut into
+// pieces; otherwise the rows follow each other as one. A piece's loads are sent without
+// a branch between them, lanes past the end at the last vector: with branches the
+// compiler waits for one before it sends the next (250 us for 195).
 template <bool F32, bool ROWS>
 __global__ __launch_bounds__(kWave * kQuantWaves) void k_quantize_mxfp4(QuantArgs a) {
+    constexpr int kAhead = kQuantAhead<F32>, kPiece = kWave * kAhead;  // vectors
     const int lane = lane_id();
-    const int64_t piece0 = (int64_t)blockIdx.x * kQuantWaves + (threadIdx.x >> 6);
-    for (int64_t piece = piece0; piece < a.pieces; piece += (int64_t)gridDim.x * kQuantWaves) {
-        int64_t base = 0;  // vectors
-        int64_t v0 = piece * kQuantStretch, end = a.vectors;
+    const int64_t step = (int64_t)gridDim.x * kQuantWaves, end = a.vectors;
+    int64_t piece = (int64_t)blockIdx.x * kQuantWaves + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    for (; piece < a.pieces; piece += step) {
+        int64_t base = 0, v0 = piece * kPiece;
         if (ROWS) {
             const int64_t row = piece / a.row_pieces;
-            if (!row_is_live(a, row)) continue;
+            if (!row_is_live(a, (int)row)) continue;
             base = row * a.vectors;
-            v0 = (piece - row * a.row_pieces) * kQuantStretch;
+            v0 = (piece - row * a.row_pieces) * kPiece;
         }
-        uint4 in[kQuantAhead][F32 ? 2 : 1];
+        uint4 in[kAhead][F32 ? 2 : 1];
 #pragma unroll
-        for (int i = 0; i < kQuantAhead; ++i) {
+        for (int i = 0; i < kAhead; ++i) {
             const int64_t v = v0 + i * kWave + lane;
-            if (v >= end) continue;
-            if (F32) {
-                in[i][0] = ((const uint4*)a.x)[2 * (base + v)];
-                in[i][F32 ? 1 : 0] = ((const uint4*)a.x)[2 * (base + v) + 1];
-            } else {
-                in[i][0] = ((const uint4*)a.x)[base + v];
-            }
+            const uint4* const from = (const uint4*)a.x + (F32 ? 2 : 1) * (base + (v < end ? v : end - 1));
+            in[i][0] = from[0];
+            if (F32) in[i][F32 ? 1 : 0] = from[1];
         }
 #pragma unroll
-        for (int i = 0; i < kQuantAhead; ++i) {
+        for (int i = 0; i < kAhead; ++i) {
             const int64_t v = v0 + i * kWave + lane;
             if (v >= end) continue;  // whole groups of four lanes
             const uint32_t* p = (const uint32_t*)&in[i][0];
@@ -111,11 +120,12 @@ __global__ __launch_bounds__(kWave * kQuantWaves) void k_quantize_mxfp4(QuantArg
 
 hipError_t launch_quantize_mxfp4(QuantArgs a, int64_t rows, int32_t k, bool live_rows, bool f32, hipStream_t stream) {
     if (rows == 0) return hipSuccess;
+    const int64_t piece = kWave * (f32 ? kQuantAhead<true> : kQuantAhead<false>);
     a.vectors = live_rows ? k / 8 : rows * (k / 8);
-    a.row_pieces = (a.vectors + kQuantStretch - 1) / kQuantStretch;
+    a.row_pieces = (a.vectors + piece - 1) / piece;
     a.pieces = live_rows ? rows * a.row_pieces : a.row_pieces;
-    const int64_t need = (a.pieces + kQuantWaves - 1) / kQuantWaves, most = 1 << 22;
-    const dim3 grid((unsigned)(need < most ? need : most)), block(kWave * kQuantWaves);
+    const int64_t need = (a.pieces + kQuantWaves - 1) / kQuantWaves;
+    const dim3 grid((unsigned)(need < kQuantBlocks ? need : kQuantBlocks)), block(kWave * kQuantWaves);
     if (launch_debug()) launch_debug_print("k_quantize_mxfp4", grid, block, "k %d f32 %d", k, (int)f32);
     if (live_rows) {
         if (f32) hipLaunchKernelGGL((k_quantize_mxfp4<true, true>), grid, block, 0, stream, a);
