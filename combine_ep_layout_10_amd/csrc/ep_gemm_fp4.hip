@@ -322,12 +322,12 @@ struct Sender {
 };
 
 __device__ __forceinline__ u32x4_t read_codes(uint32_t at) { return read_lds_words(at); }
-// The pairs of scales of rows 0 and 16 on from `at`, in a word.
-typedef uint16_t __attribute__((address_space(3), may_alias)) lds_u16_t;
-__device__ __forceinline__ uint32_t read_scales(uint32_t at) {
-    typedef uint16_t u16x2_t __attribute__((ext_vector_type(2)));
-    const u16x2_t v = {*(const lds_u16_t*)at, *(const lds_u16_t*)(at + 16 * kSlabRow)};
-    return __builtin_bit_cast(uint32_t, v);
+// The pairs of scales of rows 0 and 16 on from `at`, in a word: both rows' words with
+// one LDS read, of each the half that `select` names.
+typedef uint32_t __attribute__((address_space(3), may_alias)) lds_u32_t;
+__device__ __forceinline__ uint32_t read_scales(uint32_t at, uint32_t select) {
+    const uint32_t low = *(const lds_u32_t*)at, high = *(const lds_u32_t*)(at + 16 * kSlabRow);
+    return __builtin_amdgcn_perm(high, low, select);
 }
 
 // The loop of one group of waves over all steps.
@@ -336,16 +336,17 @@ __device__ __forceinline__ void multiply(const Sender<MI>& send, f32x4_t (&acc)[
     const int lane = lane_id(), r16 = lane & 15, g = lane >> 4;
     const int first = g == 0 ? 0 : g == 1 ? 6 : g == 2 ? 2 : 4;  // chunk of half 0
     const uint32_t row = r16 * kStepBytes + ((first ^ ((r16 >> 1) & 7)) << 4);
+    const uint32_t select = first & 2 ? 0x07060302u : 0x05040100u;
     const TileLds lds = send.lds;
     for (int kb = 0; kb < send.steps; ++kb) {
         const uint32_t at_a = lds.a(kb, SECOND ? 1 : 0) + row, at_b = lds.b(kb) + wn * 64 * kStepBytes + row;
-        const uint32_t at_s = lds.slab(kb / kSlabSteps) + r16 * kSlabRow + kb % kSlabSteps * 8 + first;
+        const uint32_t at_s = lds.slab(kb / kSlabSteps) + r16 * kSlabRow + kb % kSlabSteps * 8 + (first & 4);
         u32x4_t fa[2][2 * MI], fb[2][4];
         uint32_t sa[MI], sb[2];  // two pieces' pairs of scales a word
 #pragma unroll
-        for (int j = 0; j < 2; ++j) sb[j] = read_scales(at_s + (kTile + 64 * wn + 32 * j) * kSlabRow);
+        for (int j = 0; j < 2; ++j) sb[j] = read_scales(at_s + (kTile + 64 * wn + 32 * j) * kSlabRow, select);
 #pragma unroll
-        for (int i = 0; i < MI; ++i) sa[i] = read_scales(at_s + (64 * i + (SECOND ? 32 : 0)) * kSlabRow);
+        for (int i = 0; i < MI; ++i) sa[i] = read_scales(at_s + (64 * i + (SECOND ? 32 : 0)) * kSlabRow, select);
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
 #pragma unroll
