@@ -247,11 +247,12 @@ __global__ __launch_bounds__(64 * kWaves) void k_grouped_gemm_fp4_stream(Fp4Args
 // run, the other reads its operands from LDS, then a barrier exchanges the roles.
 // Group 0 reads step kb in interval 2 kb, group 1 in the next. The rows' slice is kept
 // in two halves, one for each group's pieces, since a half is free one interval after
-// its own group has read it:
-//   interval 2 kb      sends B of step kb + 1 (all waves),
-//   interval 2 kb + 1  group 1 sends its own half of A of step kb + 1, group 0 its own half
-//                      of A of step kb + 2; every fourth one the next slab.
-// What is sent has two intervals to land, and 128 KiB hold what would else take 160.
+// its own group has read it. With S steps in LDS,
+//   interval 2 kb      sends B of step kb + S - 1 (all waves),
+//   interval 2 kb + 1  group 1 sends its own half of A of step kb + S - 1, group 0 its own
+//                      half of A of step kb + S; every fourth one the next slab.
+// What is sent has 2 S - 2 intervals to land. S is 2, and 3 for tiles of up to 64 rows, which
+// wait for the weights (1,024 rows on 64 experts, 4096 x 7168: 177 us, with two steps 193).
 constexpr int kTile = 256;
 constexpr int kStepBytes = 128;                  // of a row: 256 codes
 constexpr int kHalfA = 128 * kStepBytes;         // bytes of a group's half of a slice of A
@@ -262,11 +263,18 @@ constexpr int kSlab = kSlabRows * kSlabRow;
 constexpr int kTileLds = 4 * kHalfA + 2 * kSliceB + 2 * kSlab;  // all of the CU's 160 KiB
 constexpr int kStoreLds = 4096;
 
+// LDS of a tile. MI: 32-row pieces of a wave; place: of a step, kb mod kSteps.
+template <int MI>
 struct TileLds {
+    static constexpr int kSteps = MI == 1 ? 3 : 2;
+    static constexpr int kHalf = MI == 1 ? kHalfA / 4 : kHalfA;
+    static_assert(kSteps * (2 * kHalf + kSliceB) <= 4 * kHalfA + 2 * kSliceB, "the slabs lie behind the steps");
     uint32_t base;
-    __device__ __forceinline__ uint32_t a(int kb, int half) const { return base + (2 * (kb & 1) + half) * kHalfA; }
-    __device__ __forceinline__ uint32_t b(int kb) const { return base + 4 * kHalfA + (kb & 1) * kSliceB; }
+    __device__ __forceinline__ uint32_t a(int place, int half) const { return base + (2 * place + half) * kHalf; }
+    __device__ __forceinline__ uint32_t b(int place) const { return base + 2 * kSteps * kHalf + place * kSliceB; }
     __device__ __forceinline__ uint32_t slab(int j) const { return base + 4 * kHalfA + 2 * kSliceB + (j & 1) * kSlab; }
+    // the place of the step d <= kSteps further on
+    __device__ __forceinline__ static int after(int place, int d) { return place + d >= kSteps ? place + d - kSteps : place + d; }
 };
 
 // What a wave sends. MI: 32-row pieces of a wave.
@@ -278,7 +286,7 @@ struct Sender {
     int steps;
     uint32_t off_a[MI], off_b[4], off_s;
     int w;
-    TileLds lds;
+    TileLds<MI> lds;
 
     __device__ __forceinline__ void init(const Fp4Args& g, int64_t first_row, int64_t first_col, int n_rows, int n_cols) {
         const int lane = lane_id(), pos = lane & 7;
@@ -304,13 +312,13 @@ struct Sender {
         s_rows = max(0, min(64, (of_b ? cols : rows) - r0));
         off_s = __umul24(lane >> 1, groups) + 16 * (lane & 1);
     }
-    __device__ __forceinline__ void send_a(int kb, int j) const {
+    __device__ __forceinline__ void send_a(int kb, int place, int j) const {
         dma16(a + (int64_t)kb * kStepBytes, kb < steps ? rows * half - kb * kStepBytes : 0, off_a[j],
-              lds.a(kb, w >> 2) + ((w & 3) * MI + j) * 1024);
+              lds.a(place, w >> 2) + ((w & 3) * MI + j) * 1024);
     }
-    __device__ __forceinline__ void send_b(int kb, int j) const {
+    __device__ __forceinline__ void send_b(int kb, int place, int j) const {
         dma16(b + (int64_t)kb * kStepBytes, kb < steps ? cols * half - kb * kStepBytes : 0, off_b[j],
-              lds.b(kb) + (4 * w + j) * 1024);
+              lds.b(place) + (4 * w + j) * 1024);
     }
     // slab j: steps 4 j .. 4 j + 3; a load takes 32 rows
     __device__ __forceinline__ void send_slab(int j) const {
@@ -337,9 +345,12 @@ __device__ __forceinline__ void multiply(const Sender<MI>& send, f32x4_t (&acc)[
     const int first = g == 0 ? 0 : g == 1 ? 6 : g == 2 ? 2 : 4;  // chunk of half 0
     const uint32_t row = r16 * kStepBytes + ((first ^ ((r16 >> 1) & 7)) << 4);
     const uint32_t select = first & 2 ? 0x07060302u : 0x05040100u;
-    const TileLds lds = send.lds;
-    for (int kb = 0; kb < send.steps; ++kb) {
-        const uint32_t at_a = lds.a(kb, SECOND ? 1 : 0) + row, at_b = lds.b(kb) + wn * 64 * kStepBytes + row;
+    using Lds = TileLds<MI>;
+    constexpr int S = Lds::kSteps, kMore = (S - 2) * (4 + MI);  // loads that may be on their way beside those of two steps
+    const Lds lds = send.lds;
+    int place = 0;
+    for (int kb = 0; kb < send.steps; ++kb, place = Lds::after(place, 1)) {
+        const uint32_t at_a = lds.a(place, SECOND ? 1 : 0) + row, at_b = lds.b(place) + wn * 64 * kStepBytes + row;
         const uint32_t at_s = lds.slab(kb / kSlabSteps) + r16 * kSlabRow + kb % kSlabSteps * 8 + (first & 4);
         u32x4_t fa[2][2 * MI], fb[2][4];
         uint32_t sa[MI], sb[2];  // two pieces' pairs of scales a word
@@ -357,14 +368,14 @@ __device__ __forceinline__ void multiply(const Sender<MI>& send, f32x4_t (&acc)[
         const bool slab = kb % kSlabSteps == 0;  // interval 2 kb + 1 sends the next slab
         if (SECOND) {  // interval 2 kb + 1
 #pragma unroll
-            for (int j = 0; j < MI; ++j) send.send_a(kb + 1, j);
+            for (int j = 0; j < MI; ++j) send.send_a(kb + S - 1, Lds::after(place, S - 1), j);
             if (slab) send.send_slab(kb / kSlabSteps + 1);
             // B of step kb + 1 has landed, and all before it
-            if (slab) wait_vmcnt<MI + 2>();
-            else wait_vmcnt<MI>();
+            if (slab) wait_vmcnt<MI + kMore + 2>();
+            else wait_vmcnt<MI + kMore>();
         } else {  // interval 2 kb
 #pragma unroll
-            for (int j = 0; j < 4; ++j) send.send_b(kb + 1, j);
+            for (int j = 0; j < 4; ++j) send.send_b(kb + S - 1, Lds::after(place, S - 1), j);
         }
         wait_lgkmcnt0();
         block_barrier();
@@ -384,11 +395,11 @@ __device__ __forceinline__ void multiply(const Sender<MI>& send, f32x4_t (&acc)[
                 if (SECOND) {  // interval 2 kb + 2
 #pragma unroll
                     for (int d = 0; d < 4; ++d)
-                        if (d * 2 * MI / 4 == h * MI + i) send.send_b(kb + 2, d);
+                        if (d * 2 * MI / 4 == h * MI + i) send.send_b(kb + S, place, d);
                 } else {  // interval 2 kb + 1
 #pragma unroll
                     for (int d = 0; d < MI; ++d)
-                        if (d * 2 == h * MI + i) send.send_a(kb + 2, d);
+                        if (d * 2 == h * MI + i) send.send_a(kb + S, place, d);
                     if (i == MI - 1 && h == 1 && slab) send.send_slab(kb / kSlabSteps + 1);
                 }
 #pragma unroll
@@ -408,10 +419,10 @@ __device__ __forceinline__ void multiply(const Sender<MI>& send, f32x4_t (&acc)[
         part(std::integral_constant<int, 1>());
         __builtin_amdgcn_s_setprio(0);
         if (SECOND) {  // this group's half of A of step kb + 1 has landed
-            wait_vmcnt<4>();
+            wait_vmcnt<4 + kMore>();
         } else {  // B of step kb + 1 has landed, and all before it
-            if (slab) wait_vmcnt<MI + 2>();
-            else wait_vmcnt<MI>();
+            if (slab) wait_vmcnt<MI + kMore + 2>();
+            else wait_vmcnt<MI + kMore>();
         }
         block_barrier();
     }
@@ -435,17 +446,21 @@ __device__ __forceinline__ void run_whole(const Fp4Args& a, const ExpertRows& er
     for (int i = 0; i < 2 * MI; ++i)
 #pragma unroll
         for (int j = 0; j < 4; ++j) acc[i][j] = (f32x4_t){0.0f, 0.0f, 0.0f, 0.0f};
-    // ahead of interval 0: slab 0, B and A of step 0, group 0's half of A of step 1
+    // ahead of interval 0: slab 0, B and A of all steps but one, and group 0's half of A of that
+    constexpr int S = TileLds<MI>::kSteps, kMore = (S - 2) * (4 + MI);
     send.send_slab(0);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) send.send_b(0, j);
+    for (int kb = 0; kb < S - 1; ++kb) {
 #pragma unroll
-    for (int j = 0; j < MI; ++j) send.send_a(0, j);
+        for (int j = 0; j < 4; ++j) send.send_b(kb, kb, j);
+#pragma unroll
+        for (int j = 0; j < MI; ++j) send.send_a(kb, kb, j);
+    }
     if (wm == 0) {
 #pragma unroll
-        for (int j = 0; j < MI; ++j) send.send_a(1, j);
+        for (int j = 0; j < MI; ++j) send.send_a(S - 1, S - 1, j);
     }
-    wait_vmcnt<MI>();  // group 1's half may still be on its way
+    wait_vmcnt<MI + kMore>();  // group 1's half of step 0 may still be on its way
     block_barrier();
     const int groups = a.K / 32;
     if (wm == 0) {
@@ -453,8 +468,8 @@ __device__ __forceinline__ void run_whole(const Fp4Args& a, const ExpertRows& er
         block_barrier();
     } else {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) send.send_b(1, j);
-        wait_vmcnt<4>();
+        for (int j = 0; j < 4; ++j) send.send_b(S - 1, S - 1, j);
+        wait_vmcnt<4 + kMore>();
         block_barrier();  // half a step later
         multiply<true, MI>(send, acc, wn, groups);
     }
@@ -531,18 +546,24 @@ hipError_t launch_whole(const Fp4Args& a, int64_t pairs, hipStream_t stream) {
 
 // Which kernel, by the sizes and the alignment of the scales (never by the device's CU
 // count: the order of the sums must not depend on it). us:
-//   top-8 of 64 experts, 4096 x 7168, mean rows     4    8   10   16   24   32   64  128
-//     16 rows a tile                              187  194  204  253  320  379  641 1168
-//     whole tiles                                 191  193  193  194  197  199  214  247
-//   top-1 of 8 experts, 4096 x 7168 (128 whole tiles) 8   32   64  128
-//     64 rows                                        31   34   62   79
-//     whole tiles                                    41   42   47
-//   top-1 of 8 experts, 1536 x 2048 (48 whole tiles)  8   32   64  128  256
-//     16 rows, split 2                              7.0  9.4 16.4   27
-//     64 rows, split 2                                   7.5 12.2 14.4   27
-//     64 rows                                            9.8 11.4 11.6 17.5
-//     whole tiles                                  10.6 10.7 12.7 15.0 18.1
-// Whole tiles want the chip full; they take scales by DMA, whose rows have to be whole words.
+//   top-8 of 64 experts, 4096 x 7168, mean rows       1    2    4    6    8   16   32   64  128
+//     16 rows a tile                                127  171  187  190  194  253  380  642 1171
+//     64 rows                                       127  172  187  190  194  201  210  293  440
+//     whole tiles                                   119  160  171  174  176  178  182  216  245
+//   top-1 of 32 experts, 4096 x 4096 (512 whole tiles)
+//     16 rows                                      40.6 52.3 55.9      57.8 75.8  111  195
+//     whole tiles                                  44.4 47.7 52.7      55.8 56.6 59.5 68.7
+//   top-1 of 8 experts, 4096 x 7168 (128 whole tiles)
+//     16 rows                                      21.7      26.0      26.7 44.6 59.4 92.1  158
+//     64 rows                                      21.8      26.2      26.8 27.8 29.7 54.3 71.2
+//     whole tiles                                  26.4      30.9      31.3 32.0 33.7 47.4 52.3
+//   top-1 of 8 experts, 1536 x 2048 (48 whole tiles)
+//     16 rows, split 2                                        6.8       6.9       9.4 16.4 27.1
+//     64 rows, split 2                                        7.0       7.0       7.6 12.2 14.4
+//     64 rows                                                 8.8       8.8       9.8 11.4 11.6
+//     whole tiles                                             9.5       9.5       9.7 12.7 15.0
+// Whole tiles want the chip full, which a row an expert, met by chance, does not tell; they
+// take scales by DMA, whose rows have to be whole words.
 hipError_t launch_grouped_gemm_mxfp4_rows(const Fp4Args& a, int64_t pairs, hipStream_t stream) {
     if (pairs == 0) return hipSuccess;
     const int64_t used = pairs < a.rows.E ? pairs : a.rows.E, mean = (pairs + used - 1) / used;
@@ -556,6 +577,10 @@ hipError_t launch_grouped_gemm_mxfp4_rows(const Fp4Args& a, int64_t pairs, hipSt
         while (split > 1 && a.K < kUnit * split) split /= 2;
         return split;
     };
+    const bool words = a.K % 128 == 0 && ((uintptr_t)a.x_scales | (uintptr_t)a.b_scales) % 4 == 0;
+    const int64_t tiles = (mean + kTile - 1) / kTile * used * ((a.N + kTile - 1) / kTile);
+    if (words && ((mean > 1 && tiles >= 192) || (mean > 48 && tiles >= 96) || mean > kTile))
+        return launch_whole(a, pairs, stream);
     if (mean <= 6) {
         switch (parts(1)) {
             case 1: return launch<16, 1>(a, pairs, stream);
@@ -564,9 +589,6 @@ hipError_t launch_grouped_gemm_mxfp4_rows(const Fp4Args& a, int64_t pairs, hipSt
             default: return launch<16, 8>(a, pairs, stream);
         }
     }
-    const bool words = a.K % 128 == 0 && ((uintptr_t)a.x_scales | (uintptr_t)a.b_scales) % 4 == 0;
-    const int64_t tiles = (mean + kTile - 1) / kTile * used * ((a.N + kTile - 1) / kTile);
-    if (words && (tiles >= 192 || (mean > 48 && tiles >= 96) || mean > kTile)) return launch_whole(a, pairs, stream);
     // an expert's rows scatter around their mean
     return parts((mean + mean / 4 + 63) / 64) > 1 ? launch<64, 2>(a, pairs, stream) : launch<64, 1>(a, pairs, stream);
 }
