@@ -228,6 +228,7 @@ struct RouteArgs {
     float* w;
     int T, E, k, G, keep, best, score, renormalize, idx_bits, f32;
     int group_lanes;  // lanes of a group where that is a power of two of whole lanes, else 0 (the launcher's)
+    int narrow;       // keys of scores are tried in binary32 first (the launcher's)
     float scale;
 };
 

@@ -6,9 +6,13 @@
 //
 // Order: a key (a binary32 logit, or a binary64 score + bias) is held as an
 // unsigned integer that orders as the number does, 0 for an expert that may not
-// be chosen. A binary64 key's halves are compared one after the other: the
-// higher one decides unless two experts share it. A round takes the highest key
-// of the wave, its lowest index, and clears it.
+// be chosen. A round takes the highest key of the wave and clears it. Where binary32 keys
+// decide a choice of scores they are taken for it; where 64 bits are needed, a key's halves are
+// compared one after the other: the higher one decides unless two experts share it.
+//
+// Bound by instructions, and for few tokens by the launches. 8192 tokens x 256 experts in
+// binary32, us: choice (sigmoid, bias, 4 of 8 groups) 8.9, loss 13.1 (two launches), gradient
+// of both 7.6; the logits alone take 1.4 us to read (6.1 TB/s). 128 tokens: choice 4.0.
 #include <type_traits>
 
 #include "ep_internal.h"
@@ -162,6 +166,13 @@ __device__ __forceinline__ float score_terms(int score, const float l[V], float 
     return wave_sum(sum);
 }
 
+// Orders the LDS accesses of a wave's lanes for the compiler; the hardware keeps them
+// in order.
+__device__ __forceinline__ void wave_lds_fence() {
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+}
+
 // ---------------------------------------------------------------- choice
 
 // The highest of the wave's keys with its lowest index, which is cleared; false
@@ -298,9 +309,179 @@ __device__ __forceinline__ void keep_groups(const RouteArgs& a, int lane, uint32
         if (!((kept >> min((lane * V + v) / size, 63)) & 1)) hi[v] = 0u;
 }
 
-// FULL: keys are scores + bias in binary64, otherwise logits.
+// The choice from binary32 keys, where they decide it. Scores: each is off by at most
+// `err`, and every comparison that the choice rests on has to be clearer than what its two
+// sides can be off by. Where a group's is not: false, and keys of 64 bits choose. Where an
+// expert's is not (among them any tie), those that may be chosen are ranked by their keys
+// of 64 bits, one a lane; false with a softmax, whose scores take the whole row. Otherwise
+// (SCORES false) the keys are the logits. Lane j < k gets the j-th choice and its score (or
+// logit); `out`: the wave's LDS. About one token in 1,000 has an unclear choice (sigmoids of 256
+// logits, top-8), and a wave that takes both ways ends late. 8192 tokens, us, with this
+// first and without it: sigmoids and a bias, 256 experts in 8 groups 8.9, 12.0; 384 experts
+// 12.1, 17.3; softmax and a bias, 160 experts 9.1, 10.3; logits, 1024 experts 16.8, 23.7, 256
+// of them 8.1, 8.9; but of 128 experts 7.2, 6.9, with softmax and a bias (4096 tokens) 6.2,
+// 5.7, with sigmoids 6.8, 7.5, and 64 5.2, 4.9: so from 4 experts a lane on.
+constexpr int kNarrowFrom = 4;
+
+struct Choice {
+    int e;
+    float s;
+};
+
+// Descending (Batcher's odd-even merges).
+template <int V>
+__device__ __forceinline__ void sort_down(uint32_t h[V]) {
+#pragma unroll
+    for (int p = 1; p < V; p *= 2)
+#pragma unroll
+        for (int d = p; d >= 1; d /= 2)
+#pragma unroll
+            for (int i = d % p; i + d < V; ++i) {
+                if ((i - d % p) % (2 * d) >= d || i / (2 * p) != (i + d) / (2 * p)) continue;
+                const uint32_t x = h[i], y = h[i + d];
+                h[i] = max(x, y);
+                h[i + d] = min(x, y);
+            }
+}
+
+__device__ __forceinline__ double score64(float l) { return 1.0 / (1.0 + exp(-(double)l)); }
+
+template <int V, bool SCORES>
+__device__ __forceinline__ bool choose_narrow(const RouteArgs& a, int lane, const float l[V], const float s[V],
+                                              const float b[V], const bool open[V], float err, Choice* out,
+                                              Choice* mine) {
+    constexpr float kUnit = 5.9604645e-8f;    // 2^-24
+    constexpr uint32_t kLeast = 0x00400000u;  // half of ordered(kLowest): what lies below is no key
+    uint32_t h[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+        const float key = SCORES ? s[v] + b[v] : s[v];
+        h[v] = open[v] ? ordered(key >= kLowest ? key : kLowest) : 0u;
+    }
+    if (a.G > 1) {
+        const int lanes = a.group_lanes;
+        uint32_t first = 0, second = 0;
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            second = max(second, min(first, h[v]));
+            first = max(first, h[v]);
+        }
+        const auto merge = [&](uint32_t f, uint32_t n) {
+            second = max(max(second, n), min(first, f));
+            first = max(first, f);
+        };
+        if (lanes > 1) merge(dpp<0xB1>(first), dpp<0xB1>(second));
+        if (lanes > 2) merge(dpp<0x4E>(first), dpp<0x4E>(second));
+        if (lanes > 4) merge(dpp<0x141>(first), dpp<0x141>(second));
+        if (lanes > 8) merge(dpp<0x140>(first), dpp<0x140>(second));
+        if (lanes > 16) merge(__shfl_xor(first, 16, kWave), __shfl_xor(second, 16, kWave));
+        if (lanes > 32) merge(__shfl_xor(first, 32, kWave), __shfl_xor(second, 32, kWave));
+        // two keys, each off by its score's error and a unit; a unit of their sum, one of each end
+        const bool two = a.best > 1 && second != 0;
+        const float f = unordered(first), n = two ? unordered(second) : 0.0f;
+        const float off = SCORES ? 2.0f * err + 4.0f * kUnit * (fabsf(f) + fabsf(n)) : 0.0f;
+        const float low = first != 0 ? (f + n) - off : -__builtin_inff(), high = first != 0 ? (f + n) + off : -__builtin_inff();
+        // groups that come first for sure, and that may; each lane of a group asks about one
+        int before = 0, maybe = 0;
+        const int at_group = lane & (lanes - 1), base = lane - at_group;
+        const uint64_t own = lanes < 64 ? (1ull << lanes) - 1 : ~0ull;
+        for (int g0 = 0; g0 < a.G; g0 += lanes) {
+            const int g = g0 + at_group, at = min(g, a.G - 1) * lanes;
+            const float other_low = __shfl(low, at, kWave), other_high = __shfl(high, at, kWave);
+            const bool other = g < a.G && at != base;
+            const uint64_t ahead = ballot64(other && (other_low > high || (!SCORES && other_low == high && at < base)));
+            before += __popcll((ahead >> base) & own);
+            if (SCORES) maybe += __popcll((ballot64(other && !(other_high < low)) >> base) & own);
+            else maybe = before;
+        }
+        if (ballot64(first != 0 && maybe >= a.keep && before < a.keep) != 0) return false;
+#pragma unroll
+        for (int v = 0; v < V; ++v) h[v] = maybe < a.keep ? h[v] : 0u;
+    }
+    // A key's lowest bits make way for the expert's place in its lane, which moves it by less
+    // than V units of its last place (two units 2^-24 each, at most); those of a bf16 logit
+    // hold nothing, and make way for its whole index, counted down. Each lane's keys are
+    // sorted; a round takes the highest of the lanes' first ones.
+    const bool exact = !SCORES && !a.f32;
+    const float unit = (2 * V + 2) * kUnit;
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+        if (exact) {
+            const uint32_t key = s[v] == s[v] ? h[v] : h[v] / 2;  // NaN lies below the lowest bf16 number, too
+            h[v] = (key & 0xFFFF0000u) | (uint32_t)(0xFFFF - (lane * V + v));
+        } else {
+            h[v] = (h[v] & ~(uint32_t)(V - 1)) | (uint32_t)(V - 1 - v);
+        }
+    }
+    sort_down<V>(h);
+    uint32_t best = 0, chosen = 0;  // lane j: the j-th key, its expert
+    const auto take = [&](int n) -> uint32_t {
+        const uint32_t m = wave_max(h[0]);
+        if (m < kLeast) return 0;
+        const int from = __builtin_ctzll(ballot64(h[0] == m));
+        const bool now = lane == n, here = lane == from;
+        best = now ? m : best;
+        const uint32_t e = exact ? 0xFFFF - (m & 0xFFFF) : (uint32_t)from * V + (V - 1 - (m & (V - 1)));
+        chosen = now ? e : chosen;
+#pragma unroll
+        for (int v = 0; v < V - 1; ++v) h[v] = here ? h[v + 1] : h[v];
+        h[V - 1] = here ? 0u : h[V - 1];
+        return m;
+    };
+    // whether the higher key of two may be the lower one in truth
+    const auto unclear = [&](float x, float y) { return !(x - y > 2.0f * err + unit * (fabsf(x) + fabsf(y))); };
+    int n = 0;  // the first one that is not chosen is looked at, too
+    while (n < a.k + (exact ? 0 : 1) && take(n) != 0) ++n;
+    const uint32_t next = __shfl(best, (lane + 1) & (kWave - 1), kWave);
+    const bool close = !exact && lane < a.k && next != 0 && unclear(unordered(best), unordered(next));
+    int place = lane;
+    if (ballot64(close) != 0) {
+        if (SCORES && a.score == EP_SCORE_SOFTMAX) return false;
+        // all that may belong to the first k
+        const float last = unordered(lane_value(best, a.k - 1));
+        while (n > a.k && unclear(last, unordered(lane_value(best, n - 1)))) {
+            if (n == kWave) return false;
+            if (take(n) == 0) break;
+            ++n;
+        }
+        float x = 0.0f, y = 0.0f;
+        const int at = (int)chosen;
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            const float lv = __shfl(l[v], at / V, kWave), bv = SCORES ? __shfl(b[v], at / V, kWave) : 0.0f;
+            x = v == at % V ? lv : x;
+            y = v == at % V ? bv : y;
+        }
+        double key = SCORES ? score64(x) + (double)y : (double)x;
+        if (!(key >= kLowest64)) key = kLowest64;  // NaN
+        place = 0;
+        for (int i = 0; i < n; ++i) {
+            const double other = lane_value(key, i);
+            const int e = (int)lane_value(chosen, i);
+            place += other > key || (other == key && e < at);
+        }
+    }
+    // the scores from the lanes that hold them
+    float score = 0.0f;
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+        const float x = __shfl(s[v], (int)chosen / V, kWave);
+        score = v == (int)chosen % V ? x : score;
+    }
+    if (ballot64(close) == 0) {
+        if (lane < min(n, a.k)) *mine = Choice{(int)chosen, score};
+        return true;
+    }
+    if (lane < n && place < a.k) out[place] = Choice{(int)chosen, score};
+    wave_lds_fence();
+    if (lane < min(n, a.k)) *mine = out[lane];
+    return true;
+}
+
+// FULL: keys are scores + bias, in binary64 where binary32 does not decide; otherwise logits.
 template <int V, bool FULL>
 __global__ __launch_bounds__(64 * kRouteWaves) void k_route(RouteArgs a) {
+    __shared__ Choice s_choice[kRouteWaves][kMaxTopk];
     const int lane = lane_id();
     const int t = __builtin_amdgcn_readfirstlane(blockIdx.x * kRouteWaves + (threadIdx.x >> 6));
     if (t >= a.T) return;
@@ -309,62 +490,86 @@ __global__ __launch_bounds__(64 * kRouteWaves) void k_route(RouteArgs a) {
     if (a.mask == nullptr || a.mask[t] != 0) {
         float l[V], s[V];
         load_logits<V>(a.logits, a.f32, t, a.E, lane, l);
-        uint32_t hi[V], lo[V];
         float max_l = 0.0f, sum = 1.0f;
-        if (FULL) {
-            double score[V];
-            if (a.score == EP_SCORE_SOFTMAX) {
-                const double m = (double)wave_max_logit<V>(l);
-                double d = 0.0;
-#pragma unroll
-                for (int v = 0; v < V; ++v) {
-                    score[v] = l[v] == -__builtin_inff() ? 0.0 : exp((double)l[v] - m);
-                    d += score[v];
-                }
-                d = wave_sum(d);
-#pragma unroll
-                for (int v = 0; v < V; ++v) score[v] /= d;
-            } else {
-#pragma unroll
-                for (int v = 0; v < V; ++v) score[v] = 1.0 / (1.0 + exp(-(double)l[v]));
-            }
-#pragma unroll
-            for (int v = 0; v < V; ++v) {
-                const int e = lane * V + v;
-                const float b = a.bias != nullptr && e < a.E ? a.bias[e] : 0.0f;
-                double key = score[v] + (double)b;
-                if (!(key >= kLowest64)) key = kLowest64;  // NaN
-                const bool open = l[v] != -__builtin_inff() && b != -__builtin_inff();
-                const uint64_t o = open ? ordered(key) : 0ull;
-                hi[v] = (uint32_t)(o >> 32);
-                lo[v] = (uint32_t)o;
-                s[v] = (float)score[v];
-            }
-        } else {
-            if (a.score == EP_SCORE_SOFTMAX) {
-                float x[V];
-                max_l = wave_max_logit<V>(l);
-                sum = softmax_terms<V>(l, max_l, x);
-            }
-#pragma unroll
-            for (int v = 0; v < V; ++v) {
-                hi[v] = l[v] == -__builtin_inff() ? 0u : ordered(l[v] >= kLowest ? l[v] : kLowest);
-                s[v] = l[v];
-            }
+        Choice mine = {-1, 0.0f};
+        const bool narrow = V >= kNarrowFrom && a.narrow;
+        if (a.score == EP_SCORE_SOFTMAX) {
+            max_l = wave_max_logit<V>(l);
+            if (!FULL || narrow) sum = softmax_terms<V>(l, max_l, s);
         }
-        if (a.G > 1) keep_groups<V, FULL>(a, lane, hi, lo);
-        for (int j = 0; j < a.k; ++j) {
-            Taken p;
-            if (!take_highest<V, FULL>(hi, lo, &p)) break;
-            chosen = lane == j ? p.lane * V + p.v : chosen;
+        float b[V], err = 1e-37f;  // of logits: for those around 0, whose units are no part of them
+        bool open[V];
+        if (FULL && narrow && a.score == EP_SCORE_SOFTMAX) {
+            // The weighted mean of max l - l, which the arguments' roundings count with, is at
+            // most log 1024, and x e^-x less than 0.4: in units 2^-24 of the largest score, a
+            // term is off by 5, the sum by 7 + 4 + 22, the quotients by 3.
+            const float inv = 1.0f / sum;
+#pragma unroll
+            for (int v = 0; v < V; ++v) s[v] *= inv;
+            err = 3.8146973e-6f * inv;  // 64 units
+        } else if (FULL && narrow) {
+            float slope;
+#pragma unroll
+            for (int v = 0; v < V; ++v) s[v] = sigmoid(l[v], &slope);
+            err = 3.5762787e-7f;  // 6 units: 10 of a score below a half, 5 of the others
         }
-        // the chosen experts' scores (or logits) from the lanes that hold them
-        const int at = chosen >= 0 ? chosen : 0;
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-            const float x = __shfl(s[v], at / V, kWave);
-            w = chosen >= 0 && v == at % V ? x : w;
+            const int e = lane * V + v;
+            b[v] = FULL && a.bias != nullptr && e < a.E ? a.bias[e] : 0.0f;
+            open[v] = l[v] != -__builtin_inff() && b[v] != -__builtin_inff();
+            if (!FULL) s[v] = l[v];
         }
+        bool decided = false;
+        if (narrow)
+            decided = choose_narrow<V, FULL>(a, lane, l, s, b, open, err, s_choice[threadIdx.x >> 6], &mine);
+        if (!decided) {
+            uint32_t hi[V], lo[V];
+            if (FULL) {
+                double score[V];
+                if (a.score == EP_SCORE_SOFTMAX) {
+                    double d = 0.0;
+#pragma unroll
+                    for (int v = 0; v < V; ++v) {
+                        score[v] = l[v] == -__builtin_inff() ? 0.0 : exp((double)l[v] - (double)max_l);
+                        d += score[v];
+                    }
+                    d = wave_sum(d);
+#pragma unroll
+                    for (int v = 0; v < V; ++v) score[v] /= d;
+                } else {
+#pragma unroll
+                    for (int v = 0; v < V; ++v) score[v] = score64(l[v]);
+                }
+#pragma unroll
+                for (int v = 0; v < V; ++v) {
+                    double key = score[v] + (double)b[v];
+                    if (!(key >= kLowest64)) key = kLowest64;  // NaN
+                    if (!narrow) s[v] = (float)score[v];
+                    const uint64_t o = open[v] ? ordered(key) : 0ull;
+                    hi[v] = (uint32_t)(o >> 32);
+                    lo[v] = (uint32_t)o;
+                }
+            } else {
+#pragma unroll
+                for (int v = 0; v < V; ++v) hi[v] = open[v] ? ordered(l[v] >= kLowest ? l[v] : kLowest) : 0u;
+            }
+            if (a.G > 1) keep_groups<V, FULL>(a, lane, hi, lo);
+            for (int j = 0; j < a.k; ++j) {
+                Taken p;
+                if (!take_highest<V, FULL>(hi, lo, &p)) break;
+                mine.e = lane == j ? p.lane * V + p.v : mine.e;
+            }
+            // the chosen experts' scores (or logits) from the lanes that hold them
+            const int at = max(mine.e, 0);
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                const float x = __shfl(s[v], at / V, kWave);
+                mine.s = mine.e >= 0 && v == at % V ? x : mine.s;
+            }
+        }
+        chosen = mine.e;
+        w = mine.s;
         if (!FULL && chosen >= 0) {
             float slope;
             w = a.score == EP_SCORE_SOFTMAX ? exp_negative(w - max_l) / sum : sigmoid(w, &slope);
@@ -579,13 +784,6 @@ __global__ __launch_bounds__(1024) void k_balance_loss(BalanceArgs a) {
 
 // ---------------------------------------------------------------- gradient
 
-// Orders the LDS accesses of a wave's lanes for the compiler; the hardware keeps them
-// in order.
-__device__ __forceinline__ void wave_lds_fence() {
-    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-    __builtin_amdgcn_wave_barrier();
-}
-
 template <int V>
 __global__ __launch_bounds__(64 * kRouteWaves) void k_route_backward(RouteBackwardArgs a) {
     __shared__ int s_pairs[kRouteWaves][64 * V];
@@ -750,8 +948,10 @@ hipError_t launch_route(RouteArgs a, hipStream_t stream) {
     while (64 * V < a.E) V *= 2;
     const int size = a.E / a.G, lanes = size / V;
     a.group_lanes = size % V == 0 && (lanes & (lanes - 1)) == 0 ? lanes : 0;
-    const dim3 grid((unsigned)((a.T + kRouteWaves - 1) / kRouteWaves)), block(64 * kRouteWaves);
     const bool full = a.bias != nullptr || (a.G > 1 && a.best > 1);
+    // scores of bf16 logits alone tie too often
+    a.narrow = (!full || a.f32 || a.bias != nullptr) && (a.G == 1 || a.group_lanes > 0);
+    const dim3 grid((unsigned)((a.T + kRouteWaves - 1) / kRouteWaves)), block(64 * kRouteWaves);
     if (launch_debug()) launch_debug_print("k_route", grid, block, "experts %d keys %d", a.E, full ? 64 : 32);
     for_experts(a.E, [&](auto v) {
         constexpr int V = decltype(v)::value;

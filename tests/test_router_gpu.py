@@ -80,6 +80,25 @@ def test_ties_go_to_the_lowest_index(E, G, biased):
     check_route(ops.Router(E, 6, 1, 1, 1, 1), logits[:1] * 0, bias)
 
 
+@pytest.mark.parametrize("sigmoid", [1, 0])
+@pytest.mark.parametrize("E,k,G,keep,best", [(24, 4, 1, 1, 1), (64, 6, 8, 3, 2), (100, 5, 1, 1, 1), (256, 8, 8, 4, 2), (256, 8, 8, 4, 1),
+                                             (384, 8, 1, 1, 1), (160, 6, 8, 3, 2), (1024, 32, 16, 4, 2)])
+def test_scores_closer_than_binary32(E, k, G, keep, best, sigmoid):
+    """Scores a fraction of a binary32 unit apart, at the border of the choice, within it, or for all
+    experts, under biases that are equal or exact; the choice is that of scores in 64 bits. Logits of
+    8 differ by steps of 2^-20, which is more than 10^-10 in a sigmoid and 2^-20 of itself in a
+    softmax's share: far more than 64 bits' rounding."""
+    g, T = gen(E + k), 60
+    r = ops.Router(E, k, sigmoid, G, keep, best, renormalize=True)
+    logits = torch.randn((T, E), device="cuda", generator=g) * 1.5
+    near = 8.0 + 2.0 ** -20 * torch.randint(0, 1 << 17, (T, E), device="cuda", generator=g).float()
+    share = torch.linspace(0, 1.2, T, device="cuda")[:, None]    # from no expert to all of them
+    logits = torch.where(torch.rand((T, E), device="cuda", generator=g) < share, near, logits)
+    for bias in (torch.zeros(E, device="cuda"), torch.randint(0, 3, (E,), device="cuda", generator=g).float() * 0.25):
+        check_route(r, logits, bias=bias)
+    check_route(r, logits)
+
+
 @pytest.mark.parametrize("E", [40, 64, 250, 256, 700])
 @pytest.mark.parametrize("biased", [False, True])
 def test_closed_experts(E, biased):
