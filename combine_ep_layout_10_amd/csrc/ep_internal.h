@@ -267,12 +267,12 @@ struct RouteBackwardArgs {
 constexpr int kMaxRouteGroups = 64;         // one a lane
 constexpr int kMaxRouteTokens = 1 << 25;    // a wave each: 2^31 threads
 constexpr int kMaxRouteSequences = 1 << 17;  // a block of 1,024 threads for 64 experts of each: 2^31 threads
-constexpr int kBalanceWaves = 8;             // of a piece
+constexpr int kBalanceTurn = 32;              // tokens that a piece's waves have in flight
 
-// Tokens of a piece: a turn of its waves, and more where that would make over 512
+// Tokens of a piece: one turn, and more where that would make over 512
 // pieces, which a block of the second kernel reads in turn. By the sizes alone.
 inline int balance_tile(int tokens) {
-    const int turn = 4 * kBalanceWaves, pieces = 512;
+    const int turn = kBalanceTurn, pieces = 512;
     return ((tokens + pieces - 1) / pieces + turn - 1) / turn * turn + (tokens == 0 ? turn : 0);
 }
 

@@ -11,7 +11,7 @@
 // compared one after the other: the higher one decides unless two experts share it.
 //
 // Bound by instructions, and for few tokens by the launches. 8192 tokens x 256 experts in
-// binary32, us: choice (sigmoid, bias, 4 of 8 groups) 8.9, loss 13.1 (two launches), gradient
+// binary32, us: choice (sigmoid, bias, 4 of 8 groups) 8.9, loss 12.2 (two launches), gradient
 // of both 7.6; the logits alone take 1.4 us to read (6.1 TB/s). 128 tokens: choice 4.0.
 #include <type_traits>
 
@@ -616,13 +616,16 @@ __device__ __forceinline__ int sequence_past(const int32_t* off, int S, int t) {
 
 // Tile b (a.tile tokens) by sequence q: a piece of its own at place b + q of the
 // partial sums. The pieces of a batch run from (0, 0) up in b or in q, never both,
-// so places are distinct. A wave has kBalanceAhead tokens in flight; their shares are
-// added in binary32, and those sums in binary64.
-constexpr int kBalanceAhead = 4;
+// so places are distinct. A wave has 2 tokens in flight (4 where 16 waves' sums do not fit
+// into LDS); their shares are added in binary32, and those sums in binary64. 16 waves, 8, 4
+// for the 32 tokens of a turn: the batch of 8192 x 256 takes 12.2, 12.8, 15.1 us.
+template <int V>
+constexpr int kBalanceWaves = V <= 8 ? 16 : 8;
 
 template <int V>
-__global__ __launch_bounds__(64 * kBalanceWaves) void k_balance_pieces(BalanceArgs a) {
-    __shared__ float s_sum[kBalanceWaves][64 * V];
+__global__ __launch_bounds__(64 * kBalanceWaves<V>) void k_balance_pieces(BalanceArgs a) {
+    constexpr int kWaves = kBalanceWaves<V>, kAhead = kBalanceTurn / kWaves;
+    __shared__ float s_sum[kWaves][64 * V];
     __shared__ int s_count[64 * V];
     __shared__ int s_tokens;
     const int tid = threadIdx.x, lane = lane_id(), wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -638,19 +641,19 @@ __global__ __launch_bounds__(64 * kBalanceWaves) void k_balance_pieces(BalanceAr
             to = min(t1, a.seq_off[q + 1]);
             if (from >= to) continue;
         }
-        for (int e = tid; e < 64 * V; e += 64 * kBalanceWaves) s_count[e] = 0;
+        for (int e = tid; e < 64 * V; e += 64 * kWaves) s_count[e] = 0;
         if (tid == 0) s_tokens = 0;
         __syncthreads();
         double sum[V];
 #pragma unroll
         for (int v = 0; v < V; ++v) sum[v] = 0.0;
         int tokens = 0;
-        for (int t = from + wave; t < to; t += kBalanceAhead * kBalanceWaves) {
-            int id[kBalanceAhead];
-            float l[kBalanceAhead][V];
+        for (int t = from + wave; t < to; t += kAhead * kWaves) {
+            int id[kAhead];
+            float l[kAhead][V];
 #pragma unroll
-            for (int i = 0; i < kBalanceAhead; ++i) {
-                const int u = t + i * kBalanceWaves;
+            for (int i = 0; i < kAhead; ++i) {
+                const int u = t + i * kWaves;
                 id[i] = -1;
                 if (u >= to) continue;
                 if (lane < a.k) id[i] = load_id(a.idx, a.idx_bits, (int64_t)u * a.k + lane, a.E);
@@ -660,7 +663,7 @@ __global__ __launch_bounds__(64 * kBalanceWaves) void k_balance_pieces(BalanceAr
 #pragma unroll
             for (int v = 0; v < V; ++v) part[v] = 0.0f;
 #pragma unroll
-            for (int i = 0; i < kBalanceAhead; ++i) {
+            for (int i = 0; i < kAhead; ++i) {
                 if (ballot64(id[i] >= 0) == 0) continue;
                 if (id[i] >= 0) atomicAdd(&s_count[id[i]], 1);
                 ++tokens;
@@ -678,10 +681,10 @@ __global__ __launch_bounds__(64 * kBalanceWaves) void k_balance_pieces(BalanceAr
         if (lane == 0 && tokens > 0) atomicAdd(&s_tokens, tokens);
         __syncthreads();
         const int64_t place = (int64_t)blockIdx.x + q;
-        for (int e = tid; e < a.E; e += 64 * kBalanceWaves) {
+        for (int e = tid; e < a.E; e += 64 * kWaves) {
             float total = 0.0f;
 #pragma unroll
-            for (int i = 0; i < kBalanceWaves; ++i) total += s_sum[i][e];
+            for (int i = 0; i < kWaves; ++i) total += s_sum[i][e];
             a.sums[place * a.E + e] = total;
             a.pairs[place * a.E + e] = s_count[e];
         }
@@ -963,10 +966,11 @@ hipError_t launch_route(RouteArgs a, hipStream_t stream) {
 
 hipError_t launch_balance_loss(const BalanceArgs& a, hipStream_t stream) {
     const int tiles = a.T > 0 ? (a.T + a.tile - 1) / a.tile : 1;  // one clears the count
-    const dim3 grid((unsigned)tiles), block(64 * kBalanceWaves);
-    if (launch_debug()) launch_debug_print("k_balance_pieces", grid, block, "experts %d sequences %d", a.E, a.S);
+    const dim3 grid((unsigned)tiles);
     for_experts(a.E, [&](auto v) {
         constexpr int V = decltype(v)::value;
+        const dim3 block(64 * kBalanceWaves<V>);
+        if (launch_debug()) launch_debug_print("k_balance_pieces", grid, block, "experts %d sequences %d", a.E, a.S);
         hipLaunchKernelGGL(k_balance_pieces<V>, grid, block, 0, stream, a);
     });
     const hipError_t e = hipGetLastError();
