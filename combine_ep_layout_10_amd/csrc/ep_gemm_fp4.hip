@@ -103,13 +103,12 @@ __device__ __forceinline__ void run_tile(const Fp4Args& a, const ExpertRows& er,
         }
 #pragma unroll
         for (int j = 0; j < SL; ++j) {
-            const int q = j * 64 * kWaves + tid, row = q / (NC * 4);
-            xs[j] = row < rows ? load_scales4(x_scales + (int64_t)row * groups, (kc * NC * 4 + q % (NC * 4)) * 4, groups)
-                               : 0u;
+            const int q = j * 64 * kWaves + tid, row = min(q / (NC * 4), rows - 1);
+            xs[j] = load_scales4(x_scales + (int64_t)row * groups, (kc * NC * 4 + q % (NC * 4)) * 4, groups);
         }
     };
-    const auto store_rows = [&](int stage) {
-        uint8_t* const at = s_x + stage * L::kBytes;
+    const auto store_rows = [&](int kc) {
+        uint8_t* const at = s_x + (kc & 1) * L::kBytes;
 #pragma unroll
         for (int j = 0; j < XL; ++j) {
             const int q = j * 64 * kWaves + tid, row = q / (NC * 16), c = q % (NC * 16);
@@ -120,8 +119,9 @@ __device__ __forceinline__ void run_tile(const Fp4Args& a, const ExpertRows& er,
             const int q = j * 64 * kWaves + tid, row = q / (NC * 4), c = q % (NC * 4);
             if (row < kRows) {
                 uint8_t* const to = at + L::kCodes + row * L::kPitch + c / 4 * 16 + c % 4;
+                const uint32_t w = place_scales4(xs[j], (kc * NC * 4 + c) * 4, groups);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) to[4 * i] = (uint8_t)(xs[j] >> (8 * i));
+                for (int i = 0; i < 4; ++i) to[4 * i] = (uint8_t)(w >> (8 * i));
             }
         }
     };
@@ -152,7 +152,8 @@ __device__ __forceinline__ void run_tile(const Fp4Args& a, const ExpertRows& er,
                 row_scale[n] = *(const uint32_t*)(x + L::kCodes + (16 * n + r16) * L::kPitch + u * 16 + g * 4);
             uint32_t col_scale[MC];
 #pragma unroll
-            for (int c = 0; c < MC; ++c) col_scale[c] = scales_by_mfma(scale[p][c], select);
+            for (int c = 0; c < MC; ++c)
+                col_scale[c] = scales_by_mfma(place_scales4(scale[p][c], (kc * NC + u) * 16 + g * 4, groups), select);
             const auto part = [&](auto tt) {
                 constexpr int t = decltype(tt)::value;
 #pragma unroll
@@ -171,7 +172,7 @@ __device__ __forceinline__ void run_tile(const Fp4Args& a, const ExpertRows& er,
             // the unit P further on in this wave's order: b + P of this slice, or of the next
             load((b + P < B ? kc : kc + 1) * NC + ks * B + (b + P) % B, p);
         }
-        if (kc + 1 < slices) store_rows((kc + 1) & 1);
+        if (kc + 1 < slices) store_rows(kc + 1);
         wait_lgkmcnt0();
         block_barrier();
     }
