@@ -12,7 +12,7 @@
 //
 // Bound by instructions, and for few tokens by the launches. 8192 tokens x 256 experts in
 // binary32, us: choice (sigmoid, bias, 4 of 8 groups) 8.9, loss 12.2 (two launches), gradient
-// of both 7.6; the logits alone take 1.4 us to read (6.1 TB/s). 128 tokens: choice 4.0.
+// of both 7.3; the logits alone take 1.4 us to read (6.1 TB/s). 128 tokens: choice 4.0.
 #include <type_traits>
 
 #include "ep_internal.h"
@@ -797,12 +797,28 @@ __global__ __launch_bounds__(64 * kRouteWaves) void k_route_backward(RouteBackwa
     float grad[V];
 #pragma unroll
     for (int v = 0; v < V; ++v) grad[v] = 0.0f;
-    const int id = lane < a.k ? load_id(a.idx, a.idx_bits, (int64_t)t * a.k + lane, a.E) : -1;
+    // all that depends on nothing is on its way before anything is waited for
+    float l[V];
+    load_logits<V>(a.logits, a.f32, t, a.E, lane, l);
+    const int64_t slot = (int64_t)t * a.k + min(lane, a.k - 1);
+    int id = load_id(a.idx, a.idx_bits, slot, a.E);
+    float gw = a.grad_w != nullptr ? a.grad_w[slot] : 0.0f;
+    int q = 0;
+    bool in = a.counts != nullptr;
+    if (in && a.seq_off != nullptr) {
+        q = sequence_past(a.seq_off, a.S, t);
+        in = q < a.S && a.seq_off[q] <= t;
+    }
+    int32_t pairs_of[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) pairs_of[v] = in ? a.counts[(int64_t)q * a.E + min(lane * V + v, a.E - 1)] : 0;
+    if (lane >= a.k) {
+        id = -1;
+        gw = 0.0f;
+    }
     if (ballot64(id >= 0) != 0) {
-        const float gw = a.grad_w != nullptr && lane < a.k ? a.grad_w[(int64_t)t * a.k + lane] : 0.0f;
-        float l[V], s[V], slope[V], u[V], b[V];
+        float s[V], slope[V], u[V], b[V];
         int n[V];
-        load_logits<V>(a.logits, a.f32, t, a.E, lane, l);
         const bool softmax = a.score == EP_SCORE_SOFTMAX;
         const float total = score_terms<V>(a.score, l, s, slope);
         const float inv = total == 0.0f ? 0.0f : 1.0f / total;
@@ -852,43 +868,34 @@ __global__ __launch_bounds__(64 * kRouteWaves) void k_route_backward(RouteBackwa
                     d += (float)n[v] * s[v];
                     q += u[v] * s[v];
                 }
-                d = wave_sum(d) + 1e-20f;
-                q = wave_sum(q) / d;
+                d = 1.0f / (wave_sum(d) + 1e-20f);
+                q = wave_sum(q) * d;
 #pragma unroll
-                for (int v = 0; v < V; ++v) u[v] = n[v] > 0 ? a.scale * ((u[v] - (float)n[v] * q) / d) : 0.0f;
+                for (int v = 0; v < V; ++v) u[v] = n[v] > 0 ? a.scale * ((u[v] - (float)n[v] * q) * d) : 0.0f;
             } else {
 #pragma unroll
                 for (int v = 0; v < V; ++v) u[v] *= a.scale;
             }
         }
-        if (a.counts != nullptr) {
-            int q = 0;
-            bool in = true;
-            if (a.seq_off != nullptr) {
-                q = sequence_past(a.seq_off, a.S, t);
-                in = q < a.S && a.seq_off[q] <= t;
+        if (in) {
+            // A constant added to every b changes nothing, and counts of a balanced
+            // batch are nearly equal: the first one goes out exactly, as an integer.
+            const float f = a.grad_loss[0] * a.coef[q];
+            const int first = __builtin_amdgcn_readfirstlane(pairs_of[0]);
+            float mean = 0.0f;
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                const int e = lane * V + v;
+                b[v] = e < a.E ? f * (float)(pairs_of[v] - first) : 0.0f;
+                mean += s[v] * b[v];
             }
-            if (in) {
-                // A constant added to every b changes nothing, and counts of a balanced
-                // batch are nearly equal: the first one goes out exactly, as an integer.
-                const int32_t* c = a.counts + (int64_t)q * a.E;
-                const float f = a.grad_loss[0] * a.coef[q];
-                const int first = c[0];
-                float mean = 0.0f;
+            mean = wave_sum(mean);
+            if (softmax) {
 #pragma unroll
-                for (int v = 0; v < V; ++v) {
-                    const int e = lane * V + v;
-                    b[v] = e < a.E ? f * (float)(c[e] - first) : 0.0f;
-                    mean += s[v] * b[v];
-                }
-                mean = wave_sum(mean);
-                if (softmax) {
+                for (int v = 0; v < V; ++v) b[v] -= mean;
+            } else {
 #pragma unroll
-                    for (int v = 0; v < V; ++v) b[v] -= mean;
-                } else {
-#pragma unroll
-                    for (int v = 0; v < V; ++v) b[v] = (b[v] - mean * inv) * inv;
-                }
+                for (int v = 0; v < V; ++v) b[v] = (b[v] - mean * inv) * inv;
             }
         }
         if (softmax) {
