@@ -242,7 +242,12 @@ __global__ __launch_bounds__(64 * kWaves) void k_grouped_gemm_fp4_stream(Fp4Args
 // DMA, two steps deep. Lane (g, r16) of the MFMA reads chunks f(g) and f(g) + 1 (16
 // bytes, 32 codes) of its row, f = 0, 6, 2, 4, whose scales are two neighbouring bytes.
 // Chunk c of row r is stored at c ^ (r / 2 mod 8): with these f a read meets each bank
-// once. Scales move in slabs of four steps, 32 bytes a row, two slabs deep.
+// once. Scales move in slabs of four steps, 32 bytes a row, two slabs deep. WORDS: their
+// rows are whole words of four bytes, as the DMA needs them. Otherwise a slab's 32 bytes start at
+// the word that a row's part starts in, up to 3 bytes before it, and hold three steps; all
+// rows of a lane are off by the same number of bytes, since 16 of them are whole words.
+// Words that would reach past the tile's last row are left out: the up to 3 scales lost
+// there are read apart and put in place in the last steps.
 //
 // Schedule: the waves form two groups (wm) half a step apart: while one group's MFMAs
 // run, the other reads its operands from LDS, then a barrier exchanges the roles.
@@ -253,13 +258,19 @@ __global__ __launch_bounds__(64 * kWaves) void k_grouped_gemm_fp4_stream(Fp4Args
 //   interval 2 kb + 1  group 1 sends its own half of A of step kb + S - 1, group 0 its own
 //                      half of A of step kb + S; every fourth one the next slab.
 // What is sent has 2 S - 2 intervals to land. S is 2, and 3 for tiles of up to 64 rows, which
-// wait for the weights (1,024 rows on 64 experts, 4096 x 7168: 177 us, with two steps 193).
+// wait for the weights (1,024 rows on 64 experts, 4096 x 7168: 177 us, with two steps 193). 65,536
+// rows on 32 experts, the same: 0.98 ms, without WORDS 1.34.
 constexpr int kTile = 256;
 constexpr int kStepBytes = 128;                  // of a row: 256 codes
 constexpr int kHalfA = 128 * kStepBytes;         // bytes of a group's half of a slice of A
 constexpr int kSliceB = kTile * kStepBytes;
 constexpr int kSlabRows = 2 * kTile;             // A's, then B's
-constexpr int kSlabSteps = 4, kSlabRow = 8 * kSlabSteps;  // steps of a slab of scales, its bytes a row
+constexpr int kSlabRow = 32;                     // bytes of a row in a slab of scales
+template <bool WORDS>
+constexpr int kSlabSteps = WORDS ? 4 : 3;
+// Rows of a tile; 256 of them and the scales of any alignment take more registers than there are.
+template <bool WORDS>
+constexpr int kTileRows = WORDS ? 256 : 192;
 constexpr int kSlab = kSlabRows * kSlabRow;
 constexpr int kTileLds = 4 * kHalfA + 2 * kSliceB + 2 * kSlab;  // all of the CU's 160 KiB
 constexpr int kStoreLds = 4096;
@@ -279,11 +290,11 @@ struct TileLds {
 };
 
 // What a wave sends. MI: 32-row pieces of a wave.
-template <int MI>
+template <int MI, bool WORDS>
 struct Sender {
     const uint8_t *a, *b, *s;        // of the tile, reduction step 0; s: this wave's scales
     int half, groups;                // bytes of a row's codes and scales
-    int rows, cols, s_rows;          // that exist
+    int rows, cols, s_bytes;         // that exist
     int steps;
     uint32_t off_a[MI], off_b[4], off_s;
     int w;
@@ -307,11 +318,17 @@ struct Sender {
             off_b[j] = __umul24(r, half) + 16 * (pos ^ ((r >> 1) & 7));
         }
         // scales: waves 0 to 3 those of 64 rows of A each, waves 4 to 7 of B
-        const int r0 = 64 * (w & 3);
-        const bool of_b = w >= 4;
-        s = (of_b ? g.b_scales + first_col * groups : g.x_scales + first_row * groups) + (int64_t)r0 * groups;
-        s_rows = max(0, min(64, (of_b ? cols : rows) - r0));
-        off_s = __umul24(lane >> 1, groups) + 16 * (lane & 1);
+        const int r0 = 64 * (w & 3), left = (w >= 4 ? cols : rows) - r0;
+        s = (w >= 4 ? g.b_scales + first_col * groups : g.x_scales + first_row * groups) + (int64_t)r0 * groups;
+        if (WORDS) {
+            s_bytes = max(0, left * groups);
+            off_s = __umul24(lane >> 1, groups) + 16 * (lane & 1);
+        } else {
+            const int before = (uintptr_t)s & 3;
+            s -= before;
+            s_bytes = left > 0 ? (before + left * groups) & ~3 : 0;
+            off_s = ((before + __umul24(lane >> 1, groups)) & ~3u) + 16 * (lane & 1);
+        }
     }
     __device__ __forceinline__ void send_a(int kb, int place, int j) const {
         dma16(a + (int64_t)kb * kStepBytes, kb < steps ? rows * half - kb * kStepBytes : 0, off_a[j],
@@ -321,12 +338,13 @@ struct Sender {
         dma16(b + (int64_t)kb * kStepBytes, kb < steps ? cols * half - kb * kStepBytes : 0, off_b[j],
               lds.b(place) + (4 * w + j) * 1024);
     }
-    // slab j: steps 4 j .. 4 j + 3; a load takes 32 rows
+    // slab j: steps kSlabSteps j on; a load takes 32 rows
     __device__ __forceinline__ void send_slab(int j) const {
-        const int size = kSlabSteps * j < steps ? max(0, s_rows * groups - j * kSlabRow) : 0;
+        constexpr int kSteps = kSlabSteps<WORDS>;
+        const int size = kSteps * j < steps ? max(0, s_bytes - j * 8 * kSteps) : 0;
 #pragma unroll
         for (int d = 0; d < 2; ++d)
-            dma16(s + (int64_t)j * kSlabRow, size, off_s + 32 * d * groups, lds.slab(j) + (2 * w + d) * 1024);
+            dma16(s + (int64_t)j * 8 * kSteps, size, off_s + 32 * d * groups, lds.slab(j) + (2 * w + d) * 1024);
     }
 };
 
@@ -339,26 +357,73 @@ __device__ __forceinline__ uint32_t read_scales(uint32_t at, uint32_t select) {
     return __builtin_amdgcn_perm(high, low, select);
 }
 
-// The loop of one group of waves over all steps.
-template <bool SECOND, int MI>
-__device__ __forceinline__ void multiply(const Sender<MI>& send, f32x4_t (&acc)[2 * MI][4], int wn, int groups) {
+// The same for scales at any byte: `at` the word that the pairs start in, or lie in the
+// next, `shift` bytes on.
+__device__ __forceinline__ uint32_t read_scales(uint32_t at, int shift) {
+    const lds_u32_t *low = (const lds_u32_t*)at, *high = (const lds_u32_t*)(at + 16 * kSlabRow);
+    const uint32_t l = __builtin_amdgcn_alignbyte(low[1], low[0], shift), h = __builtin_amdgcn_alignbyte(high[1], high[0], shift);
+    return __builtin_amdgcn_perm(h, l, 0x05040100u);
+}
+
+// The pairs of scales of groups g and g + 1 of rows r and r + 16 near a row's end: the `n`
+// last scales of row `last`, before `end`, which whole words do not reach, in their place;
+// zeros past the last group: 2^-127 by 2^-127.
+__device__ __forceinline__ uint32_t finish_scales(uint32_t pairs, int r, int g, int groups, int last, const uint8_t* end) {
+    const int first = groups - (int)((uintptr_t)end & 3);
+    uint32_t keep = 0xFFFF, mask = 0, bytes = 0;
+#pragma unroll
+    for (int b = 0; b < 2; ++b) {
+        if (g + b >= groups) {
+            keep &= ~(0xFFu << (8 * b));
+        } else if (g + b >= first) {
+            mask |= 0xFFu << (8 * b);
+            bytes |= (uint32_t)end[g + b - groups] << (8 * b);
+        }
+    }
+    if (r == last) pairs = (pairs & ~mask) | bytes;
+    if (r + 16 == last) pairs = (pairs & ~(mask << 16)) | bytes << 16;
+    return pairs & (keep | keep << 16);
+}
+
+// The loop of one group of waves over all steps. scales_a, scales_b: the tile's.
+template <bool SECOND, int MI, bool WORDS>
+__device__ __forceinline__ void multiply(const Sender<MI, WORDS>& send, f32x4_t (&acc)[2 * MI][4], int wn, int groups,
+                                         const uint8_t* scales_a, const uint8_t* scales_b) {
+    constexpr int kSlab = kSlabSteps<WORDS>;
     const int lane = lane_id(), r16 = lane & 15, g = lane >> 4;
     const int first = g == 0 ? 0 : g == 1 ? 6 : g == 2 ? 2 : 4;  // chunk of half 0
     const uint32_t row = r16 * kStepBytes + ((first ^ ((r16 >> 1) & 7)) << 4);
     const uint32_t select = first & 2 ? 0x07060302u : 0x05040100u;
+    // where in its slab a lane's first pair of scales starts: A's in the lowest 8 bits, B's in the next
+    const int bytes = (((int)(uintptr_t)scales_a + r16 * groups) & 3) + first + ((((int)(uintptr_t)scales_b + r16 * groups) & 3) + first) * 256;
     using Lds = TileLds<MI>;
     constexpr int S = Lds::kSteps, kMore = (S - 2) * (4 + MI);  // loads that may be on their way beside those of two steps
     const Lds lds = send.lds;
     int place = 0;
     for (int kb = 0; kb < send.steps; ++kb, place = Lds::after(place, 1)) {
         const uint32_t at_a = lds.a(place, SECOND ? 1 : 0) + row, at_b = lds.b(place) + wn * 64 * kStepBytes + row;
-        const uint32_t at_s = lds.slab(kb / kSlabSteps) + r16 * kSlabRow + kb % kSlabSteps * 8 + (first & 4);
+        const int slab_of = kb / kSlab, in_slab = kb - kSlab * slab_of;
+        const uint32_t at_s = lds.slab(slab_of) + r16 * kSlabRow + in_slab * 8 + (WORDS ? first & 4 : 0);
         u32x4_t fa[2][2 * MI], fb[2][4];
         uint32_t sa[MI], sb[2];  // two pieces' pairs of scales a word
+        const auto scales = [&](int piece, int byte) {
+            const uint32_t at = at_s + piece * kSlabRow;
+            return WORDS ? read_scales(at, select) : read_scales(at + (byte & ~3), byte & 3);
+        };
 #pragma unroll
-        for (int j = 0; j < 2; ++j) sb[j] = read_scales(at_s + (kTile + 64 * wn + 32 * j) * kSlabRow, select);
+        for (int j = 0; j < 2; ++j) sb[j] = scales(kTile + 64 * wn + 32 * j, bytes >> 8);
 #pragma unroll
-        for (int i = 0; i < MI; ++i) sa[i] = read_scales(at_s + (64 * i + (SECOND ? 32 : 0)) * kSlabRow, select);
+        for (int i = 0; i < MI; ++i) sa[i] = scales(64 * i + (SECOND ? 32 : 0), bytes & 255);
+        if (!WORDS && 8 * kb + 11 > groups) {  // at most two scales behind this step; ahead of the codes, for their registers
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+                sb[j] = finish_scales(sb[j], 64 * wn + 32 * j + r16, 8 * kb + first, groups, send.cols - 1,
+                                      scales_b + (int64_t)send.cols * groups);
+#pragma unroll
+            for (int i = 0; i < MI; ++i)
+                sa[i] = finish_scales(sa[i], 64 * i + (SECOND ? 32 : 0) + r16, 8 * kb + first, groups, send.rows - 1,
+                                      scales_a + (int64_t)send.rows * groups);
+        }
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
 #pragma unroll
@@ -366,11 +431,11 @@ __device__ __forceinline__ void multiply(const Sender<MI>& send, f32x4_t (&acc)[
 #pragma unroll
             for (int i = 0; i < 2 * MI; ++i) fa[h][i] = read_codes((at_a ^ (h << 4)) + 16 * kStepBytes * i);
         }
-        const bool slab = kb % kSlabSteps == 0;  // interval 2 kb + 1 sends the next slab
+        const bool slab = in_slab == 0;  // interval 2 kb + 1 sends the next slab
         if (SECOND) {  // interval 2 kb + 1
 #pragma unroll
             for (int j = 0; j < MI; ++j) send.send_a(kb + S - 1, Lds::after(place, S - 1), j);
-            if (slab) send.send_slab(kb / kSlabSteps + 1);
+            if (slab) send.send_slab(slab_of + 1);
             // B of step kb + 1 has landed, and all before it
             if (slab) wait_vmcnt<MI + kMore + 2>();
             else wait_vmcnt<MI + kMore>();
@@ -380,7 +445,7 @@ __device__ __forceinline__ void multiply(const Sender<MI>& send, f32x4_t (&acc)[
         }
         wait_lgkmcnt0();
         block_barrier();
-        if (8 * kb + first >= groups) {  // past the reduction: 2^-127 by 2^-127
+        if (WORDS && 8 * kb + first >= groups) {  // past the reduction: 2^-127 by 2^-127
 #pragma unroll
             for (int j = 0; j < 2; ++j) sb[j] = 0u;
 #pragma unroll
@@ -401,7 +466,7 @@ __device__ __forceinline__ void multiply(const Sender<MI>& send, f32x4_t (&acc)[
 #pragma unroll
                     for (int d = 0; d < MI; ++d)
                         if (d * 2 == h * MI + i) send.send_a(kb + S, place, d);
-                    if (i == MI - 1 && h == 1 && slab) send.send_slab(kb / kSlabSteps + 1);
+                    if (i == MI - 1 && h == 1 && slab) send.send_slab(slab_of + 1);
                 }
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
@@ -430,12 +495,12 @@ __device__ __forceinline__ void multiply(const Sender<MI>& send, f32x4_t (&acc)[
 }
 
 // Rows of the tile: MI 32-row pieces for each group.
-template <int MI>
+template <int MI, bool WORDS>
 __device__ __forceinline__ void run_whole(const Fp4Args& a, const ExpertRows& er, int e, int m0, int rows, int n0,
                                           bool last, uint32_t lds) {
     const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), wm = w >> 2, wn = w & 3;
     const int64_t first_row = (int64_t)er.first + m0;
-    Sender<MI> send;
+    Sender<MI, WORDS> send;
     send.half = a.K / 2;
     send.groups = a.K / 32;
     send.steps = (a.K + 255) / 256;
@@ -447,6 +512,8 @@ __device__ __forceinline__ void run_whole(const Fp4Args& a, const ExpertRows& er
     for (int i = 0; i < 2 * MI; ++i)
 #pragma unroll
         for (int j = 0; j < 4; ++j) acc[i][j] = (f32x4_t){0.0f, 0.0f, 0.0f, 0.0f};
+    const uint8_t *const scales_a = a.x_scales + first_row * send.groups,
+                  *const scales_b = a.b_scales + ((int64_t)e * a.N + n0) * send.groups;
     // ahead of interval 0: slab 0, B and A of all steps but one, and group 0's half of A of that
     constexpr int S = TileLds<MI>::kSteps, kMore = (S - 2) * (4 + MI);
     send.send_slab(0);
@@ -465,14 +532,14 @@ __device__ __forceinline__ void run_whole(const Fp4Args& a, const ExpertRows& er
     block_barrier();
     const int groups = a.K / 32;
     if (wm == 0) {
-        multiply<false, MI>(send, acc, wn, groups);
+        multiply<false, MI, WORDS>(send, acc, wn, groups, scales_a, scales_b);
         block_barrier();
     } else {
 #pragma unroll
         for (int j = 0; j < 4; ++j) send.send_b(S - 1, S - 1, j);
         wait_vmcnt<4 + kMore>();
         block_barrier();  // half a step later
-        multiply<true, MI>(send, acc, wn, groups);
+        multiply<true, MI, WORDS>(send, acc, wn, groups, scales_a, scales_b);
     }
     wait_vmcnt<0>();
     block_barrier();  // no wave reads or fills the ring any more
@@ -499,14 +566,16 @@ __device__ __forceinline__ void run_whole(const Fp4Args& a, const ExpertRows& er
     if (a.rows.zero_pad && last) clear_padding<kTile>(a.out, a.N, er, n0);
 }
 
+template <bool WORDS>
 __global__ __launch_bounds__(512) void k_grouped_gemm_fp4(Fp4Args a) {
     __shared__ __attribute__((aligned(1024))) uint8_t s_ring[kTileLds];
+    constexpr int kRows = kTileRows<WORDS>;
     const int nt_n = (a.N + kTile - 1) / kTile;
     int e, local, m, n;
-    if (!find_expert(a.rows, kTile, nt_n, &e, &local)) return;
+    if (!find_expert(a.rows, kRows, nt_n, &e, &local)) return;
     e = __builtin_amdgcn_readfirstlane(e);
     const ExpertRows er = expert_rows(a.rows, e);
-    const int nt_m = (er.live + kTile - 1) / kTile;
+    const int nt_m = (er.live + kRows - 1) / kRows;
     order_tiles<2>(local, nt_m, nt_n, &m, &n);
     const int each = ((er.live + nt_m - 1) / nt_m + 63) & ~63;  // rows of a tile; never leaves the last one empty
     const int m0 = __builtin_amdgcn_readfirstlane(m * each), n0 = __builtin_amdgcn_readfirstlane(n * kTile);
@@ -515,10 +584,10 @@ __global__ __launch_bounds__(512) void k_grouped_gemm_fp4(Fp4Args a) {
     const uint32_t lds = lds_offset(s_ring);
     asm volatile("" ::"v"(s_ring) : "memory");  // the ring is written by the DMA alone
     switch ((rows + 63) / 64) {
-        case 1: return run_whole<1>(a, er, e, m0, rows, n0, last, lds);
-        case 2: return run_whole<2>(a, er, e, m0, rows, n0, last, lds);
-        case 3: return run_whole<3>(a, er, e, m0, rows, n0, last, lds);
-        default: return run_whole<4>(a, er, e, m0, rows, n0, last, lds);
+        case 1: return run_whole<1, WORDS>(a, er, e, m0, rows, n0, last, lds);
+        case 2: return run_whole<2, WORDS>(a, er, e, m0, rows, n0, last, lds);
+        case 3: return run_whole<3, WORDS>(a, er, e, m0, rows, n0, last, lds);
+        default: return run_whole<kRows / 64, WORDS>(a, er, e, m0, rows, n0, last, lds);
     }
 }
 
@@ -534,12 +603,13 @@ hipError_t launch(const Fp4Args& a, int64_t pairs, hipStream_t stream) {
     return hipGetLastError();
 }
 
-hipError_t launch_whole(const Fp4Args& a, int64_t pairs, hipStream_t stream) {
-    const int64_t blocks = max_row_tiles(a.rows, kTile, pairs) * ((a.N + kTile - 1) / kTile);
+hipError_t launch_whole(const Fp4Args& a, int64_t pairs, bool words, hipStream_t stream) {
+    const int64_t blocks = max_row_tiles(a.rows, words ? kTileRows<true> : kTileRows<false>, pairs) * ((a.N + kTile - 1) / kTile);
     if (blocks > 0x7FFFFF) return hipErrorInvalidConfiguration;
     if (launch_debug())
-        launch_debug_print("k_grouped_gemm_fp4", dim3((unsigned)blocks), dim3(512), "n %d k %d", a.N, a.K);
-    hipLaunchKernelGGL(k_grouped_gemm_fp4, dim3((unsigned)blocks), dim3(512), 0, stream, a);
+        launch_debug_print("k_grouped_gemm_fp4", dim3((unsigned)blocks), dim3(512), "n %d k %d words %d", a.N, a.K, (int)words);
+    if (words) hipLaunchKernelGGL(k_grouped_gemm_fp4<true>, dim3((unsigned)blocks), dim3(512), 0, stream, a);
+    else hipLaunchKernelGGL(k_grouped_gemm_fp4<false>, dim3((unsigned)blocks), dim3(512), 0, stream, a);
     return hipGetLastError();
 }
 
@@ -563,8 +633,18 @@ hipError_t launch_whole(const Fp4Args& a, int64_t pairs, hipStream_t stream) {
 //     64 rows, split 2                                        7.0       7.0       7.6 12.2 14.4
 //     64 rows                                                 8.8       8.8       9.8 11.4 11.6
 //     whole tiles                                             9.5       9.5       9.7 12.7 15.0
+// and where rows of scales are no whole words:
+//   top-8 of 64 experts, 4096 x 7200                       4         8   16   32   64  128
+//     64 rows                                            220       226  232  241  333  488
+//     whole tiles (192 rows)                             217       222  224  232  261  303
+//   top-1 of 32 experts, 4096 x 4064
+//     64 rows                                           64.2      67.6      72.2  103
+//     whole tiles                                       68.7      72.6      75.4 82.9
+//   top-3 of 24 experts, 1000 x 1440 (96 whole tiles)     6   12   38   64  188
+//     64 rows                                           7.7  8.0  9.3 13.7 21.7
+//     whole tiles                                      12.0 12.0 12.3 14.9 18.7
 // Whole tiles want the chip full, which a row an expert, met by chance, does not tell; they
-// take scales by DMA, whose rows have to be whole words.
+// take scales by DMA, so at a word's boundary.
 hipError_t launch_grouped_gemm_mxfp4_rows(const Fp4Args& a, int64_t pairs, hipStream_t stream) {
     if (pairs == 0) return hipSuccess;
     const int64_t used = pairs < a.rows.E ? pairs : a.rows.E, mean = (pairs + used - 1) / used;
@@ -578,10 +658,11 @@ hipError_t launch_grouped_gemm_mxfp4_rows(const Fp4Args& a, int64_t pairs, hipSt
         while (split > 1 && a.K < kUnit * split) split /= 2;
         return split;
     };
-    const bool words = a.K % 128 == 0 && ((uintptr_t)a.x_scales | (uintptr_t)a.b_scales) % 4 == 0;
     const int64_t tiles = (mean + kTile - 1) / kTile * used * ((a.N + kTile - 1) / kTile);
-    if (words && ((mean > 1 && tiles >= 192) || (mean > 48 && tiles >= 96) || mean > kTile))
-        return launch_whole(a, pairs, stream);
+    const bool words = a.K % 128 == 0, aligned = ((uintptr_t)a.x_scales | (uintptr_t)a.b_scales) % 4 == 0;
+    const bool full = words ? (mean > 1 && tiles >= 192) || (mean > 48 && tiles >= 96)
+                            : (mean > 48 && tiles >= 192) || (mean > 96 && tiles >= 96);
+    if (aligned && a.K >= 128 && (full || mean > kTile)) return launch_whole(a, pairs, words, stream);
     if (mean <= 6) {
         switch (parts(1)) {
             case 1: return launch<16, 1>(a, pairs, stream);

@@ -430,8 +430,9 @@ ep_status ep_quantize_mxfp4(const ep_handle* h, int64_t rows, int32_t k, int32_t
  *   b, b_scales, out  as ep_grouped_gemm_mxfp4's, and likewise n.
  * Products are exact, and summed in binary32 by the MFMA (a sum's terms more than
  * 23 binary places below its largest are cut off), rounded once. Tiles: 256 columns by
- * R = 256 where k is a multiple of 128, the scales are 4-byte aligned and there are
- * enough of them; otherwise 128 columns by R = 16 for P <= 6 E, by R = 64 above. */
+ * R = 256 (192 for k no multiple of 128) where k is at least 128, the scales are 4-byte
+ * aligned and there are enough of them; otherwise 128 columns by R = 16 for P <= 6 E, by
+ * R = 64 above. */
 ep_status ep_grouped_gemm_mxfp4_rows(const ep_handle* h, const void* a, const void* a_scales, const void* b,
                                      const void* b_scales, int32_t n, int32_t k, void* out, void* stream);
 

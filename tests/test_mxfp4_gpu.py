@@ -257,7 +257,7 @@ def test_whole_tiles_fixed_capacity_and_no_zero_pad(capfd):
     run_whole(capfd, make_handle(routing(counts), len(counts), 64, flags=ops.FLAG_NO_ZERO_PAD), 1032, 640)
 
 
-@pytest.mark.parametrize("k", [128, 384, 1152, 2048])
+@pytest.mark.parametrize("k", [128, 384, 1152, 2048, 160, 416, 1184, 2080, 448])
 def test_whole_tiles_nan_scales(capfd, k):
     """A row's NaN scales stay out of the rows before and behind it, though its last slab's loads run on into the next row."""
     counts = [70, 3, 260, 64] * 8
@@ -278,6 +278,40 @@ def test_whole_tiles_nan_scales(capfd, k):
         assert torch.equal(torch.isnan(out[f:f + n]), nan), e
         x[rows], w[cols] = 0, 0
         assert torch.equal(out[f:f + n][~nan], (x @ w.t()).to(torch.bfloat16)[~nan]), e
+
+
+def run_odd_whole(capfd, h, n, k, seed=0):
+    """A case that whole tiles take whose rows of scales are no whole words."""
+    o, out = run_whole(capfd, h, n, k, seed)
+    os.environ["EP_BUFFER_DEBUG"] = "1"
+    try:
+        capfd.readouterr()
+        call(h, o, out)
+        assert "words 0" in capfd.readouterr().err
+    finally:
+        os.environ.pop("EP_BUFFER_DEBUG", None)
+
+
+@pytest.mark.parametrize("A", [1, 16, 300])
+@pytest.mark.parametrize("k", [160, 416, 992, 1440])
+def test_whole_tiles_of_odd_scales_every_count(capfd, A, k):
+    run_odd_whole(capfd, make_handle(routing(EVERY), len(EVERY), A), 1032, k)
+
+
+@pytest.mark.parametrize("n,k", [(1032, 160), (1040, 192), (1024, 224), (1272, 288), (1280, 480), (1032, 544), (1536, 736),
+                                 (1032, 1056), (1160, 1504), (1032, 1696), (1296, 2016), (1032, 3232), (2056, 7200)])
+def test_whole_tiles_of_odd_scales_sizes(capfd, n, k):
+    """Rows of scales that start at any byte of a word, by any number of groups past a step's
+    eight and a slab's 24; tiles whose last rows and columns end at any byte."""
+    counts = [0, 5, 100, 64, 300, 1, 701, 2] * 3
+    run_odd_whole(capfd, make_handle(routing(counts), len(counts), 1), n, k, seed=n + k)
+
+
+def test_whole_tiles_of_odd_scales_fixed_capacity(capfd):
+    counts = [0, 5, 130, 1, 39, 40, 700, 256] * 4
+    for C in (3, 41, 162, 600):
+        run_odd_whole(capfd, make_handle(routing(counts), len(counts), 1, ops.MODE_FIXED, C), 1032, 672)
+    run_odd_whole(capfd, make_handle(routing(counts), len(counts), 64, flags=ops.FLAG_NO_ZERO_PAD), 1032, 672)
 
 
 def test_whole_tiles_far_offsets(capfd):
