@@ -242,8 +242,9 @@ __global__ __launch_bounds__(64 * kWaves) void k_grouped_gemm_fp4_stream(Fp4Args
 // DMA, two steps deep. Lane (g, r16) of the MFMA reads chunks f(g) and f(g) + 1 (16
 // bytes, 32 codes) of its row, f = 0, 6, 2, 4, whose scales are two neighbouring bytes.
 // Chunk c of row r is stored at c ^ (r / 2 mod 8): with these f a read meets each bank
-// once. Scales move in slabs of four steps, 32 bytes a row, two slabs deep. WORDS: their
-// rows are whole words of four bytes, as the DMA needs them. Otherwise a slab's 32 bytes start at
+// once. Scales move in slabs of four steps, 32 bytes a row, two slabs deep; of 16 rows the
+// first halves, then the second ones, for the banks again. WORDS: their rows are whole
+// words of four bytes, as the DMA needs them. Otherwise a slab's 32 bytes start at
 // the word that a row's part starts in, up to 3 bytes before it, and hold three steps; all
 // rows of a lane are off by the same number of bytes, since 16 of them are whole words.
 // Words that would reach past the tile's last row are left out: the up to 3 scales lost
@@ -322,7 +323,7 @@ struct Sender {
         s = (w >= 4 ? g.b_scales + first_col * groups : g.x_scales + first_row * groups) + (int64_t)r0 * groups;
         if (WORDS) {
             s_bytes = max(0, left * groups);
-            off_s = __umul24(lane >> 1, groups) + 16 * (lane & 1);
+            off_s = __umul24((lane >> 5) * 16 + (lane & 15), groups) + (lane & 16);
         } else {
             const int before = (uintptr_t)s & 3;
             s -= before;
@@ -403,7 +404,8 @@ __device__ __forceinline__ void multiply(const Sender<MI, WORDS>& send, f32x4_t 
     for (int kb = 0; kb < send.steps; ++kb, place = Lds::after(place, 1)) {
         const uint32_t at_a = lds.a(place, SECOND ? 1 : 0) + row, at_b = lds.b(place) + wn * 64 * kStepBytes + row;
         const int slab_of = kb / kSlab, in_slab = kb - kSlab * slab_of;
-        const uint32_t at_s = lds.slab(slab_of) + r16 * kSlabRow + in_slab * 8 + (WORDS ? first & 4 : 0);
+        const uint32_t at_s = lds.slab(slab_of) + (WORDS ? r16 * 16 + (in_slab >> 1) * 256 + (in_slab & 1) * 8 + (first & 4)
+                                                         : r16 * kSlabRow + in_slab * 8);
         u32x4_t fa[2][2 * MI], fb[2][4];
         uint32_t sa[MI], sb[2];  // two pieces' pairs of scales a word
         const auto scales = [&](int piece, int byte) {
