@@ -13,11 +13,12 @@ Mapping to the DeepEP README ("Interfaces and examples"):
   grouped_gemm_fp8             -> the expert GEMM the layout is built for
   dispatch with an old Handle  -> decode_dispatch with cached_handle
 
-Around them, what an expert layer needs next: the experts' BF16 products in the
-three directions of training (grouped_gemm_bf16, ..._grad_input,
-..._grad_weight), their products with 4-bit weights (grouped_gemm_mxfp4), and
-the RMS norm before the dispatch with its backward (rms_norm,
-rms_norm_backward).
+Around them, what an expert layer needs next: the router, which makes topk_idx
+and topk_w (route, balance_loss, route_backward); the experts' BF16 products in
+the three directions of training (grouped_gemm_bf16, ..._grad_input,
+..._grad_weight), their products with 4-bit weights (grouped_gemm_mxfp4) and
+with both operands in 4 bits (quantize_mxfp4, grouped_gemm_mxfp4_rows); and the
+RMS norm before the dispatch with its backward (rms_norm, rms_norm_backward).
 """
 from __future__ import annotations
 
