@@ -76,7 +76,8 @@ def test_pairs(tokens):
 
 # tokens, top-k (1,024 experts), n, k, and the tiles of the header's rule: rows and columns of one
 @pytest.mark.parametrize("tokens,topk,n,k,rows,cols", [
-    (6 * 1024, 1, 5957 * 128 + 8, 64, 16, 128), (8 * 1024, 1, 7281 * 128 + 8, 32, 64, 128), (1 << 26, 16, 264, 128, 256, 256)])
+    (6 * 1024, 1, 5957 * 128 + 8, 64, 16, 128), (8 * 1024, 1, 7281 * 128 + 8, 32, 64, 128), (1 << 26, 16, 264, 128, 256, 256),
+    (1 << 26, 16, 264, 160, 192, 256)])
 def test_tiles_of_a_launch(tokens, topk, n, k, rows, cols):
     """The smallest width past the header's limit of 2^23 - 1 tiles."""
     tiles = lambda w: (tokens * topk // rows + 1024) * -(-w // cols)

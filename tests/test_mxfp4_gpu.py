@@ -118,10 +118,11 @@ def test_values_over_the_input():
 
 
 @pytest.mark.parametrize("f32", [True, False])
-@pytest.mark.parametrize("mode,A,C", [("compact", 1, 0), ("compact", 128, 0), ("fixed", 1, 40), ("fixed", 1, 3)])
+@pytest.mark.parametrize("mode,A,C", [("compact", 1, 0), ("compact", 128, 0), ("fixed", 1, 40), ("fixed", 1, 3), ("unpadded", 64, 0)])
 def test_live_rows_only(mode, A, C, f32):
     """With a handle: rows of pairs, and no other byte."""
-    h = make_handle(routing([0, 5, 130, 1, 39, 40, 0]), 7, A, ops.MODE_FIXED if mode == "fixed" else ops.MODE_COMPACT, C)
+    h = make_handle(routing([0, 5, 130, 1, 39, 40, 0]), 7, A, ops.MODE_FIXED if mode == "fixed" else ops.MODE_COMPACT, C,
+                    flags=ops.FLAG_NO_ZERO_PAD if mode == "unpadded" else 0)
     R = h.cfg.recv_rows_bound()
     for k in (32, 96, 7168):
         x = torch.randn((R, k), generator=gen(k), device="cuda")

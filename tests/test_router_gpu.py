@@ -145,6 +145,25 @@ def test_nan_and_infinity_reach_the_weights():
     assert (idx[:, 0] == 11).all() and not (idx == 12).any()
 
 
+@pytest.mark.parametrize("f32", [True, False])
+@pytest.mark.parametrize("E,k,G,keep", [(160, 6, 1, 1), (256, 8, 8, 3), (257, 4, 1, 1), (700, 32, 1, 1), (1024, 8, 16, 2)])
+def test_nan_and_infinity_among_many_experts(E, k, G, keep, f32):
+    """NaN, infinities and the largest finite numbers of either sign among logits and biases,
+    from a few of a token's experts to all of them."""
+    g, T = gen(E), 80
+    top = 3.3e38                                     # a finite number in either type
+    special = torch.tensor([float("nan"), float("inf"), -float("inf"), top, -top, 0.0, -0.0], device="cuda")
+    pick = lambda *shape: special[torch.randint(0, 7, shape, device="cuda", generator=g)]
+    share = torch.linspace(0, 1, T, device="cuda")[:, None]
+    logits = torch.where(torch.rand((T, E), device="cuda", generator=g) < share, pick(T, E), torch.randn((T, E), device="cuda", generator=g))
+    logits = logits if f32 else logits.to(torch.bfloat16)
+    noise = torch.randn(E, device="cuda", generator=g)
+    odd = torch.where(torch.rand(E, device="cuda", generator=g) < 0.1, pick(E), noise)
+    for bias in (None, torch.zeros(E, device="cuda"), noise, odd, 1e30 * noise):
+        for sigmoid in (0, 1):
+            check_route(ops.Router(E, k, sigmoid, G, keep, 1), logits, bias)
+
+
 def test_masked_tokens_are_not_read():
     """NaN in the padding of a batch goes nowhere."""
     logits = make_logits(gen(2), 6, 48, True)
