@@ -383,6 +383,22 @@ def test_the_same_call_gives_the_same_bits():
         assert all(torch.equal(a, b) for a, b in zip(first, now))
 
 
+@pytest.mark.parametrize("T,E,S", [(8192, 256, 1), (4096, 64, 19), (3000, 1024, 130)])
+def test_balance_again_and_again_in_one_workspace(T, E, S):
+    """Two batches in turn through the same workspace and outputs: what an earlier call left there
+    never shows."""
+    r, g = ops.Router(E, 4), gen(T)
+    off = torch.linspace(0, T, S + 1, device="cuda").int()
+    batches = [(make_logits(g, T, E, True), routing(g, T, E, 4)) for _ in range(2)]
+    want = [tuple(t.clone() for t in ops.balance_loss(r, l, i, off)) for l, i in batches]
+    ws = ops.balance_loss_workspace(r, T, S)
+    out = tuple(torch.empty_like(t) for t in want[0])
+    for rep in range(300):
+        ops.balance_loss(r, *batches[rep % 2], off, *out, workspace=ws)
+        kept = tuple(t.clone() for t in out)
+        assert all(torch.equal(a, b) for a, b in zip(kept, want[rep % 2])), rep
+
+
 def test_two_streams_at_once():
     """Calls on two streams, each with its own workspace, against the same calls one after the other."""
     E, k = 160, 6
