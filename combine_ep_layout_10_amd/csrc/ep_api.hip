@@ -348,7 +348,7 @@ struct BalanceMap {
 };
 
 BalanceMap balance_map(int E, int32_t num_tokens, int32_t num_seqs) {
-    const size_t tile = ep::balance_tile(num_tokens), places = (num_tokens + tile - 1) / tile + num_seqs;
+    const size_t tile = ep::balance_tile(num_tokens, num_seqs), places = (num_tokens + tile - 1) / tile + num_seqs;
     BalanceMap m;
     size_t o = 0;
     auto take = [&](size_t bytes) {
@@ -991,7 +991,7 @@ ep_status ep_balance_loss(const ep_router* r, int32_t num_tokens, const void* lo
     a.score = r->score;
     a.idx_bits = r->idx_bits;
     a.f32 = r->logits_f32;
-    a.tile = ep::balance_tile(num_tokens);
+    a.tile = ep::balance_tile(num_tokens, num_seqs);
     a.chunks = (r->num_experts + 63) / 64;
     hipError_t e = ep::launch_balance_loss(a, (hipStream_t)stream);
     if (e != hipSuccess) return hip_fail(e, "balance loss launch");

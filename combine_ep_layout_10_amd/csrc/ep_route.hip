@@ -632,15 +632,22 @@ __global__ __launch_bounds__(64 * kBalanceWaves<V>) void k_balance_pieces(Balanc
     const int t0 = (int)blockIdx.x * a.tile, t1 = min(t0 + a.tile, a.T);
     if (blockIdx.x == 0 && tid == 0) *a.done = 0;
     int q = a.seq_off != nullptr ? sequence_past(a.seq_off, a.S, t0) : 0;
-    for (; q < a.S; ++q) {
+    for (int at = t0; q < a.S && at < t1; ++q) {
         int from = t0, to = t1;
         if (a.seq_off != nullptr) {
+            int end = a.seq_off[q + 1];
+            if (end <= at) {  // empty: on to the next one that ends behind this place
+                q = max(q, sequence_past(a.seq_off, a.S, at));  // never back, whatever seq_off holds
+                if (q >= a.S) break;
+                end = a.seq_off[q + 1];
+            }
             const int first = a.seq_off[q];
             if (first >= t1) break;
             from = max(t0, first);
-            to = min(t1, a.seq_off[q + 1]);
-            if (from >= to) continue;
+            to = min(t1, end);
         }
+        at = max(at, to);
+        if (from >= to) continue;
         for (int e = tid; e < 64 * V; e += 64 * kWaves) s_count[e] = 0;
         if (tid == 0) s_tokens = 0;
         __syncthreads();

@@ -242,6 +242,19 @@ def test_balance(T, E, k, sigmoid, f32):
         check_balance(r, logits, idx, torch.tensor(cuts, dtype=torch.int32, device="cuda"))
 
 
+@pytest.mark.parametrize("T,S", [(33, 30), (1, 40), (7, 3), (512, 512), (700, 2000), (2048, 100), (20000, 600),
+                                 (40, 1 << 17)])
+def test_balance_of_short_sequences(T, S):
+    """Fewer tokens a sequence than a block takes at once, empty sequences among them, tokens
+    before the first and past the last."""
+    g = gen(T + S)
+    off = torch.sort(torch.randint(T // 20, T + 1, (S + 1,), device="cuda", generator=g).int())[0]
+    for E, k in ((138, 4), (16, 2)):
+        r, logits, idx = ops.Router(E, k, 1), make_logits(g, T, E, True), routing(g, T, E, k)
+        loss, counts, coef = check_balance(r, logits, idx, off)
+        check_backward(r, logits, idx, None, counts, coef, torch.tensor(1.5, device="cuda"), off)
+
+
 def test_balance_of_long_and_of_even_batches():
     g = gen(3)
     T, E = 40000, 8
