@@ -452,8 +452,9 @@ __device__ __forceinline__ bool choose_narrow(const RouteArgs& a, int lane, cons
             x = v == at % V ? lv : x;
             y = v == at % V ? bv : y;
         }
+        constexpr double kLeastKey = SCORES ? kLowest64 : (double)kLowest;  // of keys of this type: the NaN's
         double key = SCORES ? score64(x) + (double)y : (double)x;
-        if (!(key >= kLowest64)) key = kLowest64;  // NaN
+        if (!(key >= kLeastKey)) key = kLeastKey;
         place = 0;
         for (int i = 0; i < n; ++i) {
             const double other = lane_value(key, i);
