@@ -166,6 +166,23 @@ __device__ __forceinline__ float score_terms(int score, const float l[V], float 
     return wave_sum(sum);
 }
 
+// Where all of a token's sigmoids are tiny their sum, or a ratio to it, may underflow, and the
+// shares would be lost. Below 2^-26 a sigmoid is e^l to less than half a unit, so the shares are
+// those of softmax. Such a token is told by its sum, and its shares are taken apart, from logits that
+// are read again: kept in registers they, or a branch between the tokens, would cost all
+// others time. Softmax has a sum that small for rows of -infinity alone, whose shares are 0.
+constexpr float kFaint = 1.4901161e-8f;  // 2^-26
+
+template <int V>
+__device__ __forceinline__ void faint_shares(const void* logits, int f32, int64_t t, int E, int lane, float p[V]) {
+    float l[V];
+    load_logits<V>(logits, f32, t, E, lane, l);
+    const float sum = softmax_terms<V>(l, wave_max_logit<V>(l), p);
+    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+#pragma unroll
+    for (int v = 0; v < V; ++v) p[v] *= inv;
+}
+
 // Orders the LDS accesses of a wave's lanes for the compiler; the hardware keeps them
 // in order.
 __device__ __forceinline__ void wave_lds_fence() {
@@ -668,6 +685,7 @@ __global__ __launch_bounds__(64 * kBalanceWaves<V>) void k_balance_pieces(Balanc
                 load_logits<V>(a.logits, a.f32, u, a.E, lane, l[i]);
             }
             float part[V];
+            bool faint = false;
 #pragma unroll
             for (int v = 0; v < V; ++v) part[v] = 0.0f;
 #pragma unroll
@@ -677,9 +695,30 @@ __global__ __launch_bounds__(64 * kBalanceWaves<V>) void k_balance_pieces(Balanc
                 ++tokens;
                 float x[V], slope[V];
                 const float total = score_terms<V>(a.score, l[i], x, slope);
-                const float inv = total == 0.0f ? 0.0f : 1.0f / total;
+                const float inv = 1.0f / total;
+                faint |= total < kFaint;
 #pragma unroll
                 for (int v = 0; v < V; ++v) part[v] += x[v] * inv;
+            }
+            if (faint) {  // these tokens again, in the same order
+#pragma unroll
+                for (int v = 0; v < V; ++v) part[v] = 0.0f;
+#pragma unroll 1
+                for (int u = t; u < min(to, t + kAhead * kWaves); u += kWaves) {
+                    if (ballot64(lane < a.k && load_id(a.idx, a.idx_bits, (int64_t)u * a.k + min(lane, a.k - 1), a.E) >= 0) == 0) continue;
+                    float x[V], slope[V];
+                    load_logits<V>(a.logits, a.f32, u, a.E, lane, x);
+                    const float total = score_terms<V>(a.score, x, x, slope);
+                    const float inv = 1.0f / total;
+                    if (total < kFaint) {
+                        faint_shares<V>(a.logits, a.f32, u, a.E, lane, x);
+                    } else {
+#pragma unroll
+                        for (int v = 0; v < V; ++v) x[v] *= inv;
+                    }
+#pragma unroll
+                    for (int v = 0; v < V; ++v) part[v] += x[v];
+                }
             }
 #pragma unroll
             for (int v = 0; v < V; ++v) sum[v] += (double)part[v];
@@ -832,7 +871,8 @@ __global__ __launch_bounds__(64 * kRouteWaves) void k_route_backward(RouteBackwa
         int n[V];
         const bool softmax = a.score == EP_SCORE_SOFTMAX;
         const float total = score_terms<V>(a.score, l, s, slope);
-        const float inv = total == 0.0f ? 0.0f : 1.0f / total;
+        const bool faint = total < kFaint;
+        const float inv = faint ? 0.0f : 1.0f / total;  // the loss's part is 0 here then
         if (softmax) {
 #pragma unroll
             for (int v = 0; v < V; ++v) s[v] *= inv;
@@ -922,6 +962,20 @@ __global__ __launch_bounds__(64 * kRouteWaves) void k_route_backward(RouteBackwa
         } else {
 #pragma unroll
             for (int v = 0; v < V; ++v) grad[v] = slope[v] * (u[v] + b[v]);
+            if (in && faint) {  // p (1 - s) (b - sum p b), and 1 - s is 1
+                float p[V], c[V], mean = 0.0f;
+                faint_shares<V>(a.logits, a.f32, t, a.E, lane, p);
+                const int32_t* const row = a.counts + (int64_t)q * a.E;
+                const float f = a.grad_loss[0] * a.coef[q];
+#pragma unroll
+                for (int v = 0; v < V; ++v) {
+                    c[v] = f * (float)(row[min(lane * V + v, a.E - 1)] - row[0]);
+                    mean += p[v] * c[v];
+                }
+                mean = wave_sum(mean);
+#pragma unroll
+                for (int v = 0; v < V; ++v) grad[v] += p[v] * (c[v] - mean);
+            }
         }
     }
     const int e = lane * V;

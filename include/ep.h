@@ -523,7 +523,7 @@ typedef struct {
  * chosen, highest first; among equals the lowest index goes first. Then
  *   topk_w[j] = scale * s[i_j]  or, with renormalize,
  *               scale * s[i_j] / (sum_m s[i_m] + 1e-20),
- * in binary32: the bias steers the choice alone.
+ * in binary32, where a score below 2^-126 may count as 0: the bias steers the choice alone.
  * An expert whose logit or bias is -infinity is never chosen. Where that
  * leaves fewer than k (a group none), the remaining topk_idx are -1 and their
  * weights 0: ep_layout skips such pairs. A key that is NaN counts as the lowest
@@ -546,7 +546,8 @@ size_t ep_balance_loss_workspace_bytes(const ep_router* r, int32_t num_tokens, i
 /* The balance loss of a batch, for every sequence of it, with the counts. A token
  * is routed when one of its topk_idx lies in [0, E); others (padding) enter
  * nothing. With p the shares of a token's scores (softmax: s; sigmoid:
- * s / sum_i s[i]), for every sequence q and expert e
+ * s / sum_i s[i], also where the scores themselves underflow), for every sequence q and
+ * expert e
  *   counts[q, e] = pairs of q's tokens with topk_idx = e,
  *   N_q          = routed tokens of q, Q = sequences with N_q > 0,
  *   coef[q]      = E / (k N_q^2 Q), 0 where N_q is 0;

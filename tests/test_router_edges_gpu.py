@@ -1,13 +1,16 @@
 """The router on the GPU where its formulas are hardest to keep: the lowest finite
-logits beside NaN. References and bounds are test_router_gpu.py's."""
+logits beside NaN, sigmoids that underflow. References and bounds are test_router_gpu.py's."""
+import numpy as np
 import pytest
 import torch
+
+import router_reference as ref
 
 pytestmark = pytest.mark.gpu
 
 if torch.cuda.is_available():
     from combine_ep_layout_10_amd import ops
-    from test_router_gpu import check_route
+    from test_router_gpu import U, check_route, gen, routing
 
 
 @pytest.mark.parametrize("E,k,G,keep", [(24, 3, 1, 1), (100, 4, 4, 2), (128, 8, 1, 1), (160, 6, 1, 1), (256, 8, 8, 3),
@@ -30,3 +33,93 @@ def test_nan_ties_with_the_lowest_logit(E, k, G, keep):
     for sigmoid in (0, 1):
         for renorm in (False, True):
             check_route(ops.Router(E, k, sigmoid, G, keep, 1, renorm), logits)
+
+
+# ---------------------------------------------------------------- sigmoids that underflow
+
+def shares(l):
+    """Shares of sigmoid scores, with the scores and one minus them, of any finite or infinite logits: from logarithms."""
+    up, down = -np.logaddexp(0, -l), -np.logaddexp(0, l)
+    top = up.max(1, keepdims=True)
+    x = np.exp(up - np.where(np.isfinite(top), top, 0.0))
+    total = x.sum(1, keepdims=True)
+    return x / np.where(total == 0, 1.0, total), np.exp(up), np.exp(down)
+
+
+def faint_logits(g, E, f32):
+    """Rows whose highest logit lies at many levels below 0, from where 1 + e^l is 1 in binary32 to where e^l is 0,
+    some with an ordinary logit or closed experts among them."""
+    levels = [-12.0, -16.0, -17.5, -18.5, -21.0, -40.0, -80.0, -87.0, -88.5, -95.0, -104.0, -110.0, -300.0, -2000.0, -3e4]
+    l = torch.tensor(levels, device="cuda").repeat_interleave(3)[:, None] + 1.5 * torch.randn((45, E), generator=g, device="cuda")
+    l[1::3, E // 2] = -torch.inf
+    l[2::9, E // 3] = 0.25
+    flat = torch.full((3, E), -1e30, device="cuda")
+    flat[1], flat[2, 0] = torch.finfo(torch.float32).min / 2, -torch.inf
+    l = torch.cat([l, flat])
+    return l if f32 else l.to(torch.bfloat16)
+
+
+def reach(l):
+    """What the exponentials' arguments can be off by, in units of 2^-24: a row's spread, as far as a term counts,
+    and the 30 that an ordinary sigmoid's argument has before e^l drops out of 1 + e^l."""
+    l = np.where(np.isfinite(l), l, np.nan)
+    return min(111.0, np.nanmax(np.nanmax(l, 1) - np.nanmin(l, 1))) + 30.0
+
+
+@pytest.mark.parametrize("f32", [True, False])
+@pytest.mark.parametrize("E,k", [(5, 2), (64, 4), (250, 8), (256, 8), (700, 8), (1024, 3)])
+def test_shares_of_sigmoids_that_underflow(E, k, f32):
+    """Balance loss and gradient where all of a token's sigmoids are tiny or 0 in binary32: the shares are ratios
+    and stay. The weights' part of the gradient has the scores themselves, which are 0 below 2^-126: its bound
+    adds what that times its other factor makes."""
+    g = gen(E)
+    logits = faint_logits(g, E, f32)
+    T = logits.shape[0]
+    idx = routing(g, T, E, k, dropped=0.1)
+    l, ids = logits.double().cpu().numpy(), idx.cpu().numpy()
+    p, s, rest = shares(l)
+    R, out = reach(l), U if f32 else 2.0 ** -8
+    live = (ids >= 0) & (ids < E)
+    grad_w = torch.randn((T, k), generator=g, device="cuda")
+    gw, grad_loss = grad_w.double().cpu().numpy(), torch.tensor(0.7, device="cuda")
+    n, ge, ga = (np.zeros((T, E)) for _ in range(3))
+    for t, j in zip(*np.nonzero(live)):
+        n[t, ids[t, j]] += 1
+        ge[t, ids[t, j]] += gw[t, j]
+        ga[t, ids[t, j]] += abs(gw[t, j])
+    for cuts in (None, list(range(T + 1)), [0, T // 3, T // 3, T - 1]):
+        off = None if cuts is None else torch.tensor(cuts, dtype=torch.int32, device="cuda")
+        r = ops.Router(E, k, ops.SCORE_SIGMOID)
+        loss, counts, coef = ops.balance_loss(r, logits, idx, off)
+        c, f = counts.double().cpu().numpy(), coef.double().cpu().numpy()
+        at = np.zeros(T, int) if cuts is None else np.searchsorted(cuts, np.arange(T), side="right") - 1
+        inside, at = at < len(f), np.minimum(at, len(f) - 1)
+        routed = live.any(1)
+        want = float((f[at] * (p * c[at]).sum(1))[inside & routed].sum())
+        ref.close(loss.item(), want, (2 * R + 60) * U * want, "loss")
+        scale = 0.7 * (f[at] * inside)[:, None]
+        c = c[at]
+        c = c - c[:, :1]  # a constant of all counts changes nothing, and would hide shares far below 2^-53 here
+        b, ba = scale * (c - (p * c).sum(1, keepdims=True)), scale * (abs(c) + (p * abs(c)).sum(1, keepdims=True))
+        for weights, renorm in ((None, False), (grad_w, False), (grad_w, True)):
+            u, ua = np.zeros((T, E)), np.zeros((T, E))
+            if weights is not None:
+                u, ua = ge, ga
+                if renorm:
+                    D = (n * s).sum(1, keepdims=True) + 1e-20
+                    u, ua = (ge - n * (ge * s).sum(1, keepdims=True) / D) / D, (ga + n * (ga * s).sum(1, keepdims=True) / D) / D
+            r = ops.Router(E, k, ops.SCORE_SIGMOID, renormalize=renorm)
+            got = ops.route_backward(r, logits, idx, weights, counts, coef, grad_loss, off)
+            want = np.where(routed[:, None], s * rest * u + p * rest * b, 0.0)
+            size = s * rest * ua + p * rest * ba
+            ref.close(got.double().cpu().numpy(), want,
+                      (8 * R + 240) * U * size + out * abs(want) + 1e-37 + 2.0 ** -126 * ua, "gradient %s %s" % (cuts is None, renorm))
+
+
+def test_equal_faint_sigmoids_have_equal_shares():
+    """The same logit for all experts, however low: shares of 1 / E, and a loss of 1 for an even choice."""
+    E, T = 64, 32
+    idx = torch.arange(2 * T, device="cuda").view(T, 2) % E
+    for level in (0.0, -20.0, -87.5, -90.0, -103.0, -104.0, -500.0, -1e30):
+        loss, counts, coef = ops.balance_loss(ops.Router(E, 2, 1), torch.full((T, E), level, device="cuda"), idx)
+        assert abs(loss.item() - 1.0) <= 60 * U, level
