@@ -1023,7 +1023,7 @@ hipError_t launch_route(RouteArgs a, hipStream_t stream) {
     while (64 * V < a.E) V *= 2;
     const int size = a.E / a.G, lanes = size / V;
     a.group_lanes = size % V == 0 && (lanes & (lanes - 1)) == 0 ? lanes : 0;
-    const bool full = a.bias != nullptr || (a.G > 1 && a.best > 1);
+    const bool full = a.bias != nullptr || a.best > 1;  // also where all groups stay: equal scores tie
     // scores of bf16 logits alone tie too often
     a.narrow = (!full || a.f32 || a.bias != nullptr) && (a.G == 1 || a.group_lanes > 0);
     const dim3 grid((unsigned)((a.T + kRouteWaves - 1) / kRouteWaves)), block(64 * kRouteWaves);

@@ -1,5 +1,6 @@
 """The router on the GPU where its formulas are hardest to keep: the lowest finite
-logits beside NaN, sigmoids that underflow. References and bounds are test_router_gpu.py's."""
+logits beside NaN, sigmoids that underflow, scores that are equal where their logits are not.
+References and bounds are test_router_gpu.py's."""
 import numpy as np
 import pytest
 import torch
@@ -123,3 +124,22 @@ def test_equal_faint_sigmoids_have_equal_shares():
     for level in (0.0, -20.0, -87.5, -90.0, -103.0, -104.0, -500.0, -1e30):
         loss, counts, coef = ops.balance_loss(ops.Router(E, 2, 1), torch.full((T, E), level, device="cuda"), idx)
         assert abs(loss.item() - 1.0) <= 60 * U, level
+
+
+# ---------------------------------------------------------------- scores as keys
+
+@pytest.mark.parametrize("f32", [True, False])
+@pytest.mark.parametrize("E,k,G,keep", [(24, 4, 1, 1), (64, 6, 8, 8), (128, 8, 4, 4), (256, 8, 1, 1), (256, 8, 8, 8), (256, 8, 8, 4),
+                                        (700, 9, 1, 1), (1024, 32, 16, 16)])
+def test_scores_are_the_keys_where_two_of_a_group_count(E, k, G, keep, f32):
+    """With group_best 2 a key is the score in binary64, whether groups are dropped or not: sigmoids of logits from
+    40 on are 1 there, and terms 800 below a row's largest logit 0, so those experts tie and the lowest
+    index goes first."""
+    g = gen(E)
+    high = 40.0 + 20.0 * torch.rand((6, E), generator=g, device="cuda")
+    some = torch.where(torch.rand((6, E), generator=g, device="cuda") < 0.9, -800.0 - high, -high)
+    some[:, 1] = 0.0
+    logits = torch.cat([high, some])
+    logits = logits if f32 else logits.to(torch.bfloat16)
+    check_route(ops.Router(E, k, ops.SCORE_SIGMOID, G, keep, 2), logits[:6])
+    check_route(ops.Router(E, k, ops.SCORE_SOFTMAX, G, keep, 2), logits[6:])
