@@ -1,6 +1,7 @@
 """The router on the GPU where its formulas are hardest to keep: the lowest finite
-logits beside NaN, sigmoids that underflow, scores that are equal where their logits are not.
-References and bounds are test_router_gpu.py's."""
+logits beside NaN, sigmoids that underflow, scores that are equal where their logits are not,
+logits past 2^31. References and bounds are
+test_router_gpu.py's."""
 import numpy as np
 import pytest
 import torch
@@ -11,7 +12,7 @@ pytestmark = pytest.mark.gpu
 
 if torch.cuda.is_available():
     from combine_ep_layout_10_amd import ops
-    from test_router_gpu import U, check_route, gen, routing
+    from test_router_gpu import U, check_route, gen, make_logits, routing
 
 
 @pytest.mark.parametrize("E,k,G,keep", [(24, 3, 1, 1), (100, 4, 4, 2), (128, 8, 1, 1), (160, 6, 1, 1), (256, 8, 8, 3),
@@ -143,3 +144,60 @@ def test_scores_are_the_keys_where_two_of_a_group_count(E, k, G, keep, f32):
     logits = logits if f32 else logits.to(torch.bfloat16)
     check_route(ops.Router(E, k, ops.SCORE_SIGMOID, G, keep, 2), logits[:6])
     check_route(ops.Router(E, k, ops.SCORE_SOFTMAX, G, keep, 2), logits[6:])
+
+
+@pytest.mark.parametrize("sigmoid", [0, 1])
+@pytest.mark.parametrize("E,k,G,keep", [(60, 6, 4, 2), (128, 8, 8, 3), (160, 6, 8, 3), (256, 8, 8, 4), (256, 8, 8, 8), (512, 10, 64, 9),
+                                        (384, 8, 8, 3), (1024, 32, 64, 2), (1024, 8, 1, 1)])
+def test_two_of_a_group_of_bf16_logits(E, k, G, keep, sigmoid):
+    """bf16 logits without a bias, which tie. Two groups' sums of different scores may be equal but for their last
+    bit (s(x) + s(-x) is 1), and then either may go first: tokens whose sums at the border lie within 1e-12 without being
+    sums of the same logits are left out, all others compared exactly."""
+    g, T = gen(E + k), 200
+    logits = make_logits(g, T, E, False)
+    clear = torch.ones(T, dtype=torch.bool)
+    if keep < G:
+        top = logits.double().cpu().view(T, G, -1).topk(2, 2).values.numpy()
+        for t in range(T):
+            s = np.exp(top[t] - logits[t].double().max().item()) if not sigmoid else 1.0 / (1.0 + np.exp(-top[t]))
+            total = 1.0 if sigmoid else np.exp(logits[t].double().cpu().numpy() - logits[t].double().max().item()).sum()
+            sums = s.sum(1) / total
+            order = np.argsort(-sums, kind="stable")
+            border = sums[order[keep - 1]]
+            for a in order:
+                for b in order:
+                    if abs(sums[a] - border) < 1e-12 and abs(sums[b] - border) < 1e-12 and not np.array_equal(top[t][a], top[t][b]):
+                        clear[t] = False
+    assert clear.sum() >= T // 2
+    for renorm in (False, True):
+        check_route(ops.Router(E, k, sigmoid, G, keep, 2, renorm), logits[clear.cuda()].contiguous())
+
+
+# ---------------------------------------------------------------- far rows
+
+@pytest.mark.parametrize("E,f32", [(1024, True), (1000, False), (999, True)])
+def test_rows_past_2_31_logits(E, f32):
+    """Tokens whose logits start past 2^31 elements (8 GB in binary32): all calls give them what they give a batch of those
+    tokens alone."""
+    k, last = 8, 70
+    T = (1 << 31) // E + last + 1
+    g = gen(E)
+    logits = torch.zeros((T, E), device="cuda", dtype=torch.float32 if f32 else torch.bfloat16)
+    logits[-last:] = make_logits(g, last, E, f32)
+    some = logits[-last:].clone()
+    bias = 0.2 * torch.randn(E, generator=g, device="cuda")
+    r = ops.Router(E, k, ops.SCORE_SIGMOID, renormalize=True)
+    idx, w = ops.route(r, logits, bias)
+    few_idx, few_w = check_route(r, some, bias)
+    assert torch.equal(idx[-last:], few_idx) and torch.equal(w[-last:], few_w)
+    # the last tokens as two sequences, those before them none
+    off = torch.tensor([T - last, T - 30, T], dtype=torch.int32, device="cuda")
+    loss, counts, coef = ops.balance_loss(r, logits, idx, off)
+    want, want_counts, want_coef, _ = ref.balance(some, few_idx, [0, last - 30, last], r)
+    assert np.array_equal(counts.cpu().numpy(), want_counts)
+    ref.close(coef.cpu().numpy(), want_coef, 2 * U * want_coef, "coef")
+    ref.close(loss.item(), want, (2 * ref.spread(some) + 60) * U * want, "loss")
+    # written over the logits
+    few = ops.route_backward(r, some, few_idx, few_w, counts, coef, loss, off - (T - last))
+    grad = ops.route_backward(r, logits, idx, w, counts, coef, loss, off, grad_logits=logits)
+    assert torch.equal(grad[-last:], few) and few.any()
