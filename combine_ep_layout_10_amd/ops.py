@@ -62,8 +62,36 @@ SCORE_SOFTMAX = F.EP_SCORE_SOFTMAX
 SCORE_SIGMOID = F.EP_SCORE_SIGMOID
 
 
+class _Sizes:
+    """What Config and Router share: their C struct, built at the first call that needs
+    it, kept with its address as one value (so whichever of two threads comes first,
+    the address is that of the struct that stays)."""
+
+    def _struct(self):
+        raise NotImplementedError
+
+    def _keep(self):
+        c = self._struct()
+        return self.__dict__.setdefault("_c", (c, ctypes.addressof(c)))
+
+    def c(self):
+        """The C struct, built once per instance."""
+        return (self.__dict__.get("_c") or self._keep())[0]
+
+    def c_addr(self) -> int:
+        """Its address, which the compiled binding reads."""
+        return (self.__dict__.get("_c") or self._keep())[1]
+
+    # copies and pickles carry the fields alone: an address is another object's, or another process's
+    def __getstate__(self):
+        return {f.name: getattr(self, f.name) for f in dataclasses.fields(self)}
+
+    def __setstate__(self, state):
+        self.__dict__.update((f.name, state[f.name]) for f in dataclasses.fields(self))
+
+
 @dataclasses.dataclass(frozen=True)
-class Config:
+class Config(_Sizes):
     max_tokens: int
     hidden: int
     num_experts: int
@@ -75,23 +103,9 @@ class Config:
     idx_bits: int = 64
     flags: int = 0
 
-    def c(self) -> F.ep_config:
-        """The C struct, built once per Config (cached on the instance)."""
-        c = self.__dict__.get("_c_struct")
-        if c is None:
-            c = F.ep_config(self.max_tokens, self.hidden, self.num_experts, self.num_topk, self.num_dests,
-                            self.expert_alignment, self.capacity, self.mode, self.idx_bits, self.flags)
-            object.__setattr__(self, "_c_struct", c)
-            object.__setattr__(self, "_c_addr", ctypes.addressof(c))
-        return c
-
-    def c_addr(self) -> int:
-        """Address of the cached C struct (the compiled binding reads it)."""
-        a = self.__dict__.get("_c_addr")
-        if a is None:
-            self.c()
-            a = self.__dict__["_c_addr"]
-        return a
+    def _struct(self) -> F.ep_config:
+        return F.ep_config(self.max_tokens, self.hidden, self.num_experts, self.num_topk, self.num_dests,
+                           self.expert_alignment, self.capacity, self.mode, self.idx_bits, self.flags)
 
     def workspace_bytes(self) -> int:
         n = F.ep_workspace_bytes(self.c())
@@ -464,7 +478,7 @@ def rms_norm_backward(total: torch.Tensor, weight: torch.Tensor, rstd: torch.Ten
 # ---------------------------------------------------------------- router
 
 @dataclasses.dataclass(frozen=True)
-class Router:
+class Router(_Sizes):
     """Sizes and rule of a router. Logits may be float32 or bfloat16 in any call."""
     num_experts: int
     num_topk: int
@@ -476,23 +490,9 @@ class Router:
     scale: float = 1.0
     idx_bits: int = 64
 
-    def c(self) -> F.ep_router:
-        """The C struct, built once per Router (cached on the instance)."""
-        c = self.__dict__.get("_c_struct")
-        if c is None:
-            c = F.ep_router(self.num_experts, self.num_topk, self.score, self.num_groups, self.topk_groups,
-                            self.group_best, int(self.renormalize), self.idx_bits, 1, self.scale)
-            object.__setattr__(self, "_c_struct", c)
-            object.__setattr__(self, "_c_addr", ctypes.addressof(c))
-        return c
-
-    def c_addr(self) -> int:
-        """Address of the cached C struct (the compiled binding reads it)."""
-        a = self.__dict__.get("_c_addr")
-        if a is None:
-            self.c()
-            a = self.__dict__["_c_addr"]
-        return a
+    def _struct(self) -> F.ep_router:
+        return F.ep_router(self.num_experts, self.num_topk, self.score, self.num_groups, self.topk_groups,
+                           self.group_best, int(self.renormalize), self.idx_bits, 1, self.scale)
 
 
 def route(router: Router, logits: torch.Tensor, bias: Optional[torch.Tensor] = None,
