@@ -256,7 +256,7 @@ def _run_own(state, op):
     if op == "backward":
         return ops.route_backward(state["router"], state["logits"], state["idx"], grad_topk_w=state["grad_w"],
                                   counts=state.get("counts"), coef=state.get("coef"), grad_loss=state.get("grad_loss"),
-                                  seq_off=state["seq_off"])
+                                  seq_off=state["seq_off"] if case["loss"] else None)  # read with the counts alone
     if op == "quantize":
         if "live" not in state:
             values = torch.empty(state["x"].shape, dtype=torch.bfloat16, device="cuda") if case["values"] else None
