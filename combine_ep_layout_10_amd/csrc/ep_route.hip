@@ -745,7 +745,9 @@ __global__ __launch_bounds__(64 * kBalanceWaves<V>) void k_balance_pieces(Balanc
 // parts in order, so that nothing depends on which one that is. What passes between blocks
 // are atomic stores and loads at agent scope, which go past the caches that blocks do not
 // share, so that waiting for the stores orders them before the count; a release would
-// write the whole L2 back first (the batch of 8192 x 256: 12.2 us for 10.7).
+// write the whole L2 back first (the batch of 8192 x 256: 12.2 us for 10.7). The language does
+// not order relaxed accesses: the instructions that they become do, which
+// tests/test_balance_order.py reads, so none of them may become a plain one.
 __global__ __launch_bounds__(1024) void k_balance_loss(BalanceArgs a) {
     __shared__ double s_sum[16][64];
     __shared__ int s_pairs[16][64];
