@@ -5,7 +5,7 @@
 // binary32, and the only other rounding is the output's.
 //
 // The weights go from memory straight into registers; a block of 8 waves takes up to
-// TB rows of one expert by 128 MC / S output columns. A wave's piece is 16 MC columns
+// TB rows of one expert by 128 / S output columns. A wave's piece is 16 columns
 // of the weights as the MFMA's first operand. The reduction runs in units of 512: lane
 // (g, r16) reads codes 128 g .. + 127 of its column (four 16-byte loads) with their
 // four scales (one word), and MFMA t takes the t-th 32 of each group, so its scale is byte t.
@@ -56,7 +56,7 @@ struct Slice {
 };
 
 // Rows m0 .. m0 + rows - 1 of the expert (rows <= 16 NT) by the block's columns.
-template <int TB, int MC, int S, int NT>
+template <int TB, int S, int NT>
 __device__ __forceinline__ void run_tile(const Fp4Args& a, const ExpertRows& er, int e, int m0, int rows, int n0,
                                          uint8_t* s_x) {
     using L = Slice<TB, S>;
@@ -68,8 +68,8 @@ __device__ __forceinline__ void run_tile(const Fp4Args& a, const ExpertRows& er,
     const int ks = w / (kWaves / S), cw = w % (kWaves / S);
     const int half = a.K / 2, groups = a.K / 32;  // bytes of a row's codes and scales
     const int slices = (a.K + NC * kUnit - 1) / (NC * kUnit);
-    const int c0 = n0 + 16 * MC * cw;
-    const int cols = max(0, min(16 * MC, a.N - c0));
+    const int c0 = n0 + 16 * cw;
+    const int cols = max(0, min(16, a.N - c0));
     const int64_t first_col = (int64_t)e * a.N + min(c0, a.N - 1), first_row = (int64_t)er.first + m0;
     const __amdgpu_buffer_rsrc_t rw = resource(a.b + first_col * half, cols * half);
     const __amdgpu_buffer_rsrc_t rx = resource(a.x + first_row * half, rows * half);
@@ -77,21 +77,16 @@ __device__ __forceinline__ void run_tile(const Fp4Args& a, const ExpertRows& er,
     const uint8_t* const x_scales = a.x_scales + first_row * groups;
 
     const uint32_t select = (uint32_t)(0x0400 + 0x0101 * g);  // bytes g of two words, as v_perm_b32 names them
-    u32x4_t code[P][MC][4];
-    uint32_t scale[P][MC];
+    u32x4_t code[P][4];
+    uint32_t scale[P];
     // unit u of the reduction; columns past N, and the reduction past K, are zero
     const auto load = [&](int u, int p) {
 #pragma unroll
-        for (int c = 0; c < MC; ++c) {
-#pragma unroll
-            for (int t = 0; t < 4; ++t) {
-                const int byte = u * 256 + t * 64 + g * 16;
-                code[p][c][t] = __builtin_amdgcn_raw_buffer_load_b128(
-                    rw, byte < half ? (16 * c + r16) * half + byte : kOutOfRange, 0, 0);
-            }
-            scale[p][c] = load_scales4(w_scales + (int64_t)min(16 * c + r16, max(cols - 1, 0)) * groups,
-                                       u * 16 + g * 4, groups);
+        for (int t = 0; t < 4; ++t) {
+            const int byte = u * 256 + t * 64 + g * 16;
+            code[p][t] = __builtin_amdgcn_raw_buffer_load_b128(rw, byte < half ? r16 * half + byte : kOutOfRange, 0, 0);
         }
+        scale[p] = load_scales4(w_scales + (int64_t)min(r16, max(cols - 1, 0)) * groups, u * 16 + g * 4, groups);
     };
     u32x4_t xr[XL];
     uint32_t xs[SL];
@@ -130,11 +125,9 @@ __device__ __forceinline__ void run_tile(const Fp4Args& a, const ExpertRows& er,
     load_rows(0);
 #pragma unroll
     for (int p = 0; p < P; ++p) load(ks * B + p, p);
-    f32x4_t acc[NT][MC];
+    f32x4_t acc[NT];
 #pragma unroll
-    for (int n = 0; n < NT; ++n)
-#pragma unroll
-        for (int c = 0; c < MC; ++c) acc[n][c] = (f32x4_t){0.0f, 0.0f, 0.0f, 0.0f};
+    for (int n = 0; n < NT; ++n) acc[n] = (f32x4_t){0.0f, 0.0f, 0.0f, 0.0f};
     store_rows(0);
     wait_lgkmcnt0();
     block_barrier();
@@ -151,19 +144,14 @@ __device__ __forceinline__ void run_tile(const Fp4Args& a, const ExpertRows& er,
 #pragma unroll
             for (int n = 0; n < NT; ++n)
                 row_scale[n] = *(const uint32_t*)(x + L::kCodes + (16 * n + r16) * L::kPitch + u * 16 + g * 4);
-            uint32_t col_scale[MC];
-#pragma unroll
-            for (int c = 0; c < MC; ++c)
-                col_scale[c] = scales_by_mfma(place_scales4(scale[p][c], (kc * NC + u) * 16 + g * 4, groups), select);
+            const uint32_t col_scale = scales_by_mfma(place_scales4(scale[p], (kc * NC + u) * 16 + g * 4, groups), select);
             const auto part = [&](auto tt) {
                 constexpr int t = decltype(tt)::value;
 #pragma unroll
                 for (int n = 0; n < NT; ++n) {
                     const u32x4_t v = *(const u32x4_t*)(x + (16 * n + r16) * (NC * 256) +
                                                         ((16 * u + ((4 * t + g) ^ row_slot(r16))) << 4));
-#pragma unroll
-                    for (int c = 0; c < MC; ++c)
-                        acc[n][c] = mfma_fp4<t, t>(code[p][c][t], v, acc[n][c], col_scale[c], row_scale[n]);
+                    acc[n] = mfma_fp4<t, t>(code[p][t], v, acc[n], col_scale, row_scale[n]);
                 }
             };
             part(std::integral_constant<int, 0>());
@@ -182,9 +170,7 @@ __device__ __forceinline__ void run_tile(const Fp4Args& a, const ExpertRows& er,
         f32x4_t* sum = (f32x4_t*)s_x;
         if (ks > 0) {
 #pragma unroll
-            for (int n = 0; n < NT; ++n)
-#pragma unroll
-                for (int c = 0; c < MC; ++c) sum[((w * NT + n) * MC + c) * 64 + lane] = acc[n][c];
+            for (int n = 0; n < NT; ++n) sum[(w * NT + n) * 64 + lane] = acc[n];
         }
         wait_lgkmcnt0();
         block_barrier();
@@ -192,26 +178,21 @@ __device__ __forceinline__ void run_tile(const Fp4Args& a, const ExpertRows& er,
 #pragma unroll
         for (int s = 1; s < S; ++s)
 #pragma unroll
-            for (int n = 0; n < NT; ++n)
-#pragma unroll
-                for (int c = 0; c < MC; ++c)
-                    acc[n][c] += sum[(((s * (kWaves / S) + cw) * NT + n) * MC + c) * 64 + lane];
+            for (int n = 0; n < NT; ++n) acc[n] += sum[((s * (kWaves / S) + cw) * NT + n) * 64 + lane];
     }
     // lane: row r16 of each piece, columns 4 g .. 4 g + 3
 #pragma unroll
-    for (int n = 0; n < NT; ++n)
-#pragma unroll
-        for (int c = 0; c < MC; ++c) {
-            const int row = 16 * n + r16, col = c0 + 16 * c + 4 * g;
-            if (row < rows && col < a.N)
-                *(uint2*)(a.out + (first_row + row) * a.N + col) =
-                    make_uint2(pack_bf16x2(acc[n][c][0], acc[n][c][1]), pack_bf16x2(acc[n][c][2], acc[n][c][3]));
-        }
+    for (int n = 0; n < NT; ++n) {
+        const int row = 16 * n + r16, col = c0 + 4 * g;
+        if (row < rows && col < a.N)
+            *(uint2*)(a.out + (first_row + row) * a.N + col) =
+                make_uint2(pack_bf16x2(acc[n][0], acc[n][1]), pack_bf16x2(acc[n][2], acc[n][3]));
+    }
 }
 
-template <int TB, int MC, int S>
+template <int TB, int S>
 __global__ __launch_bounds__(64 * kWaves) void k_grouped_gemm_fp4_stream(Fp4Args a) {
-    constexpr int kCols = 16 * MC * kWaves / S;
+    constexpr int kCols = 16 * kWaves / S;
     __shared__ __attribute__((aligned(16))) uint8_t s_x[2 * Slice<TB, S>::kBytes];
     const int nt_n = (a.N + kCols - 1) / kCols;
     int e, local;
@@ -226,12 +207,12 @@ __global__ __launch_bounds__(64 * kWaves) void k_grouped_gemm_fp4_stream(Fp4Args
     const int rows = __builtin_amdgcn_readfirstlane(min(each, er.live - m0));
     const int n0 = __builtin_amdgcn_readfirstlane(local / nt_m * kCols);
     if (a.rows.zero_pad && m == nt_m - 1) clear_padding<kCols>(a.out, a.N, er, n0);
-    if (TB == 16) return run_tile<TB, MC, S, 1>(a, er, e, m0, rows, n0, s_x);
+    if (TB == 16) return run_tile<TB, S, 1>(a, er, e, m0, rows, n0, s_x);
     switch ((rows + 15) / 16) {
-        case 1: return run_tile<TB, MC, S, 1>(a, er, e, m0, rows, n0, s_x);
-        case 2: return run_tile<TB, MC, S, TB == 64 ? 2 : 1>(a, er, e, m0, rows, n0, s_x);
-        case 3: return run_tile<TB, MC, S, TB == 64 ? 3 : 1>(a, er, e, m0, rows, n0, s_x);
-        default: return run_tile<TB, MC, S, TB == 64 ? 4 : 1>(a, er, e, m0, rows, n0, s_x);
+        case 1: return run_tile<TB, S, 1>(a, er, e, m0, rows, n0, s_x);
+        case 2: return run_tile<TB, S, TB == 64 ? 2 : 1>(a, er, e, m0, rows, n0, s_x);
+        case 3: return run_tile<TB, S, TB == 64 ? 3 : 1>(a, er, e, m0, rows, n0, s_x);
+        default: return run_tile<TB, S, TB == 64 ? 4 : 1>(a, er, e, m0, rows, n0, s_x);
     }
 }
 
@@ -605,7 +586,7 @@ hipError_t launch(const Fp4Args& a, int64_t pairs, hipStream_t stream) {
     if (launch_debug())
         launch_debug_print("k_grouped_gemm_fp4_stream", dim3((unsigned)blocks), dim3(64 * kWaves),
                            "rows %d split %d n %d k %d", TB, S, a.N, a.K);
-    hipLaunchKernelGGL((k_grouped_gemm_fp4_stream<TB, 1, S>), dim3((unsigned)blocks), dim3(64 * kWaves), 0, stream, a);
+    hipLaunchKernelGGL((k_grouped_gemm_fp4_stream<TB, S>), dim3((unsigned)blocks), dim3(64 * kWaves), 0, stream, a);
     return hipGetLastError();
 }
 
