@@ -563,8 +563,8 @@ size_t ep_balance_loss_workspace_bytes(const ep_router* r, int32_t num_tokens, i
  *   coef        device binary32 [num_seqs].
  *   workspace   device, >= ep_balance_loss_workspace_bytes, 256-byte aligned; not
  *               to be shared by calls that may overlap.
- * Sums over tokens are taken in an order that depends on the sizes and seq_off
- * alone. num_tokens is at most 2^25, num_seqs 2^17. Two launches. */
+ * Sums over tokens are taken in an order that depends on the sizes, seq_off and which
+ * tokens' sigmoids are all tiny. num_tokens is at most 2^25, num_seqs 2^17. Two launches. */
 ep_status ep_balance_loss(const ep_router* r, int32_t num_tokens, const void* logits, const void* topk_idx,
                           const int32_t* seq_off, int32_t num_seqs, float* loss, int32_t* counts, float* coef,
                           void* workspace, size_t workspace_bytes, void* stream);
