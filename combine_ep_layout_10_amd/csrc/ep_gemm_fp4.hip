@@ -243,7 +243,8 @@ __global__ __launch_bounds__(64 * kWaves) void k_grouped_gemm_fp4_stream(Fp4Args
 // What is sent has 2 S - 2 intervals to land. S is 2, and 3 for tiles of up to 64 rows, which
 // wait for the weights (1,024 rows on 64 experts, 4096 x 7168: 177 us, with two steps 193).
 //
-// 65,536 rows on 32 experts, 4096 x 7168: 0.96 ms (4.0 PFLOP/s), without WORDS 1.34. MFMAs are
+// 65,536 rows on 32 experts, 4096 x 7168: 0.98 ms settled (0.96 to 0.99 from card to card, 3.9
+// PFLOP/s), without WORDS 1.34. MFMAs are
 // 55 % busy, at the 1.6 to 1.7 GHz that power leaves; without the DMA it is 0.78 ms, with MFMAs,
 // barriers and stores alone 0.73.
 constexpr int kTile = 256;
@@ -630,6 +631,19 @@ hipError_t launch_whole(const Fp4Args& a, int64_t pairs, bool words, hipStream_t
 //   top-3 of 24 experts, 1000 x 1440 (96 whole tiles)     6   12   38   64  188
 //     64 rows                                           7.7  8.0  9.3 13.7 21.7
 //     whole tiles                                      12.0 12.0 12.3 14.9 18.7
+// Routing that is uneven, the j-th expert's share as j^-1.2, mean rows:
+//   top-8 of 64 experts, 4096 x 7168                       2    8        32
+//     64 rows                                            121  196       260
+//     whole tiles                                        117  164       234
+//   top-1 of 8 experts, 4096 x 7168                       16   32   48   64   96  128
+//     64 rows                                           33.6 52.6 50.7 51.5 58.6 74.9
+//     whole tiles                                       33.5 47.3 51.7 57.0 51.8 55.1
+//   top-3 of 24 experts, 1000 x 1440                      12   38   64  100  188
+//     64 rows                                            8.9 10.2 13.3 13.8 20.6
+//     whole tiles                                       14.3 17.1 17.7 18.0 18.8
+// The rule has the mean alone, and loses up to 11 % at its limits there, 30 % at the last one's;
+// at that one's 12 and 38 rows it splits the reduction in two, which takes 12.3 and 12.8 (10.9 and 12.9
+// where routing is even).
 // Whole tiles want the chip full, which a row an expert, met by chance, does not tell; they
 // take scales by DMA, so at a word's boundary.
 hipError_t launch_grouped_gemm_mxfp4_rows(const Fp4Args& a, int64_t pairs, hipStream_t stream) {

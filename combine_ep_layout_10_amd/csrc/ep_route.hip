@@ -11,8 +11,10 @@
 // compared one after the other: the higher one decides unless two experts share it.
 //
 // Bound by instructions, and for few tokens by the launches. 8192 tokens x 256 experts in
-// binary32, us: choice (sigmoid, bias, 4 of 8 groups) 8.9, loss 10.7 (two launches), gradient
-// of both 7.3; the logits alone take 1.4 us to read (6.1 TB/s). 128 tokens: choice 4.0.
+// binary32, settled times of single launches, us: choice (sigmoid, bias, 4 of 8 groups) 9.2, loss
+// 5.7 and 5.4 (two launches), gradient of both 7.7; 128 tokens: choice 4.3. Calls on end
+// overlap a little, 8.9, 10.8, 7.3 and 4.0, and other times in these comments are of those. The
+// logits alone take 1.4 us to read (6.1 TB/s).
 #include <type_traits>
 
 #include "ep_internal.h"
@@ -260,7 +262,11 @@ __device__ __forceinline__ uint64_t dpp64(uint64_t v) {
     return (uint64_t)dpp<CTRL>((uint32_t)(v >> 32)) << 32 | dpp<CTRL>((uint32_t)v);
 }
 
-// Clears the keys of the experts outside the best groups.
+// Clears the keys of the experts outside the best groups. Groups that are no power of two of
+// whole lanes take one maximum over the wave after another, and no binary32 keys: 8192 tokens, us,
+// sigmoids and a bias, 4 of 8 groups by two experts each, top-6: 96 experts 18.9, 192 26.0, 384 42.4,
+// where 256, whose groups are, take 8.2; 160 in 8, by one expert each, 19.7, as softmax
+// without a bias 12.5.
 template <int V, bool FULL>
 __device__ __forceinline__ void keep_groups(const RouteArgs& a, int lane, uint32_t hi[V], const uint32_t lo[V]) {
     const int size = a.E / a.G;
@@ -636,7 +642,10 @@ __device__ __forceinline__ int sequence_past(const int32_t* off, int S, int t) {
 // Tile b (a.tile tokens) by sequence q: a piece of its own at place b + q of the
 // partial sums. The pieces of a batch run from (0, 0) up in b or in q, never both,
 // so places are distinct. A wave has 2 tokens in flight (4 where 16 waves' sums do not fit
-// into LDS); their shares are added in binary32, and those sums in binary64. 16 waves, 8, 4
+// into LDS); their shares are added in binary32, and those sums in binary64 over the piece. A
+// wave's sum is rounded to binary32, which halves its LDS, and so are the waves' sums added: shares
+// are positive, so that is off by at most kWaves units 2^-24 of the sum, however long the
+// piece. Pieces are added in binary64. 16 waves, 8, 4
 // for the 32 tokens of a turn: the batch of 8192 x 256 takes 12.2, 12.8, 15.1 us.
 template <int V>
 constexpr int kBalanceWaves = V <= 8 ? 16 : 8;
@@ -915,7 +924,7 @@ __global__ __launch_bounds__(64 * kRouteWaves) void k_route_backward(RouteBackwa
                     d += (float)n[v] * s[v];
                     q += u[v] * s[v];
                 }
-                d = 1.0f / (wave_sum(d) + 1e-20f);
+                d = 1.0f / (wave_sum(d) + 1e-20f);  // one quotient; its products are off by a unit more
                 q = wave_sum(q) * d;
 #pragma unroll
                 for (int v = 0; v < V; ++v) u[v] = n[v] > 0 ? a.scale * ((u[v] - (float)n[v] * q) * d) : 0.0f;
