@@ -1,7 +1,6 @@
 """The router on the GPU where its formulas are hardest to keep: the lowest finite
 logits beside NaN, sigmoids that underflow, scores that are equal where their logits are not,
-logits past 2^31. References and bounds are
-test_router_gpu.py's."""
+logits past 2^31, the largest sizes. References and bounds are test_router_gpu.py's."""
 import numpy as np
 import pytest
 import torch
@@ -201,3 +200,59 @@ def test_rows_past_2_31_logits(E, f32):
     few = ops.route_backward(r, some, few_idx, few_w, counts, coef, loss, off - (T - last))
     grad = ops.route_backward(r, logits, idx, w, counts, coef, loss, off, grad_logits=logits)
     assert torch.equal(grad[-last:], few) and few.any()
+
+
+# ---------------------------------------------------------------- the largest sizes
+
+def test_the_most_tokens():
+    """2^25 tokens: slices of them as in a call of their own, the loss against torch in 64 bits."""
+    T, E, k = 1 << 25, 8, 2
+    logits = make_logits(gen(25), T, E, False)
+    r = ops.Router(E, k, ops.SCORE_SIGMOID, renormalize=True)
+    idx, w = ops.route(r, logits)
+    loss, counts, coef = ops.balance_loss(r, logits, idx)
+    assert torch.equal(counts[0].long(), torch.bincount(idx.flatten(), minlength=E))
+    assert abs(coef.item() - E / (k * float(T) ** 2)) <= 2 * U * coef.item()
+    total = torch.zeros(E, dtype=torch.float64, device="cuda")
+    for part in logits.split(1 << 22):
+        s = torch.sigmoid(part.double())
+        total += (s / s.sum(1, keepdim=True)).sum(0)
+    want = (E / (k * float(T) ** 2) * (counts[0].double() * total).sum()).item()
+    spread = 2.0 * float(logits.abs().max())  # at least the distances within a token
+    assert abs(loss.item() - want) <= (2 * (spread + float(logits.abs().max())) + 60) * U * want
+    grad = ops.route_backward(r, logits, idx, w, counts, coef, loss)
+    for first in (0, T // 2 - 7, T - 300):
+        some = logits[first:first + 300].clone()
+        few_idx, few_w = check_route(r, some)
+        assert torch.equal(idx[first:first + 300], few_idx) and torch.equal(w[first:first + 300], few_w)
+        assert torch.equal(grad[first:first + 300], ops.route_backward(r, some, few_idx, few_w, counts, coef, loss))
+    with pytest.raises(RuntimeError, match="num_tokens"):
+        ops.route(r, torch.empty((T + 1, E), dtype=torch.bfloat16, device="cuda"))
+
+
+def test_the_most_sequences_and_experts():
+    """2^17 sequences, most of them empty, of 1024 experts."""
+    T, E, k, S = 5000, 1024, 2, 1 << 17
+    g = gen(17)
+    logits, idx = make_logits(g, T, E, True), torch.randint(0, E, (T, k), generator=g, device="cuda")
+    off = torch.sort(torch.randint(0, T + 1, (S + 1,), generator=g, device="cuda").int())[0]
+    r = ops.Router(E, k)
+    loss, counts, coef = ops.balance_loss(r, logits, idx, off)
+    q = torch.searchsorted(off[1:].long(), torch.arange(T, device="cuda"), right=True)
+    inside = (q < S) & (torch.arange(T, device="cuda") >= off[0])
+    q = q.clamp(max=S - 1)
+    want_counts = torch.zeros((S, E), dtype=torch.int32, device="cuda")
+    want_counts.index_put_((q[inside].repeat_interleave(k), idx[inside].flatten()), torch.ones((), dtype=torch.int32, device="cuda"),
+                           accumulate=True)
+    assert torch.equal(counts, want_counts)
+    n = torch.bincount(q[inside], minlength=S).double()
+    want_coef = torch.where(n > 0, E / (k * n.clamp(min=1).square() * (n > 0).sum()), 0.0)
+    assert ((coef.double() - want_coef).abs() <= 2 * U * want_coef).all()
+    p = torch.softmax(logits.double(), 1)
+    want = (want_coef[q] * (p * want_counts[q].double()).sum(1))[inside].sum().item()
+    assert abs(loss.item() - want) <= (2 * ref.spread(logits) + 60) * U * want
+    grad = ops.route_backward(r, logits, idx, None, counts, coef, torch.ones((), device="cuda"), off)
+    c = want_counts[q].double() * (want_coef[q] * inside)[:, None]
+    want = p * (c - (p * c).sum(1, keepdim=True))
+    size = p * (c + (p * c).sum(1, keepdim=True))
+    assert ((grad.double() - want).abs() <= (8 * ref.spread(logits) + 240) * U * size + U * want.abs() + 1e-37).all()
