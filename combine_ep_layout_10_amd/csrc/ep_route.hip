@@ -924,10 +924,20 @@ __global__ __launch_bounds__(64 * kRouteWaves) void k_route_backward(RouteBackwa
                     d += (float)n[v] * s[v];
                     q += u[v] * s[v];
                 }
-                d = 1.0f / (wave_sum(d) + 1e-20f);  // one quotient; its products are off by a unit more
+                const float named = wave_sum(d), sum = named + 1e-20f;
+                d = 1.0f / sum;  // one quotient; its products are off by a unit more
                 q = wave_sum(q) * d;
+                // An expert that is named alone has a share that only 1e-20 keeps from 1. The difference
+                // below would be what rounding leaves of it: the share's rest times g instead.
+                const int alone = (int)lane_value((uint32_t)id, __builtin_ctzll(ballot64(id >= 0)));
+                if (ballot64(id >= 0 && id != alone) == 0) {
+                    const float rest = sum == named ? 0.0f : 1e-20f * d;
 #pragma unroll
-                for (int v = 0; v < V; ++v) u[v] = n[v] > 0 ? a.scale * ((u[v] - (float)n[v] * q) * d) : 0.0f;
+                    for (int v = 0; v < V; ++v) u[v] = n[v] > 0 ? a.scale * (u[v] * rest * d) : 0.0f;
+                } else {
+#pragma unroll
+                    for (int v = 0; v < V; ++v) u[v] = n[v] > 0 ? a.scale * ((u[v] - (float)n[v] * q) * d) : 0.0f;
+                }
             } else {
 #pragma unroll
                 for (int v = 0; v < V; ++v) u[v] *= a.scale;

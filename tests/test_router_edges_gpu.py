@@ -256,3 +256,41 @@ def test_the_most_sequences_and_experts():
     want = p * (c - (p * c).sum(1, keepdim=True))
     size = p * (c + (p * c).sum(1, keepdim=True))
     assert ((grad.double() - want).abs() <= (8 * ref.spread(logits) + 240) * U * size + U * want.abs() + 1e-37).all()
+
+
+# ---------------------------------------------------------------- one expert alone
+
+@pytest.mark.parametrize("f32", [True, False])
+@pytest.mark.parametrize("sigmoid", [0, 1])
+@pytest.mark.parametrize("E", [1, 16, 60, 256, 700])
+def test_a_renormalised_weight_alone_has_no_gradient(E, sigmoid, f32):
+    """Where all of a token's ids name one expert, its renormalised weights are shares of 1 that nothing changes, as long
+    as their sum takes up 1e-20 in binary32: gradients are 0 exactly, not what rounding leaves of them."""
+    g, T = gen(E), 200
+    logits = make_logits(g, T, E, f32)
+    one = torch.randint(0, E, (T, 1), generator=g, device="cuda")
+    for k in (1, 2, 4):
+        if k > E:
+            continue
+        idx = one.repeat(1, k)
+        if k > 1:
+            idx[::3, 1:] = -1          # one pair of several
+            idx[1::3, :k // 2] = E + 3
+        r = ops.Router(E, k, sigmoid, renormalize=True, scale=-1.5)
+        grad = ops.route_backward(r, logits, idx, torch.randn((T, k), generator=g, device="cuda"))
+        assert not grad.any()
+
+
+@pytest.mark.parametrize("level", [-38.0, -44.0, -46.0, -48.0, -60.0, -80.0])
+def test_a_renormalised_faint_weight_alone(level):
+    """The same where 1e-20 counts: s / (s + 1e-20) has the slope 1e-20 / (s + 1e-20)^2 times the sigmoid's."""
+    T, E = 100, 40
+    g = gen(int(-level))
+    logits = level + make_logits(g, T, E, True)
+    idx = torch.randint(0, E, (T, 1), generator=g, device="cuda")
+    grad_w = torch.randn((T, 1), generator=g, device="cuda")
+    got = ops.route_backward(ops.Router(E, 1, 1, renormalize=True, scale=2.5), logits, idx, grad_w).double()
+    s = torch.sigmoid(logits.double()).gather(1, idx)
+    want = torch.zeros((T, E), dtype=torch.float64, device="cuda")
+    want.scatter_(1, idx, 2.5 * grad_w.double() * s * (1 - s) * 1e-20 / (s + 1e-20).square())
+    assert ((got - want).abs() <= (8 * 30 + 240) * U * want.abs()).all()
