@@ -243,7 +243,7 @@ __global__ __launch_bounds__(64 * kWaves) void k_grouped_gemm_fp4_stream(Fp4Args
 // What is sent has 2 S - 2 intervals to land. S is 2, and 3 for tiles of up to 64 rows, which
 // wait for the weights (1,024 rows on 64 experts, 4096 x 7168: 177 us, with two steps 193).
 //
-// 65,536 rows on 32 experts, 4096 x 7168: 0.98 ms settled (0.96 to 0.99 from card to card, 3.9
+// 65,536 rows on 32 experts, 4096 x 7168: 0.98 ms settled (0.96 to 1.01 from card to card, 3.9
 // PFLOP/s), without WORDS 1.34. MFMAs are
 // 55 % busy, at the 1.6 to 1.7 GHz that power leaves; without the DMA it is 0.78 ms, with MFMAs,
 // barriers and stores alone 0.73.

@@ -11,9 +11,9 @@
 // compared one after the other: the higher one decides unless two experts share it.
 //
 // Bound by instructions, and for few tokens by the launches. 8192 tokens x 256 experts in
-// binary32, settled times of single launches, us: choice (sigmoid, bias, 4 of 8 groups) 9.2, loss
-// 5.7 and 5.4 (two launches), gradient of both 7.7; 128 tokens: choice 4.3. Calls on end
-// overlap a little, 8.9, 10.8, 7.3 and 4.0, and other times in these comments are of those. The
+// binary32, settled times of single launches, us: choice (sigmoid, bias, 4 of 8 groups) 9.3, loss
+// 5.7 and 5.5 (two launches), gradient of both 7.8; 128 tokens: choice 4.5. Calls on end
+// overlap a little, 8.9, 10.8, 7.4 and 4.0, and other times in these comments are of those. The
 // logits alone take 1.4 us to read (6.1 TB/s).
 #include <type_traits>
 
